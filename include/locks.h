@@ -295,6 +295,218 @@ int locks_select_noalloc(const locks_cfg_t* cfg, const void* q, const void* summ
                          int32_t budget_tokens, int32_t* selected, float* page_lse,
                          float* page_share, int32_t* status, void* stream);
 
+/* ===========================================================================
+ * The quantised cache: rotary positions, writing and reading a paged KV cache
+ * in 8 or 4 bits, and decode attention over it.
+ *
+ * The conventions above hold (device pointers, no allocation, no
+ * synchronisation, status bits).  The calls take their own configuration:
+ * supported are head_dim = 128; page_size 64, 32 or 16; any G from 1 to 16;
+ * max_pages < 2^24; num_blocks * n_kv_heads < 2^31; batch * n_kv_heads < 2^24.
+ * =========================================================================== */
+
+/* element type of a quantised cache */
+#define LOCKS_KV_F8 0   /* e4m3 codes, one scale per token and KV head              */
+#define LOCKS_KV_I8 1   /* 8-bit integers, one scale per token and KV head          */
+#define LOCKS_KV_I4 2   /* 4-bit integers, e4m3 scales of 32 dims, a scale per token */
+
+typedef struct locks_kv_cfg {
+  int32_t batch;          /* sequences (rows of block_table, >= 0)                     */
+  int32_t n_q_heads;      /* query heads H_q                                           */
+  int32_t n_kv_heads;     /* KV heads H_kv; H_q % H_kv == 0                            */
+  int32_t head_dim;       /* d                                                         */
+  int32_t page_size;      /* B, tokens per page                                        */
+  int32_t max_pages;      /* row stride of block_table (pages per sequence, at most)  */
+  int32_t num_blocks;     /* physical blocks in the pools                              */
+  int32_t kv_dtype;       /* LOCKS_KV_F8, LOCKS_KV_I8 or LOCKS_KV_I4                   */
+} locks_kv_cfg_t;
+
+/*
+ * Cache record: one per (physical block, KV head) in each of the K and the V
+ * pool, at byte (block * n_kv_heads + h) * locks_kv_record_bytes(cfg).  With
+ * B = page_size:
+ *
+ *   uint8_t codes[B][R]        R = 128 (F8, I8) or 64 (I4)
+ *   uint8_t group[B][4]        I4 only: e4m3 scale of dims 32j .. 32j + 31
+ *   float   scale[B]           scale of the token's row
+ *
+ * The 16-byte chunk c of row r is stored at byte r R + 16 (c ^ x(r)), with
+ * x(r) = r & 7 for R = 128 and (r >> 1) & 3 for R = 64 (the order in which the
+ * attention reads rows from shared memory without bank conflicts).  Before
+ * that permutation byte i of a row is the code of dim i (F8: e4m3 bits; I8:
+ * code + 128) or, in I4, of dims 2i (low nibble) and 2i + 1 (high nibble),
+ * code + 8.  A dim stands for
+ *
+ *   F8, I8:  code * scale         I4:  code * group[dim / 32] * scale
+ *
+ * A row x is quantised in float32, every operation rounded to nearest even:
+ *   scale = max|x| * (1 / t), t = 448 (F8), 127 (I8), 7 * 448 (I4);
+ *   y = x * (1 / scale);  F8: code = e4m3(y);  I8: code = rint(y);
+ *   I4: group = e4m3(max|y| over the group * (1 / 7)),
+ *       code = rint(y * (1 / group)) within -7 .. 7 (0 where group is 0).
+ * A row whose largest magnitude is below 2^-96 is stored as zeros with scale
+ * 0; a row that holds an infinity or a NaN is stored with scale NaN, reads
+ * back as NaN and makes the attention over it NaN.
+ */
+size_t locks_kv_record_bytes(const locks_kv_cfg_t* cfg);
+
+/* rotary layouts: which elements of a head form the pair i < rotary_dim / 2 */
+#define LOCKS_ROPE_HALF        0   /* (i, i + rotary_dim / 2) */
+#define LOCKS_ROPE_INTERLEAVED 1   /* (2 i, 2 i + 1)          */
+
+/* rotary frequency scalings */
+#define LOCKS_ROPE_SCALE_NONE   0
+#define LOCKS_ROPE_SCALE_LINEAR 1  /* w / factor                                          */
+#define LOCKS_ROPE_SCALE_NTK    2  /* base theta * factor^(r / (r - 2)), r = rotary_dim   */
+#define LOCKS_ROPE_SCALE_LLAMA3 3  /* by wavelength bands of the original context         */
+#define LOCKS_ROPE_SCALE_YARN   4  /* ramp between two dims, and a factor on cos and sin   */
+
+typedef struct locks_rope_spec {
+  int32_t rotary_dim;         /* even, 2 .. 512                                          */
+  int32_t scaling;            /* LOCKS_ROPE_SCALE_*                                      */
+  double theta;               /* base, > 1                                               */
+  double factor;              /* context extension, >= 1 (not read by SCALE_NONE)         */
+  double low_freq_factor;     /* LLAMA3                                                  */
+  double high_freq_factor;    /* LLAMA3, > low_freq_factor                               */
+  double original_positions;  /* LLAMA3, YARN: original context, > 0                     */
+  double beta_fast;           /* YARN: turns in the original context (usually 32)        */
+  double beta_slow;           /* YARN (usually 1)                                        */
+} locks_rope_spec_t;
+
+/*
+ * locks_rope_frequencies -- the rotation rate of each pair, on the HOST.
+ *
+ * w_i = theta^(-2 i / rotary_dim) radians per position, scaled by the spec:
+ *   LINEAR  w / factor
+ *   NTK     theta' = theta * factor^(rotary_dim / (rotary_dim - 2))
+ *   LLAMA3  wavelength 2 pi / w above original / low_freq_factor: w / factor;
+ *           below original / high_freq_factor: w; between: interpolated by
+ *           (original / wavelength - low) / (high - low)
+ *   YARN    w / factor * z + w * (1 - z), z = clamp((i - a) / (b - a), 0, 1),
+ *           a = floor(D(beta_fast)), b = ceil(D(beta_slow)), clamped to
+ *           [0, rotary_dim - 1], D(t) = rotary_dim ln(original / (2 pi t)) /
+ *           (2 ln theta); mscale = 0.1 ln(factor) + 1
+ * turns[i] = w_i / (2 pi) as a 64-bit binary fraction of a turn: the kernels
+ * multiply it by the position modulo 2^64, so that the angle of any position
+ * is exact to 2^-32 of a turn.
+ *
+ *   turns    HOST uint64 [rotary_dim / 2]: written
+ *   mscale   HOST float: written, the factor on cos and sin (1 but for YARN)
+ */
+int locks_rope_frequencies(const locks_rope_spec_t* spec, uint64_t* turns, float* mscale);
+
+/* a rotary table as the kernels take it */
+typedef struct locks_rope_table {
+  const uint64_t* turns;      /* DEVICE uint64 [rotary_dim / 2]                          */
+  int32_t rotary_dim;         /* leading dims of a head that are rotated                 */
+  int32_t layout;             /* LOCKS_ROPE_HALF or LOCKS_ROPE_INTERLEAVED               */
+  float mscale;               /* factor on cos and sin                                   */
+} locks_rope_table_t;
+
+/* element types of locks_rope */
+#define LOCKS_BF16 0
+#define LOCKS_F16  1
+#define LOCKS_F32  2
+
+/*
+ * locks_rope -- rotary positions: the pair (u, v) of a head at position p
+ * becomes (u c - v s, v c + u s) with c, s = mscale * cos, sin(p w_i); dims
+ * from rotary_dim on are copied.  `inverse` != 0 rotates by -p: the transposed
+ * map, which is the gradient of the forward call with respect to x.  Computed
+ * in float32, rounded once.
+ *
+ *   head_dim          even, 2 .. 512; rope->rotary_dim <= head_dim
+ *   x, out            [n_tokens][n_heads][head_dim] of dtype, strides in
+ *                     elements between tokens and between heads (the last dim
+ *                     is contiguous); out may be x with the same strides, and
+ *                     may not overlap it otherwise
+ *   positions         int32 [n_tokens], any values
+ */
+int locks_rope(const locks_rope_table_t* rope, int32_t dtype, int32_t head_dim, const void* x,
+               int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+               int32_t n_tokens, int32_t n_heads, void* out, int64_t out_token_stride,
+               int64_t out_head_stride, int32_t inverse, void* stream);
+
+/*
+ * locks_kv_write -- tokens (of a prompt, a chunk of one, or a decode step)
+ * into a quantised cache, with the rotation of their queries and keys.
+ *
+ * Token i belongs to sequence token_seq[i] (i itself when token_seq is NULL)
+ * at position token_pos[i]; its key rows, rotated by `rope`, and its value
+ * rows go, quantised, to slot pos % B of block
+ * block_table[seq * max_pages + pos / B] of the pools.  Keys are quantised
+ * from the float32 rotation, without a rounding to bf16 in between.  Its query
+ * rows, rotated and rounded to bf16, go to q_out.
+ *
+ *   k_new, v_new  bf16 rows: element e of head h of token i is at
+ *                 i * stride + h * d + e; 16-byte aligned, strides multiples
+ *                 of 8 elements (slices of one projection's output will do)
+ *   q_new, q_out  nullable (both or neither); q_new as k_new, q_out bf16
+ *                 [n_tokens][n_q_heads][d]; q_out may be q_new
+ *   token_seq     nullable int32 [n_tokens]; a token with an entry < 0 is
+ *                 padding: nothing of it is written
+ *   token_pos     int32 [n_tokens]; no two tokens of a call may share a slot
+ *   rope          nullable: no rotation; rotary_dim a multiple of 16, <= d
+ *   seq_lens      nullable int32 [batch]: raised to at least pos + 1 (may not
+ *                 be the array passed as token_pos)
+ *   completed     nullable int32 [n_tokens]: the block whose last slot the
+ *                 token took, else -1
+ *   status        nullable int32[1]
+ * A position outside [0, max_pages * B) (LOCKS_DEV_BAD_SEQ_LEN), a sequence
+ * >= batch (LOCKS_DEV_BAD_PAGE_ID) or an invalid block (LOCKS_DEV_BAD_BLOCK_ID)
+ * leaves the cache and seq_lens as they are, with completed -1; the query is
+ * rotated all the same.
+ */
+int locks_kv_write(const locks_kv_cfg_t* cfg, const void* k_new, int64_t k_stride,
+                   const void* v_new, int64_t v_stride, const void* q_new, int64_t q_stride,
+                   void* q_out, const int32_t* token_seq, const int32_t* token_pos,
+                   int32_t n_tokens, const locks_rope_table_t* rope, void* k_pool, void* v_pool,
+                   const int32_t* block_table, int32_t* seq_lens, int32_t* completed,
+                   int32_t* status, void* stream);
+
+/*
+ * locks_kv_read -- listed blocks of a quantised cache as bf16 pages, in the
+ * layout of a bf16 pool of n_blocks blocks (locks_build_summaries reads it as
+ * it stands).  Entries < 0 are skipped; an entry >= num_blocks is skipped with
+ * LOCKS_DEV_BAD_BLOCK_ID.  Slots that were never written read as whatever
+ * their bytes stand for.
+ *
+ *   block_ids     int32 [n_blocks]
+ *   k_out, v_out  bf16 [n_blocks][n_kv_heads][B][d], 16-byte aligned; each
+ *                 nullable (not both): only the other pool is read
+ */
+int locks_kv_read(const locks_kv_cfg_t* cfg, const void* k_pool, const void* v_pool,
+                  const int32_t* block_ids, int32_t n_blocks, void* k_out, void* v_out,
+                  int32_t* status, void* stream);
+
+/* Bytes of workspace locks_kv_decode needs for this cfg. */
+size_t locks_kv_decode_workspace_bytes(const locks_kv_cfg_t* cfg);
+
+/*
+ * locks_kv_decode -- attention of one new token per sequence over a quantised
+ * cache: out = sum_t p_t v_t, p = softmax(q^T k_t / sqrt(d)) over the attended
+ * tokens: those of every page or of the listed pages, and with window > 0 only
+ * the last `window` positions.  The codes are read once, and scales multiply
+ * logits and weights.
+ *
+ *   q             bf16 [batch][n_q_heads][d], 16-byte aligned
+ *   seq_lens      int32 [batch], the new token included; a length of 0 gives
+ *                 out = 0 and out_lse = -inf
+ *   selected, k   nullable int32 [batch][n_kv_heads][k] logical page ids, each
+ *                 at most once (as locks_select writes them); entries < 0 are
+ *                 skipped.  NULL: every page (k is not read)
+ *   window        0: no window
+ *   out           bf16 [batch][n_q_heads][d], 16-byte aligned
+ *   out_lse       nullable float [batch][n_q_heads]: natural-log log-sum-exp
+ *   workspace     >= locks_kv_decode_workspace_bytes(cfg) bytes, 16-byte
+ *                 aligned, zero-filled before its first use
+ *   status        nullable int32[1]
+ */
+int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool,
+                    const void* v_pool, const int32_t* block_table, const int32_t* seq_lens,
+                    const int32_t* selected, int32_t k, int32_t window, void* out, float* out_lse,
+                    void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* Static string for a LOCKS_* return code. */
 const char* locks_status_string(int code);
 

@@ -34,6 +34,22 @@ LOCKS_SUMMARY_F32 = 0
 LOCKS_SUMMARY_BF16 = 1
 LOCKS_SUMMARY_I4 = 2
 
+LOCKS_KV_F8 = 0
+LOCKS_KV_I8 = 1
+LOCKS_KV_I4 = 2
+
+LOCKS_ROPE_HALF = 0
+LOCKS_ROPE_INTERLEAVED = 1
+LOCKS_ROPE_SCALE_NONE = 0
+LOCKS_ROPE_SCALE_LINEAR = 1
+LOCKS_ROPE_SCALE_NTK = 2
+LOCKS_ROPE_SCALE_LLAMA3 = 3
+LOCKS_ROPE_SCALE_YARN = 4
+
+LOCKS_BF16 = 0
+LOCKS_F16 = 1
+LOCKS_F32 = 2
+
 
 class LocksLibraryMissing(RuntimeError):
     pass
@@ -87,9 +103,56 @@ class LocksConfig:
                            summary_dtype=summary_dtype)
 
 
+class locks_kv_cfg_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "max_pages", "num_blocks",
+        "kv_dtype")]
+
+
+class locks_rope_spec_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "low_freq_factor", "high_freq_factor",
+                                       "original_positions", "beta_fast", "beta_slow")]
+
+
+class locks_rope_table_t(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+@dataclass(frozen=True)
+class LocksKvConfig:
+    """Shapes of a quantised paged cache (locks_kv_cfg_t)."""
+    batch: int
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int
+    page_size: int
+    max_pages: int
+    num_blocks: int
+    kv_dtype: int = LOCKS_KV_F8
+
+    def __post_init__(self):
+        # the C structure and its reference, made once: a decode step passes them at every call
+        c = locks_kv_cfg_t(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim,
+                           self.page_size, self.max_pages, self.num_blocks, self.kv_dtype)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "ref", ctypes.byref(c))
+
+    def c(self) -> locks_kv_cfg_t:
+        return self._c
+
+    @property
+    def group(self) -> int:
+        return self.n_q_heads // self.n_kv_heads
+
+
 _lib = None
 
 _P = ctypes.c_void_p
+_I, _L, _Z = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_KV = ctypes.POINTER(locks_kv_cfg_t)
+_ROPE = ctypes.POINTER(locks_rope_table_t)
 _SIGS = {
     "locks_summary_record_bytes": (ctypes.c_size_t, [ctypes.POINTER(locks_cfg_t)]),
     "locks_summary_bytes": (ctypes.c_size_t, [ctypes.POINTER(locks_cfg_t)]),
@@ -109,6 +172,16 @@ _SIGS = {
                                        _P]),
     "locks_build_completed": (ctypes.c_int, [ctypes.POINTER(locks_cfg_t), _P, _P, ctypes.c_int32,
                                              _P, _P, _P, ctypes.c_int32, _P]),
+    "locks_kv_record_bytes": (_Z, [_KV]),
+    "locks_kv_decode_workspace_bytes": (_Z, [_KV]),
+    "locks_rope_frequencies": (ctypes.c_int, [ctypes.POINTER(locks_rope_spec_t), _P,
+                                              ctypes.POINTER(ctypes.c_float)]),
+    "locks_rope": (ctypes.c_int, [_ROPE, _I, _I, _P, _L, _L, _P, _I, _I, _P, _L, _L, _I, _P]),
+    "locks_kv_write": (ctypes.c_int, [_KV, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _ROPE, _P, _P,
+                                      _P, _P, _P, _P, _P]),
+    "locks_kv_read": (ctypes.c_int, [_KV, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "locks_kv_decode": (ctypes.c_int, [_KV, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P,
+                                       _P]),
     "locks_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "locks_abi_version": (ctypes.c_int, []),
 }
@@ -248,6 +321,146 @@ def locks_dense_decode(cfg: LocksConfig, q, k_cache, v_cache, block_table, seq_l
         _ptr(seq_lens), _ptr(out), _ptr(out_lse), _ptr(workspace), int(wsb), _ptr(status),
         _stream(stream))
     _check("locks_dense_decode", rc)
+
+
+# --------------------------------------------------------------------------
+# the quantised cache (C names)
+# --------------------------------------------------------------------------
+def kv_record_bytes(cfg: LocksKvConfig) -> int:
+    return int(load_library().locks_kv_record_bytes(cfg.ref))
+
+
+def kv_decode_workspace_bytes(cfg: LocksKvConfig) -> int:
+    return int(load_library().locks_kv_decode_workspace_bytes(cfg.ref))
+
+
+def rope_frequencies(spec: locks_rope_spec_t) -> Tuple:
+    """(turns as a list of ints, mscale) of a rotary specification (host only)."""
+    turns = (ctypes.c_uint64 * max(1, min(256, spec.rotary_dim // 2)))()
+    mscale = ctypes.c_float()
+    rc = load_library().locks_rope_frequencies(ctypes.byref(spec), turns, ctypes.byref(mscale))
+    _check("locks_rope_frequencies", rc)
+    return list(turns), mscale.value
+
+
+def _typed(x, dtype: str, what: str):
+    """x, if it is a tensor (or None, or a raw pointer) of the dtype of that name."""
+    if x is not None and not isinstance(x, int):
+        import torch
+        if x.dtype is not getattr(torch, dtype):
+            raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
+    return x
+
+
+def _sized(x, dtype: str, shape: Tuple, what: str) -> Optional[int]:
+    """Pointer of a contiguous device tensor of that type and shape; None stays None."""
+    _typed(x, dtype, what)
+    if x is not None and not isinstance(x, int) and tuple(x.shape) != shape:
+        raise ValueError(f"{what}: shape {shape} expected, got {tuple(x.shape)}")
+    return _ptr(x)
+
+
+def _pool(x, cfg: LocksKvConfig, what: str) -> Optional[int]:
+    """Pointer of a pool tensor, if it holds the records of every block of cfg."""
+    if x is not None and not isinstance(x, int):
+        need = cfg.num_blocks * cfg.n_kv_heads * kv_record_bytes(cfg)
+        if x.numel() * x.element_size() < need:
+            raise ValueError(f"{what}: {need} bytes expected, got {x.numel() * x.element_size()}")
+    return _ptr(x)
+
+
+def _rows(x, heads: int, dim: int, what: str) -> Tuple[int, int]:
+    """(pointer, elements between tokens) of bf16 rows [tokens][heads][dim] whose heads are
+    contiguous; the token stride is free (a slice of a projection's output)."""
+    _typed(x, "bfloat16", what)
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{what}: [tokens][{heads}][{dim}] expected, got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: device tensor expected")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"{what}: contiguous heads expected")
+    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else heads * dim)
+
+
+_ROPE_DTYPES = {"torch.bfloat16": LOCKS_BF16, "torch.float16": LOCKS_F16, "torch.float32": LOCKS_F32}
+
+
+def locks_rope(rope, x, positions, out, inverse: bool = False, stream=None) -> None:
+    """Rotary positions of x [tokens][heads][head_dim] (bf16, f16 or f32; any token and head
+    strides, also x is out) into `out`; `rope` is a runtime.RopeTable, `inverse` the gradient."""
+    dtype = _ROPE_DTYPES.get(str(x.dtype))
+    if dtype is None or out.dtype != x.dtype:
+        raise ValueError("x, out: bf16, f16 or f32 tensors of one type expected")
+    if x.dim() != 3 or out.shape != x.shape:
+        raise ValueError("x, out: [tokens][heads][head_dim] tensors of one shape expected")
+    if not (x.is_cuda and out.is_cuda):
+        raise ValueError("x, out: device tensors expected")
+    n, heads, dim = x.shape
+    if dim > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("x, out: contiguous last dimension expected")
+    rc = load_library().locks_rope(
+        rope.ref, dtype, dim, x.data_ptr(), x.stride(0), x.stride(1),
+        _sized(positions, "int32", (n,), "positions"), n, heads, out.data_ptr(), out.stride(0),
+        out.stride(1), 1 if inverse else 0, _stream(stream))
+    _check("locks_rope", rc)
+
+
+def locks_kv_write(cfg: LocksKvConfig, k_new, v_new, token_pos, k_pool, v_pool, block_table,
+                   token_seq=None, rope=None, q=None, q_out=None, seq_lens=None, completed=None,
+                   status=None, stream=None) -> None:
+    """Tokens into the quantised pools, keys (and queries q, into q_out) rotated by `rope`
+    (runtime.RopeTable, None: no rotation).  k_new, v_new: bf16 [tokens][H_kv][d], q: bf16
+    [tokens][H_q][d], token strides free."""
+    n = k_new.shape[0]
+    if v_new.shape[0] != n or (q is not None and q.shape[0] != n):
+        raise ValueError("k_new, v_new, q: as many tokens expected in each")
+    d = cfg.head_dim
+    kp, ks = _rows(k_new, cfg.n_kv_heads, d, "k_new")
+    vp, vs = _rows(v_new, cfg.n_kv_heads, d, "v_new")
+    qp, qs = (None, 0) if q is None else _rows(q, cfg.n_q_heads, d, "q")
+    rc = load_library().locks_kv_write(
+        cfg.ref, kp, ks, vp, vs, qp, qs, _sized(q_out, "bfloat16", (n, cfg.n_q_heads, d), "q_out"),
+        _sized(token_seq, "int32", (n,), "token_seq"), _sized(token_pos, "int32", (n,), "token_pos"),
+        n, None if rope is None else rope.ref, _pool(k_pool, cfg, "k_pool"),
+        _pool(v_pool, cfg, "v_pool"),
+        _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
+        _sized(seq_lens, "int32", (cfg.batch,), "seq_lens"),
+        _sized(completed, "int32", (n,), "completed"), _ptr(_typed(status, "int32", "status")),
+        _stream(stream))
+    _check("locks_kv_write", rc)
+
+
+def locks_kv_read(cfg: LocksKvConfig, k_pool, v_pool, block_ids, k_out, v_out, status=None,
+                  stream=None) -> None:
+    """Listed blocks as bf16 pages [blocks][H_kv][page_size][d] (k_out or v_out may be None)."""
+    n = block_ids.numel()
+    shape = (n, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
+    rc = load_library().locks_kv_read(
+        cfg.ref, _pool(k_pool, cfg, "k_pool"), _pool(v_pool, cfg, "v_pool"),
+        _sized(block_ids, "int32", (n,), "block_ids"), n,
+        _sized(k_out, "bfloat16", shape, "k_out"), _sized(v_out, "bfloat16", shape, "v_out"),
+        _ptr(_typed(status, "int32", "status")), _stream(stream))
+    _check("locks_kv_read", rc)
+
+
+def locks_kv_decode(cfg: LocksKvConfig, q, k_pool, v_pool, block_table, seq_lens, out, workspace,
+                    selected=None, window: int = 0, out_lse=None, status=None,
+                    workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """Attention of one new token per sequence over the quantised pools: every page, or the
+    pages listed in `selected` (int32 [batch][H_kv][k]), and with `window` the last positions."""
+    wsb = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    rows = (cfg.batch, cfg.n_q_heads, cfg.head_dim)
+    k = 0 if selected is None else selected.shape[-1]
+    rc = load_library().locks_kv_decode(
+        cfg.ref, _sized(q, "bfloat16", rows, "q"), _pool(k_pool, cfg, "k_pool"),
+        _pool(v_pool, cfg, "v_pool"),
+        _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
+        _sized(seq_lens, "int32", (cfg.batch,), "seq_lens"),
+        _sized(selected, "int32", (cfg.batch, cfg.n_kv_heads, k), "selected"), k, int(window),
+        _sized(out, "bfloat16", rows, "out"),
+        _sized(out_lse, "float32", (cfg.batch, cfg.n_q_heads), "out_lse"), _ptr(workspace),
+        int(wsb), _ptr(_typed(status, "int32", "status")), _stream(stream))
+    _check("locks_kv_decode", rc)
 
 
 # --------------------------------------------------------------------------

@@ -25,6 +25,37 @@ def complete_page_blocks(block_table: np.ndarray, seq_lens: np.ndarray, page_siz
     return np.concatenate(out).astype(np.int32) if out else np.zeros(0, np.int32)
 
 
+class RopeTable:
+    """Rotary frequencies of one model, on the device: the rates of the pairs as fractions of a
+    turn per position, the layout of the pairs and the factor on cos and sin.  `scaling` is
+    "none", "linear", "ntk", "llama3" or "yarn" (see locks_rope_frequencies)."""
+
+    LAYOUTS = {"half": B.LOCKS_ROPE_HALF, "interleaved": B.LOCKS_ROPE_INTERLEAVED}
+    SCALINGS = {"none": B.LOCKS_ROPE_SCALE_NONE, "linear": B.LOCKS_ROPE_SCALE_LINEAR,
+                "ntk": B.LOCKS_ROPE_SCALE_NTK, "llama3": B.LOCKS_ROPE_SCALE_LLAMA3,
+                "yarn": B.LOCKS_ROPE_SCALE_YARN}
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, low_freq_factor: float = 1.0,
+                 high_freq_factor: float = 4.0, original_positions: float = 8192.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, device: str = "cuda"):
+        import ctypes
+
+        import torch
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise ValueError(f"layout one of {sorted(self.LAYOUTS)}, scaling one of "
+                             f"{sorted(self.SCALINGS)} expected")
+        spec = B.locks_rope_spec_t(rotary_dim, self.SCALINGS[scaling], theta, factor,
+                                   low_freq_factor, high_freq_factor, original_positions,
+                                   beta_fast, beta_slow)
+        turns, self.mscale = B.rope_frequencies(spec)
+        self.rotary_dim, self.layout = rotary_dim, layout
+        self.turns = torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(device)
+        self._c = B.locks_rope_table_t(self.turns.data_ptr(), rotary_dim, self.LAYOUTS[layout],
+                                       self.mscale)
+        self.ref = ctypes.byref(self._c)
+
+
 class LocksLayer:
     def __init__(self, cfg: B.LocksConfig, budget_tokens: int, device: str = "cuda"):
         import torch
