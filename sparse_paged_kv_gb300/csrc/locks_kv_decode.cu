@@ -20,8 +20,8 @@
 //
 // Block.  Warp 8 is a producer: it looks up 32 pages at a time (one a lane) and
 // copies each page's K and V records (cp.async.bulk, one contiguous piece each)
-// into a ring of 64-token stages.  Consumer warps 0-7 take 16 tokens of every
-// other stage and keep everything in registers:
+// into a ring of 64-token stages.  Consumer warps 0-7 take 16-token chunks of
+// the stages in turn and keep everything in registers:
 //   S^T (16 tokens x 8 heads)  = K (16 x 128) . Q^T      8 mma m16n8k16
 //   O^T (128 dims x 8 heads)  += V^T (128 x 16) . P^T    8 mma m16n8k16
 // Tokens and dims are the long sides of the products, so the short one, the
@@ -36,11 +36,12 @@ namespace locks {
 namespace {
 
 constexpr int kKvWarps = 8;                       // consumer warps
+constexpr int kMergeWarps = 4;                    // warps whose states the merge buffer holds
 constexpr int kKvConsumers = kKvWarps * 32;
 constexpr int kKvThreads = kKvConsumers + 32;
 constexpr int kStageTok = 64;
 constexpr float kNone = -3.402823466e38f;         // running maximum before any token
-constexpr int kKvMergeBytes = kKvWarps * 4096;    // a warp's 8 heads x 128 floats
+constexpr int kKvMergeBytes = kMergeWarps * 4096; // a warp's 8 heads x 128 floats
 
 // Blocks: two per SM (one for more than 8 heads, whose accumulators fill the registers).
 constexpr int kSms = 152;
@@ -50,12 +51,18 @@ __host__ __device__ constexpr size_t kv_part_bytes(int nt) { return size_t(nt) *
 __host__ __device__ constexpr int kv_stage_bytes(int fmt) {
   return 2 * kStageTok * (kv_row_bytes(fmt) + (fmt == LOCKS_KV_I4 ? 8 : 4));
 }
-// stages of the ring: what two blocks per SM (one for NT = 2) leave beside the merge buffer
+// Stages of the ring: what half an SM's shared memory (all of it for NT = 2)
+// holds beside the merge buffer.  The number has to make 4 stages a whole number
+// of rounds of the warps: a warp then comes back to a ring slot at every use of
+// it, as waiting by the barrier's parity requires (copies land out of order, so
+// having seen a later stage full says nothing about a slot's earlier use).
 constexpr int kv_stages(int fmt, int nt) {
-  const int budget = (nt == 1 ? 115712 : 232448) - kKvMergeBytes - 4096;
-  const int n = budget / kv_stage_bytes(fmt);
-  return n > 16 ? 16 : n;
+  return nt == 1 ? (fmt == LOCKS_KV_I4 ? 10 : 4) : (fmt == LOCKS_KV_I4 ? 16 : 10);
 }
+constexpr bool kv_rounds(int fmt, int nt) { return 4 * kv_stages(fmt, nt) % kKvWarps == 0; }
+static_assert(kv_rounds(LOCKS_KV_F8, 1) && kv_rounds(LOCKS_KV_I4, 1) && kv_rounds(LOCKS_KV_F8, 2) &&
+                  kv_rounds(LOCKS_KV_I4, 2),
+              "every warp must see every use of the ring slots it visits");
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -95,14 +102,38 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds128(const unsigned char* p) {
-  return *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
 }
-__device__ __forceinline__ float lds_f(const unsigned char* p) {
-  return *reinterpret_cast<const float*>(p);
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
 }
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kKvConsumers) : "memory");
+}
+
+// (a & b) | c as one instruction: left to itself the compiler makes two of it
+// when both b and c are constants (int4, 4 x 128K: 166 -> 154 us)
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
 }
 
 // 4-bit codes: nibbles n and n + 4 of a word as f16x2 of c * s, exact.  A nibble
@@ -122,10 +153,10 @@ __device__ __forceinline__ I4Scale i4_scale(uint32_t s) {
 }
 __device__ __forceinline__ void i4_pairs(uint32_t w, const I4Scale& s, uint32_t (&x)[4]) {
   const uint32_t v = w >> 8;
-  x[0] = hfma2((w & 0x000f000fu) | 0x64006400u, s.s, s.off);
-  x[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, s.s16, s.off16);
-  x[2] = hfma2((v & 0x000f000fu) | 0x64006400u, s.s, s.off);
-  x[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, s.s16, s.off16);
+  x[0] = hfma2(and_or(w, 0x000f000fu, 0x64006400u), s.s, s.off);
+  x[1] = hfma2(and_or(w, 0x00f000f0u, 0x64006400u), s.s16, s.off16);
+  x[2] = hfma2(and_or(v, 0x000f000fu, 0x64006400u), s.s, s.off);
+  x[3] = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), s.s16, s.off16);
 }
 // two 8-bit codes in bytes (0, 1) or (2, 3) of w -> f16x2, exact
 template <int FMT, int HI>
@@ -144,26 +175,51 @@ struct State {
   float m[2 * NT];       // reference of the exponent (log2), within 8 of the running maximum
   float l[2 * NT];       // this lane's part of sum 2^(z - m)
   float f[2 * NT];       // factor that brings the weights to f16: largest seen -> 2^7 .. 2^15
-  float lim[2 * NT];     // weights above it need a new factor
   float acc[NT][8][4];   // O^T, times f
 };
 
-// One warp's 16 tokens: records k, v (rows r0 ..), valid rows [lo, hi) of them.
+// Where a lane finds its part of 16 tokens: shared-memory byte offsets from the
+// tokens' codes, or from their scales, in a stage (V's records are half a stage
+// further on).  Rows 8 apart share a permutation, so the other addresses are
+// these plus constants, or with bit 4 flipped (the neighbouring chunk).
+struct LaneOff {
+  uint32_t k;            // K: row g, first chunk
+  uint32_t v;            // V: row 2t, this lane's dims
+  uint32_t scale;        // scale of row g
+  uint32_t gk, gv;       // I4: group scales of K's row g and of V's row 2t
+};
+template <int FMT>
+__device__ __forceinline__ LaneOff lane_off(int B, int g, int t) {
+  constexpr uint32_t kV = kv_stage_bytes(FMT) / 2;
+  LaneOff o;
+  o.k = kv_chunk_off<FMT>(g, FMT == LOCKS_KV_I4 ? t : 2 * t);
+  o.v = kV + (FMT == LOCKS_KV_I4 ? kv_chunk_off<FMT>(2 * t, g >> 1) + 8 * (g & 1)
+                                 : kv_chunk_off<FMT>(2 * t, g));
+  o.scale = kv_scale_off(FMT, B) + 4 * g;
+  o.gk = kv_group_off(FMT, B) + 4 * g + t;
+  o.gv = kV + kv_group_off(FMT, B) + 8 * t + (g >> 1);
+  return o;
+}
+
+// 16 tokens of a stage, whose codes and scales are at shared-memory addresses
+// `base` and `sbase` (plus LaneOff), of which rows [lo, hi) are attended.
 template <int FMT, int NT>
-__device__ __forceinline__ void attend16(const unsigned char* k, const unsigned char* v, int B,
-                                         int r0, int lo, int hi, int g, int t,
-                                         const uint32_t (&qb)[NT][8][2], const float (&qs)[2 * NT],
-                                         State<NT>& st) {
+__device__ __forceinline__ void attend16(uint32_t base, uint32_t sbase, const LaneOff& off,
+                                         int range, int g, int t, uint32_t qa,
+                                         const float (&qs)[2 * NT], State<NT>& st) {
+  constexpr uint32_t kV = kv_stage_bytes(FMT) / 2;
+  constexpr uint32_t kRow = kv_row_bytes(FMT);
+  const bool whole = range == (16 << 8);
   // ---- S^T = K Q^T ----
-  float sa[NT][4], sb[NT][4];
+  float sa[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
-  const int ra = r0 + g, rb = r0 + g + 8;
+    for (int e = 0; e < 4; ++e) sa[n][e] = 0.f;
+  const uint32_t ka = base + off.k;
   if constexpr (FMT == LOCKS_KV_I4) {
-    const uint4 A = lds128(k + kv_chunk_off<FMT>(ra, t)), C = lds128(k + kv_chunk_off<FMT>(rb, t));
-    const uint32_t ga = k[kv_group_off(FMT, B) + 4 * ra + t], gb = k[kv_group_off(FMT, B) + 4 * rb + t];
+    const uint4 A = lds128(ka), C = lds128(ka + 8 * kRow);
+    const uint32_t ga = lds_u8(sbase + off.gk), gb = lds_u8(sbase + off.gk + 32);
     const I4Scale s0 = i4_scale(e4m3x2_to_f16x2(ga | (ga << 8)));
     const I4Scale s1 = i4_scale(e4m3x2_to_f16x2(gb | (gb << 8)));
     const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, cw[4] = {C.x, C.y, C.z, C.w};
@@ -174,72 +230,103 @@ __device__ __forceinline__ void attend16(const unsigned char* k, const unsigned 
       i4_pairs(cw[w], s1, y);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma_f16(sa[n], x[0], y[0], x[1], y[1], qb[n][2 * w][0], qb[n][2 * w][1]);
-        mma_f16(sb[n], x[2], y[2], x[3], y[3], qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+        const uint4 q = lds128(qa + (n * 4 + w) * 512);
+        mma_f16(sa[n], x[0], y[0], x[1], y[1], q.x, q.y);
+        mma_f16(sa[n], x[2], y[2], x[3], y[3], q.z, q.w);
       }
     }
   } else {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const uint4 A = lds128(k + kv_chunk_off<FMT>(ra, 2 * t + c));
-      const uint4 C = lds128(k + kv_chunk_off<FMT>(rb, 2 * t + c));
+      const uint32_t kc = ka ^ (16 * c);
+      const uint4 A = lds128(kc), C = lds128(kc + 8 * kRow);
       const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, cw[4] = {C.x, C.y, C.z, C.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < 4; w += 2) {
         const uint32_t a0 = pair8<FMT, 0>(aw[w]), a2 = pair8<FMT, 1>(aw[w]);
         const uint32_t a1 = pair8<FMT, 0>(cw[w]), a3 = pair8<FMT, 1>(cw[w]);
+        const uint32_t b0 = pair8<FMT, 0>(aw[w + 1]), b2 = pair8<FMT, 1>(aw[w + 1]);
+        const uint32_t b1 = pair8<FMT, 0>(cw[w + 1]), b3 = pair8<FMT, 1>(cw[w + 1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma_f16((w & 1) ? sb[n] : sa[n], a0, a1, a2, a3, qb[n][4 * c + w][0], qb[n][4 * c + w][1]);
+        for (int n = 0; n < NT; ++n) {
+          const uint4 q = lds128(qa + (n * 4 + 2 * c + w / 2) * 512);
+          mma_f16(sa[n], a0, a1, a2, a3, q.x, q.y);
+          mma_f16(sa[n], b0, b1, b2, b3, q.z, q.w);
+        }
       }
     }
   }
-  // ---- logits in log2 units, masked; weights ----
-  const bool on0 = g >= lo && g < hi, on1 = g + 8 >= lo && g + 8 < hi;
-  const float ks0 = lds_f(k + kv_scale_off(FMT, B) + 4 * ra), ks1 = lds_f(k + kv_scale_off(FMT, B) + 4 * rb);
-  const float vs0 = on0 ? lds_f(v + kv_scale_off(FMT, B) + 4 * ra) : 0.f;
-  const float vs1 = on1 ? lds_f(v + kv_scale_off(FMT, B) + 4 * rb) : 0.f;
-  float z0[2 * NT], z1[2 * NT], p0[2 * NT], p1[2 * NT];
-  bool over = false;
+  // ---- weights: y = logit (log2 units) - m, p = 2^y, w = p v_scale f ----
+  float ks0 = lds_f(sbase + off.scale), ks1 = lds_f(sbase + off.scale + 32);
+  float vs0 = lds_f(sbase + off.scale + kV), vs1 = lds_f(sbase + off.scale + kV + 32);
+  float y[2 * NT][2], p[2 * NT][2], w[2 * NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int j = 2 * n + e;
-      z0[j] = on0 ? (sa[n][e] + sb[n][e]) * qs[j] * ks0 : -INFINITY;
-      z1[j] = on1 ? (sa[n][2 + e] + sb[n][2 + e]) * qs[j] * ks1 : -INFINITY;
-      p0[j] = ex2_approx(z0[j] - st.m[j]);
-      p1[j] = ex2_approx(z1[j] - st.m[j]);
-      over |= fmaxf(z0[j], z1[j]) > st.m[j] + 8.f ||
-              fmaxf(fabsf(p0[j] * vs0), fabsf(p1[j] * vs1)) > st.lim[j];
+      y[j][0] = fmaf(sa[n][e], qs[j] * ks0, -st.m[j]);
+      y[j][1] = fmaf(sa[n][2 + e], qs[j] * ks1, -st.m[j]);
     }
-  // The reference moves only when a logit passes it by 2^8 or a weight leaves
-  // f16's range: a few times per sequence, so most chunks do no rescaling.
-  if (__any_sync(kFull, over)) {
+  if (!whole) {
+    // rows outside the attended range may hold anything: no value of theirs is used
+    const int lo = range & 255, hi = range >> 8;
+    const bool on0 = g >= lo && g < hi, on1 = g + 8 >= lo && g + 8 < hi;
+    if (!on0) vs0 = 0.f;
+    if (!on1) vs1 = 0.f;
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-      float mx = fmaxf(z0[j], z1[j]);
+      if (!on0) y[j][0] = -INFINITY;
+      if (!on1) y[j][1] = -INFINITY;
+    }
+  }
+  float pmax = 0.f, wmax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) {
+    p[j][0] = ex2_approx(y[j][0]);
+    p[j][1] = ex2_approx(y[j][1]);
+    w[j][0] = p[j][0] * vs0 * st.f[j];
+    w[j][1] = p[j][1] * vs1 * st.f[j];
+    pmax = fmaxf(pmax, fmaxf(p[j][0], p[j][1]));
+    wmax = fmaxf(wmax, fmaxf(fabsf(w[j][0]), fabsf(w[j][1])));
+  }
+  // The references move only when a logit passes its reference by 2^8 or a
+  // weight leaves f16's range: a few times per sequence, so most chunks do no
+  // rescaling.  (Before the first token m is the lowest float and p infinite.)
+  if (__any_sync(kFull, pmax > 256.f || wmax > 32768.f)) {
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {
+      float up_m = fmaxf(0.f, fmaxf(y[j][0], y[j][1]));
+      // y is relative to m; before the first token it is logit + FLT_MAX, whose
+      // logit is lost to rounding: take the logits themselves there
+      const bool fresh = st.m[j] == kNone;
+      const int n = j >> 1, e = j & 1;
+      const float z0 = y[j][0] == -INFINITY ? -INFINITY : sa[n][e] * (qs[j] * ks0);
+      const float z1 = y[j][1] == -INFINITY ? -INFINITY : sa[n][2 + e] * (qs[j] * ks1);
+      float mx = fresh ? fmaxf(z0, z1) : st.m[j] + up_m;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-      mx = fmaxf(st.m[j], mx);
+      mx = fmaxf(mx, kNone);                       // (no token of this head yet)
       const float alpha = ex2_approx(st.m[j] - mx);
       st.m[j] = mx;
       st.l[j] *= alpha;
-      p0[j] = ex2_approx(z0[j] - mx);
-      p1[j] = ex2_approx(z1[j] - mx);
-      float xm = fmaxf(fabsf(p0[j] * vs0), fabsf(p1[j] * vs1));
+      p[j][0] = ex2_approx(z0 - mx);
+      p[j][1] = ex2_approx(z1 - mx);
+      float xm = fmaxf(fabsf(p[j][0] * vs0), fabsf(p[j][1] * vs1));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
       const float f = st.f[j];
       xm = fmaxf(xm, f > 0.f ? alpha * 128.f / f : 0.f);
-      const float fn = xm > 0.f ? fminf(128.f / xm, 1.2676506e30f) : 0.f;
+      // (weights that are all zero so far leave the largest factor: any that is not will move it)
+      const float fn = fminf(128.f / xm, 1.2676506e30f);
       const float up = f > 0.f ? alpha * (fn / f) : 0.f;
       st.f[j] = fn;
-      st.lim[j] = fn > 0.f ? 32768.f / fn : 0.f;
+      w[j][0] = p[j][0] * vs0 * fn;
+      w[j][1] = p[j][1] * vs1 * fn;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        st.acc[j >> 1][i][j & 1] *= up;
-        st.acc[j >> 1][i][2 + (j & 1)] *= up;
+        st.acc[n][i][e] *= up;
+        st.acc[n][i][2 + e] *= up;
       }
     }
   }
@@ -248,62 +335,68 @@ __device__ __forceinline__ void attend16(const unsigned char* k, const unsigned 
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int j = 2 * n;
-    st.l[j] += p0[j] + p1[j];
-    st.l[j + 1] += p0[j + 1] + p1[j + 1];
-    pb[n][0] = transpose8x8(f16x2(p0[j] * vs0 * st.f[j], p0[j + 1] * vs0 * st.f[j + 1]));
-    pb[n][1] = transpose8x8(f16x2(p1[j] * vs1 * st.f[j], p1[j + 1] * vs1 * st.f[j + 1]));
+    st.l[j] += p[j][0] + p[j][1];
+    st.l[j + 1] += p[j + 1][0] + p[j + 1][1];
+    pb[n][0] = transpose8x8(f16x2(w[j][0], w[j + 1][0]));
+    pb[n][1] = transpose8x8(f16x2(w[j][1], w[j + 1][1]));
   }
   // ---- O^T += V^T P^T: this lane's tokens 2t, 2t+1, 2t+8, 2t+9, dims 16g .. 16g+15 ----
-  const int tok[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-  const bool whole = lo == 0 && hi == 16;
+  const uint32_t va = base + off.v;
+  constexpr int kTok[4] = {0, 1, 8, 9};            // beyond 2t
   if constexpr (FMT == LOCKS_KV_I4) {
     uint2 T[4];
     uint32_t gs[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = r0 + tok[i];
-      T[i] = *reinterpret_cast<const uint2*>(v + kv_chunk_off<FMT>(r, g >> 1) + 8 * (g & 1));
-      gs[i] = v[kv_group_off(FMT, B) + 4 * r + (g >> 1)];
-      // a row outside the sequence may hold NaN scales: 0 x NaN must not enter the sum
-      if (!whole && (tok[i] < lo || tok[i] >= hi)) gs[i] = 0;
+      T[i] = lds64(va + kTok[i] * kRow);
+      gs[i] = lds_u8(sbase + off.gv + 4 * kTok[i]);
+    }
+    if (!whole) {                                  // 0 x NaN must not enter the sum
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (2 * t + kTok[i] < (range & 255) || 2 * t + kTok[i] >= (range >> 8)) gs[i] = 0;
     }
     const I4Scale s01 = i4_scale(e4m3x2_to_f16x2(gs[0] | (gs[1] << 8)));
     const I4Scale s23 = i4_scale(e4m3x2_to_f16x2(gs[2] | (gs[3] << 8)));
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {       // dims 4w .. 4w + 3: half a word of each token
-      const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
-      const uint32_t a = prmt(w < 2 ? T[0].x : T[0].y, w < 2 ? T[1].x : T[1].y, sel);
-      const uint32_t c = prmt(w < 2 ? T[2].x : T[2].y, w < 2 ? T[3].x : T[3].y, sel);
-      uint32_t x[4], y[4];
+    for (int q = 0; q < 4; ++q) {       // dims 4q .. 4q + 3: half a word of each token
+      const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
+      const uint32_t a = prmt(q < 2 ? T[0].x : T[0].y, q < 2 ? T[1].x : T[1].y, sel);
+      const uint32_t c = prmt(q < 2 ? T[2].x : T[2].y, q < 2 ? T[3].x : T[3].y, sel);
+      uint32_t x[4], z[4];
       i4_pairs(a, s01, x);
-      i4_pairs(c, s23, y);
+      i4_pairs(c, s23, z);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma_f16(st.acc[n][2 * w], x[0], x[1], y[0], y[1], pb[n][0], pb[n][1]);
-        mma_f16(st.acc[n][2 * w + 1], x[2], x[3], y[2], y[3], pb[n][0], pb[n][1]);
+        mma_f16(st.acc[n][2 * q], x[0], x[1], z[0], z[1], pb[n][0], pb[n][1]);
+        mma_f16(st.acc[n][2 * q + 1], x[2], x[3], z[2], z[3], pb[n][0], pb[n][1]);
       }
     }
   } else {
     uint4 T[4];
+    T[0] = lds128(va);
+    T[1] = lds128((va ^ 16) + kRow);               // odd rows: the neighbouring chunk place
+    T[2] = lds128(va + 8 * kRow);
+    T[3] = lds128((va ^ 16) + 9 * kRow);
+    if (FMT == LOCKS_KV_F8 && !whole) {            // e4m3 NaN codes
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      T[i] = lds128(v + kv_chunk_off<FMT>(r0 + tok[i], g));
-      // a row outside the sequence may hold e4m3 NaN codes
-      if (FMT == LOCKS_KV_F8 && !whole && (tok[i] < lo || tok[i] >= hi)) T[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        if (2 * t + kTok[i] < (range & 255) || 2 * t + kTok[i] >= (range >> 8))
+          T[i] = make_uint4(0, 0, 0, 0);
     }
     const uint32_t T0[4] = {T[0].x, T[0].y, T[0].z, T[0].w}, T1[4] = {T[1].x, T[1].y, T[1].z, T[1].w};
     const uint32_t T2[4] = {T[2].x, T[2].y, T[2].z, T[2].w}, T3[4] = {T[3].x, T[3].y, T[3].z, T[3].w};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int q = 0; q < 4; ++q) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {     // dims 4w + 2e, 4w + 2e + 1
+      for (int e = 0; e < 2; ++e) {     // dims 4q + 2e, 4q + 2e + 1
         const uint32_t sel = e ? 0x7362u : 0x5140u;
-        const uint32_t x = prmt(T0[w], T1[w], sel), y = prmt(T2[w], T3[w], sel);
+        const uint32_t x = prmt(T0[q], T1[q], sel), z = prmt(T2[q], T3[q], sel);
         const uint32_t a0 = pair8<FMT, 0>(x), a1 = pair8<FMT, 1>(x);
-        const uint32_t a2 = pair8<FMT, 0>(y), a3 = pair8<FMT, 1>(y);
+        const uint32_t a2 = pair8<FMT, 0>(z), a3 = pair8<FMT, 1>(z);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          mma_f16(st.acc[n][2 * w + e], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          mma_f16(st.acc[n][2 * q + e], a0, a1, a2, a3, pb[n][0], pb[n][1]);
       }
     }
   }
@@ -329,6 +422,26 @@ __device__ __forceinline__ Seq seq_of(const KvDecodeParams& p, int b) {
   return s;
 }
 
+// A warp's state for heads 8n .. 8n + 7 into shared memory: float4 x of a lane
+// is head parity x / 4, dims 4 (x % 4) .. + 3 of its 16.
+template <int NT>
+__device__ __forceinline__ void put_state(const State<NT>& st, int n, float4* to, float* m, float* l,
+                                          int g, int t) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int i = 2 * (x & 3), e = x >> 2;
+    to[x * 32] = make_float4(st.acc[n][i][e], st.acc[n][i][2 + e], st.acc[n][i + 1][e],
+                             st.acc[n][i + 1][2 + e]);
+  }
+  if (g == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[8 * n + 2 * t + e] = st.m[2 * n + e];
+      l[8 * n + 2 * t + e] = st.l[2 * n + e];
+    }
+  }
+}
+
 template <int FMT, int NT>
 __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(const KvDecodeParams p) {
   constexpr int STAGES = kv_stages(FMT, NT);
@@ -337,10 +450,12 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   unsigned char* ring = smem;
   float4* mbuf = reinterpret_cast<float4*>(smem + STAGES * kStageBytes);    // [warp][8][32]
   __shared__ uint64_t s_full[STAGES], s_empty[STAGES];
+  __shared__ uint2 s_chunk[4];                    // a chunk's codes and scales in a stage
   __shared__ int s_range[STAGES][4];              // valid rows of each 16-token chunk: lo | hi << 8
+  __shared__ uint4 s_q[NT][4][32];                // query operands of the k-steps
+  __shared__ float s_qs[8 * NT];                  // what brings their products to log2 units
   __shared__ float s_m[kKvWarps][8 * NT], s_l[kKvWarps][8 * NT];
-  __shared__ long long s_scan[kKvThreads / 32], s_base;
-  __shared__ int s_first, s_last;
+  __shared__ int s_scan[kKvThreads / 32], s_base, s_first, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.page_size, pps = kStageTok / B, hk = p.n_kv_heads;
@@ -357,35 +472,35 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   // ---- this block's share of the stages of all units ----
   const int per = (p.batch + kKvThreads - 1) / kKvThreads;
   const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
-  long long mine = 0;
+  int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     mine += seq_of(p, b).stages;
     if (blockIdx.x == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.max_pages * B))
       flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
   }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(kFull, incl, o);
+    const int x = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += x;
   }
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kKvThreads / 32; ++w) {
     if (w == warp) incl += total;
     total += s_scan[w];
   }
-  const long long W = total * hk;
-  const int N = int(min((long long)gridDim.x, max(W, 1ll)));
-  const long long w_lo = int(blockIdx.x) < N ? W * blockIdx.x / N : 0;
-  const long long w_hi = int(blockIdx.x) < N ? W * (blockIdx.x + 1) / N : 0;
+  const int W = total * hk;                       // below 2^31: the host has checked
+  const int N = min(int(gridDim.x), max(W, 1));
+  const int w_lo = int(blockIdx.x) < N ? int(int64_t(W) * blockIdx.x / N) : 0;
+  const int w_hi = int(blockIdx.x) < N ? int(int64_t(W) * (blockIdx.x + 1) / N) : 0;
   if (w_lo < w_hi && (incl - mine) * hk <= w_lo && w_lo < incl * hk) {
-    long long at = (incl - mine) * hk;
+    int at = (incl - mine) * hk;
     for (int b = b_lo; b < b_hi; ++b) {
-      const long long n = (long long)seq_of(p, b).stages * hk;
-      if (w_lo < at + n) {
+      const int n = seq_of(p, b).stages * hk;
+      if (w_lo - at < n) {
         s_first = b;
         s_base = at;
         break;
@@ -408,18 +523,22 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   const size_t rec = size_t(kv_rec_bytes(FMT, B));
   int b = s_first;
   Seq sq = seq_of(p, b);
-  long long base = s_base;                        // first stage of sequence b in the list
-  int h = int((w_lo - base) / sq.stages);
-  int i0 = int((w_lo - base) % sq.stages);
-  long long left = w_hi - w_lo;
+  int base = s_base;                              // first stage of sequence b in the list
+  int h = (w_lo - base) / sq.stages;
+  int i0 = (w_lo - base) % sq.stages;
+  int left = w_hi - w_lo;
   int it = 0;                                     // stages of this block so far
+  if (tid < 4) {                                  // (one barrier before its first use is below)
+    const int e = 16 * tid / B, r0 = 16 * tid - e * B;
+    s_chunk[tid] = make_uint2(e * uint32_t(rec) + r0 * kv_row_bytes(FMT), e * uint32_t(rec) + 4 * r0);
+  }
 
   if (warp == kKvWarps) {
     // ---------------- producer ----------------
     const uint64_t pol = l2_evict_first();
     bool ok = true;
     while (left > 0 && ok) {
-      const int cnt = int(min((long long)(sq.stages - i0), left));
+      const int cnt = min(sq.stages - i0, left);
       const int32_t* row = p.block_table + size_t(b) * p.max_pages;
       const int32_t* sel = p.selected ? p.selected + (size_t(b) * hk + h) * p.k : nullptr;
       const int pages = (sq.n + B - 1) / B;
@@ -483,7 +602,7 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
       if (++h == hk && left > 0) {
         h = 0;
         do {
-          base += (long long)sq.stages * hk;
+          base += sq.stages * hk;
           sq = seq_of(p, ++b);
         } while (sq.stages == 0);
       }
@@ -493,26 +612,29 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
 
   // ---------------- consumers ----------------
   const int g = lane >> 2, t = lane & 3, G = p.group;
-  const int half = warp >> 2, chunk = warp & 3;   // stages of this parity, this 16-token chunk
+  const LaneOff off = lane_off<FMT>(B, g, t);
+  const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(s_q) + 16 * lane;
   bool ok = true;
-  float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
-  int* tickets = reinterpret_cast<int*>(p.ws);
+  // 16-token chunks go round the warps: chunk `job` of this block, in ring slot s
+  int job = warp, s = warp >> 2, phase = 0;
+  while (s >= STAGES) {
+    s -= STAGES;
+    phase ^= 1;
+  }
   while (left > 0) {
-    const int cnt = int(min((long long)(sq.stages - i0), left));
-    const size_t unit = size_t(b) * hk + h;
-    // ---- the query: head 8n + g, dims 32t .. 32t + 31, brought to a largest magnitude in
-    // [2^14, 2^15) by a power of two and rounded to f16 (exact but for elements 2^-28 of it) ----
-    uint32_t qb[NT][8][2];
-    float qs[2 * NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int head = 8 * n + g;
+    const int cnt = min(sq.stages - i0, left);
+    const int unit = b * hk + h;
+    // ---- the query, by warp n for heads 8n + g, dims 32t .. 32t + 31: brought to a largest
+    // magnitude in [2^14, 2^15) by a power of two, rounded to f16 (exact but for elements below
+    // 2^-28 of it) and laid out as the second operand of the eight k-steps ----
+    if (warp < NT) {
+      const int head = 8 * warp + g;
       float x[32];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (head < G)
-          w = *reinterpret_cast<const uint4*>(p.q + (unit * G + head) * kHeadDim + 32 * t + 8 * i);
+          w = *reinterpret_cast<const uint4*>(p.q + (size_t(unit) * G + head) * kHeadDim + 32 * t + 8 * i);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -529,31 +651,31 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
       // factor 2^(14 - (ex - 127)), at most 2^126; an infinity keeps its value
       const int up = ex == 255 ? 0 : min(126, 141 - ex);
       const float factor = __uint_as_float(uint32_t(127 + up) << 23);
-      const float back = __uint_as_float(uint32_t(127 - up) << 23);
+      constexpr float kScale = 0.08838834764831845f * kLog2e * (FMT == LOCKS_KV_I4 ? 256.f : 1.f);
+      if (t == 0) s_qs[head] = __uint_as_float(uint32_t(127 - up) << 23) * kScale;
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] *= factor;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        if constexpr (FMT == LOCKS_KV_I4) {
-          // word ks / 2, nibbles (n, n + 4) with n = 0, 1 or 2, 3
-          const int d = 8 * (ks >> 1) + 2 * (ks & 1);
-          qb[n][ks][0] = f16x2(x[d], x[d + 4]);
-          qb[n][ks][1] = f16x2(x[d + 1], x[d + 5]);
-        } else {
-          const int d = 4 * ks;
-          qb[n][ks][0] = f16x2(x[d], x[d + 1]);
-          qb[n][ks][1] = f16x2(x[d + 2], x[d + 3]);
-        }
+      for (int w = 0; w < 4; ++w) {                           // k-steps 2w, 2w + 1
+        const int d = 8 * w;
+        // 4 bits: nibbles (n, n + 4) of word w; 8 bits: bytes (0, 1), (2, 3) of words 2w, 2w + 1
+        s_q[warp][w][lane] =
+            FMT == LOCKS_KV_I4
+                ? make_uint4(f16x2(x[d], x[d + 4]), f16x2(x[d + 1], x[d + 5]),
+                             f16x2(x[d + 2], x[d + 6]), f16x2(x[d + 3], x[d + 7]))
+                : make_uint4(f16x2(x[d], x[d + 1]), f16x2(x[d + 2], x[d + 3]),
+                             f16x2(x[d + 4], x[d + 5]), f16x2(x[d + 6], x[d + 7]));
       }
-      constexpr float kScale = 0.08838834764831845f * kLog2e * (FMT == LOCKS_KV_I4 ? 256.f : 1.f);
-      qs[2 * n] = __shfl_sync(kFull, back, 8 * t) * kScale;       // heads 8n + 2t, 8n + 2t + 1
-      qs[2 * n + 1] = __shfl_sync(kFull, back, 8 * t + 4) * kScale;
     }
+    consumers_sync();
+    float qs[2 * NT];
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) qs[j] = s_qs[8 * (j >> 1) + 2 * t + (j & 1)];
     State<NT> st;
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
       st.m[j] = kNone;
-      st.l[j] = st.f[j] = st.lim[j] = 0.f;
+      st.l[j] = st.f[j] = 0.f;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -562,63 +684,89 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.acc[n][i][e] = 0.f;
 
-    for (const int end = it + cnt; it < end; ++it) {
-      if ((it & 1) != half) continue;
-      const int s = it % STAGES;
-      if (ok && !__all_sync(kFull, mbar_wait_bounded(s_full + s, (it / STAGES) & 1))) {
+    it += cnt;
+    for (; (job >> 2) < it; job += kKvWarps) {
+      const int c = job & 3;
+      if (ok && !__all_sync(kFull, mbar_wait_bounded(s_full + s, phase))) {
         if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
         ok = false;                               // the rest counts as empty: tickets stay right
       }
-      if (!ok) continue;
-      const int range = s_range[s][chunk];
-      if ((range >> 8) > (range & 255)) {
-        const int tok0 = chunk * 16, e = tok0 / B;
-        const unsigned char* k = ring + s * kStageBytes + e * rec;
-        attend16<FMT, NT>(k, k + kStageBytes / 2, B, tok0 - e * B, range & 255, range >> 8, g, t, qb,
-                          qs, st);
+      if (ok) {
+        const int range = s_range[s][c];
+        const uint2 at = s_chunk[c];
+        if ((range >> 8) > (range & 255))
+          attend16<FMT, NT>(ring_at + s * kStageBytes + at.x, ring_at + s * kStageBytes + at.y, off,
+                            range, g, t, q_at, qs, st);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + s);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_empty + s);
+      s += ((job + kKvWarps) >> 2) - (job >> 2);
+      if (s >= STAGES) {
+        s -= STAGES;
+        phase ^= 1;
+      }
     }
 
     // ---- merge the warps' states; finish the unit or leave a partial ----
-    const long long u_lo = base + (long long)h * sq.stages, u_hi = u_lo + sq.stages;
-    const int c_lo = int(((u_lo + 1) * N - 1) / W), c_hi = int((u_hi * N - 1) / W);
+    const int u_lo = base + h * sq.stages, u_hi = u_lo + sq.stages;
+    const int c_lo = int((int64_t(u_lo + 1) * N - 1) / W), c_hi = int((int64_t(u_hi) * N - 1) / W);
     const bool alone = c_lo == c_hi;
     const int slot = int(blockIdx.x) == c_lo ? 1 : 0;
+    float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
+    int* tickets = reinterpret_cast<int*>(p.ws);
     float* part = parts + (size_t(blockIdx.x) * 2 + slot) * (kv_part_bytes(NT) / 4);
+    // a warp's state from here on: m, l over its tokens, acc = sum p v (this lane's dims)
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-      float l = st.l[j];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
-      if (g == 0) {
-        s_m[warp][8 * (j >> 1) + 2 * t + (j & 1)] = st.m[j];
-        s_l[warp][8 * (j >> 1) + 2 * t + (j & 1)] = l;
+      for (int o = 4; o < 32; o <<= 1) st.l[j] += __shfl_xor_sync(kFull, st.l[j], o);
+      const float f = st.f[j] > 0.f ? (FMT == LOCKS_KV_I4 ? 256.f : 1.f) / st.f[j] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        st.acc[j >> 1][i][j & 1] *= f;
+        st.acc[j >> 1][i][2 + (j & 1)] *= f;
       }
     }
     // item of this thread: head parity and 4 dims of a lane's 16
-    const int q4 = warp, odd = q4 >> 2, dq = q4 & 3;
+    const int odd = warp >> 2, dq = warp & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      // warps from kMergeWarps on hand their states to the first ones ...
+      float4* mine = mbuf + (warp % kMergeWarps) * 256 + lane;
+      if (warp >= kMergeWarps) put_state<NT>(st, n, mine, s_m[warp], s_l[warp], g, t);
+      consumers_sync();
+      if (warp + kMergeWarps < kKvWarps) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int j = 2 * n + (x >> 2), i = 2 * (x & 3), e = x >> 2;
-        const float f = st.f[j] > 0.f ? (FMT == LOCKS_KV_I4 ? 256.f : 1.f) / st.f[j] : 0.f;
-        mbuf[(warp * 8 + x) * 32 + lane] =
-            make_float4(st.acc[n][i][e] * f, st.acc[n][i][2 + e] * f, st.acc[n][i + 1][e] * f,
-                        st.acc[n][i + 1][2 + e] * f);
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * n + e, head = 8 * n + 2 * t + e;
+          const float m2 = s_m[warp + kMergeWarps][head], M = fmaxf(st.m[j], m2);
+          const float fa = exp2f(st.m[j] - M), fb = exp2f(m2 - M);
+          st.m[j] = M;
+          st.l[j] = st.l[j] * fa + s_l[warp + kMergeWarps][head] * fb;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 o = mine[(4 * e + x) * 32];
+            float (&a0)[4] = st.acc[n][2 * x], (&a1)[4] = st.acc[n][2 * x + 1];
+            a0[e] = a0[e] * fa + o.x * fb;
+            a0[2 + e] = a0[2 + e] * fa + o.y * fb;
+            a1[e] = a1[e] * fa + o.z * fb;
+            a1[2 + e] = a1[2 + e] * fa + o.w * fb;
+          }
+        }
       }
+      consumers_sync();
+      // ... whose sums are taken item by item
+      if (warp < kMergeWarps) put_state<NT>(st, n, mine, s_m[warp], s_l[warp], g, t);
       consumers_sync();
       const int head = 8 * n + 2 * t + odd;
       float M = kNone, L = 0.f;
       float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, s_m[w][head]);
+      for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w][head]);
 #pragma unroll
-      for (int w = 0; w < kKvWarps; ++w) {
+      for (int w = 0; w < kMergeWarps; ++w) {
         const float f = exp2f(s_m[w][head] - M);
-        const float4 a = mbuf[(w * 8 + q4) * 32 + lane];
+        const float4 a = mbuf[(w * 8 + warp) * 32 + lane];
         L += s_l[w][head] * f;
         A.x += a.x * f; A.y += a.y * f; A.z += a.z * f; A.w += a.w * f;
       }
@@ -630,12 +778,12 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
           const __nv_bfloat162 o1 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
           o.x = *reinterpret_cast<const uint32_t*>(&o0);
           o.y = *reinterpret_cast<const uint32_t*>(&o1);
-          *reinterpret_cast<uint2*>(p.out + (unit * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
+          *reinterpret_cast<uint2*>(p.out + (size_t(unit) * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
           if (p.out_lse && g == 0 && dq == 0)
-            p.out_lse[unit * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
+            p.out_lse[size_t(unit) * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
         }
       } else {
-        reinterpret_cast<float4*>(part)[(n * 8 + q4) * 32 + lane] = A;
+        reinterpret_cast<float4*>(part)[(n * 8 + warp) * 32 + lane] = A;
         if (g == 0 && dq == 0)
           *reinterpret_cast<float2*>(part + NT * 1024 + 2 * head) = make_float2(M, L);
       }
@@ -663,7 +811,7 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
               if (c + i <= c_hi) {
                 const float* src = parts + (size_t(c + i) * 2 + (c + i == c_lo)) * (kv_part_bytes(NT) / 4);
                 ml[i] = __ldcg(reinterpret_cast<const float2*>(src + NT * 1024 + 2 * head));
-                a[i] = __ldcg(reinterpret_cast<const float4*>(src) + (n * 8 + q4) * 32 + lane);
+                a[i] = __ldcg(reinterpret_cast<const float4*>(src) + (n * 8 + warp) * 32 + lane);
               }
             }
             float Mn = M;
@@ -687,9 +835,9 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
             const __nv_bfloat162 o1 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
             o.x = *reinterpret_cast<const uint32_t*>(&o0);
             o.y = *reinterpret_cast<const uint32_t*>(&o1);
-            *reinterpret_cast<uint2*>(p.out + (unit * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
+            *reinterpret_cast<uint2*>(p.out + (size_t(unit) * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
             if (p.out_lse && g == 0 && dq == 0)
-              p.out_lse[unit * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
+              p.out_lse[size_t(unit) * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
           }
         }
         if (tid == 0) tickets[unit] = 0;
@@ -700,7 +848,7 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
     if (++h == hk && left > 0) {
       h = 0;
       do {
-        base += (long long)sq.stages * hk;
+        base += sq.stages * hk;
         sq = seq_of(p, ++b);
       } while (sq.stages == 0);
     }

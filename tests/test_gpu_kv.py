@@ -633,6 +633,14 @@ def test_decode_many_sequences(batch, hkv):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("hq,hkv,page", [(8, 4, 64), (12, 4, 16), (48, 3, 32)])
+@pytest.mark.parametrize("name,fmt", FMTS)
+def test_decode_long(name, fmt, hq, hkv, page):
+    """Enough tokens that every block goes round its ring of stages several times."""
+    c = Cache(fmt, page, [40000, 25001, 17], hq, hkv, seed=hq + fmt)
+    c.check(c.run())
+
+
 def test_pools_past_four_gigabytes():
     """Blocks whose byte offsets pass 32 bits: written, read back and attended."""
     import torch
