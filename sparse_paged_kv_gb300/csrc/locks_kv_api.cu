@@ -178,9 +178,9 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
   const int rc = check_kv_cfg(cfg);
   if (rc != LOCKS_OK) return rc;
   if (window < 0 || (selected && k <= 0)) return LOCKS_ERR_INVALID_ARG;
-  // the kernel counts the 64-token stages of all units in an int
+  // the kernel counts the 64-token stages of all units (and 8 more a unit) in an int
   const int64_t pages = selected ? k : cfg->max_pages;
-  if ((pages * cfg->page_size + 63) / 64 * cfg->batch * cfg->n_kv_heads >= (int64_t(1) << 31))
+  if (((pages * cfg->page_size + 63) / 64 + 8) * cfg->batch * cfg->n_kv_heads >= (int64_t(1) << 31))
     return LOCKS_ERR_UNSUPPORTED;
   if (cfg->batch == 0) return LOCKS_OK;
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || !workspace)

@@ -11,17 +11,19 @@
 // rounding); the sum of p_t that divides the result is kept in float32.
 //
 // Work split.  The 64-token stages of all (sequence, KV head) units form one
-// list; block c of N takes the c-th N-th of it, whatever the lengths of the
-// sequences, so that ragged batches load every SM alike.  A unit that lies in
-// one block is finished there; one that is cut is left as partials (running
-// maximum, sum, weighted values) in the workspace, and the last of its blocks
-// to arrive (atomic ticket) merges them in the blocks' order, so results do not
-// depend on the order of arrival.  The workspace is a few MB for any shape.
+// list, each unit preceded by its fixed cost; block c of 152 (one per SM) takes
+// the c-th part of it, whatever the lengths of the sequences, so that ragged
+// batches load every SM alike.  A unit that lies in one block is finished there;
+// one that is cut is left as partials (running maximum, sum, weighted values) in
+// the workspace, and the last of its blocks to arrive (atomic ticket) merges them
+// in the blocks' order, so results do not depend on the order of arrival.  The
+// workspace is about a megabyte for any shape.
 //
-// Block.  Warp 8 is a producer: it looks up 32 pages at a time (one a lane) and
-// copies each page's K and V records (cp.async.bulk, one contiguous piece each)
-// into a ring of 64-token stages.  Consumer warps 0-7 take 16-token chunks of
-// the stages in turn and keep everything in registers:
+// Block.  Four producer warps take the stages in turn: each looks up its next
+// pages (one a lane) and copies their K and V records (cp.async.bulk, one
+// contiguous piece each) into a ring of 64-token stages; the last of them also
+// brings the next unit's query.  Consumer warps take 16-token chunks of the
+// stages in turn and keep everything in registers:
 //   S^T (16 tokens x 8 heads)  = K (16 x 128) . Q^T      8 mma m16n8k16
 //   O^T (128 dims x 8 heads)  += V^T (128 x 16) . P^T    8 mma m16n8k16
 // Tokens and dims are the long sides of the products, so the short one, the
@@ -29,40 +31,56 @@
 // are rows as they lie in memory (the dims of a product may come in any order
 // that Q shares); V's are two tokens' bytes interleaved by a byte permute; P is
 // turned from S^T's layout into an operand by movmatrix.
+//
+// Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 310 us (7.1 TB/s), 8 x
+// 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 122 us (4.95 TB/s): instructions,
+// of which the unpacking of codes is over half.
 #include "locks_kv.cuh"
 
 namespace locks {
 
 namespace {
 
-constexpr int kKvWarps = 8;                       // consumer warps
-constexpr int kMergeWarps = 4;                    // warps whose states the merge buffer holds
-constexpr int kKvConsumers = kKvWarps * 32;
-constexpr int kKvThreads = kKvConsumers + 32;
+// One block per SM.  For up to 8 heads a group 16 consumer warps of 104
+// registers; for up to 16, whose accumulators are twice as large, 8 of 168.
+constexpr int kSms = 152;
+__host__ __device__ constexpr int kv_warps(int nt) { return nt == 1 ? 16 : 8; }
+// and four producer warps: among busy consumers a warp issues an instruction in
+// about seven cycles, and one producer could not keep up with the stages (1M e4m3:
+// 415 us)
+__host__ __device__ constexpr int kv_threads(int nt) { return kv_warps(nt) * 32 + 128; }
+constexpr int kConsumerRegs = 104, kProducerRegs = 64;
+static_assert(16 * 32 * kConsumerRegs + 128 * kProducerRegs <= 640 * 96, "registers of the launch");
 constexpr int kStageTok = 64;
 constexpr float kNone = -3.402823466e38f;         // running maximum before any token
-constexpr int kKvMergeBytes = kMergeWarps * 4096; // a warp's 8 heads x 128 floats
+// merge buffer: the warps' states of 8 heads x 128 floats
+constexpr int kv_merge_bytes(int nt) { return kv_warps(nt) * 4096; }
 
-// Blocks: two per SM (one for more than 8 heads, whose accumulators fill the registers).
-constexpr int kSms = 152;
-__host__ __device__ constexpr int kv_blocks(int nt) { return kSms * (nt == 1 ? 2 : 1); }
 __host__ __device__ constexpr size_t kv_part_bytes(int nt) { return size_t(nt) * (4096 + 64); }
 
 __host__ __device__ constexpr int kv_stage_bytes(int fmt) {
   return 2 * kStageTok * (kv_row_bytes(fmt) + (fmt == LOCKS_KV_I4 ? 8 : 4));
 }
-// Stages of the ring: what half an SM's shared memory (all of it for NT = 2)
-// holds beside the merge buffer.  The number has to make 4 stages a whole number
-// of rounds of the warps: a warp then comes back to a ring slot at every use of
-// it, as waiting by the barrier's parity requires (copies land out of order, so
-// having seen a later stage full says nothing about a slot's earlier use).
-constexpr int kv_stages(int fmt, int nt) {
-  return nt == 1 ? (fmt == LOCKS_KV_I4 ? 10 : 4) : (fmt == LOCKS_KV_I4 ? 16 : 10);
+// 16-token chunks a warp takes at a time: two in 4 bits, where instructions bind
+// (int4 4 x 128K: 144 -> 122 us); one in 8 bits, where two would hold the whole
+// ring while they are computed on (e4m3 1M: 316 -> 320 us).
+constexpr int kv_chunks(int fmt, int nt) { return nt == 1 && fmt == LOCKS_KV_I4 ? 2 : 1; }
+// Stages of the ring, beside the merge buffer.  The number has to make a ring of
+// jobs a whole number of rounds of the warps: a warp then comes back to a ring
+// slot at every use of it, as waiting by the barrier's parity requires (copies
+// land out of order, so having seen a later stage full says nothing about a
+// slot's earlier use).
+constexpr int kv_stages(int fmt) {
+  return fmt == LOCKS_KV_I4 ? 16 : 8;
 }
-constexpr bool kv_rounds(int fmt, int nt) { return 4 * kv_stages(fmt, nt) % kKvWarps == 0; }
+constexpr bool kv_rounds(int fmt, int nt) {
+  return 4 / kv_chunks(fmt, nt) * kv_stages(fmt) % kv_warps(nt) == 0;
+}
 static_assert(kv_rounds(LOCKS_KV_F8, 1) && kv_rounds(LOCKS_KV_I4, 1) && kv_rounds(LOCKS_KV_F8, 2) &&
                   kv_rounds(LOCKS_KV_I4, 2),
               "every warp must see every use of the ring slots it visits");
+static_assert(kv_stages(LOCKS_KV_F8) % 4 == 0 && kv_stages(LOCKS_KV_I4) % 4 == 0,
+              "a ring slot belongs to one producer warp");
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -124,8 +142,9 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+template <int NT>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kKvConsumers) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kv_warps(NT) * 32) : "memory");
 }
 
 // (a & b) | c as one instruction: left to itself the compiler makes two of it
@@ -201,118 +220,134 @@ __device__ __forceinline__ LaneOff lane_off(int B, int g, int t) {
   return o;
 }
 
-// 16 tokens of a stage, whose codes and scales are at shared-memory addresses
-// `base` and `sbase` (plus LaneOff), of which rows [lo, hi) are attended.
-template <int FMT, int NT>
-__device__ __forceinline__ void attend16(uint32_t base, uint32_t sbase, const LaneOff& off,
-                                         int range, int g, int t, uint32_t qa,
-                                         const float (&qs)[2 * NT], State<NT>& st) {
+// C chunks of 16 tokens of a stage, whose codes and scales are at shared-memory
+// addresses base[c] and sbase[c] (plus LaneOff), of which rows lo .. hi - 1
+// (range[c] = lo | hi << 8) are attended.
+template <int FMT, int NT, int C>
+__device__ __forceinline__ void attend(const uint32_t (&base)[C], const uint32_t (&sbase)[C],
+                                       const int (&range)[C], const LaneOff& off, int g, int t,
+                                       uint32_t qa, const float (&qs)[2 * NT], State<NT>& st) {
   constexpr uint32_t kV = kv_stage_bytes(FMT) / 2;
   constexpr uint32_t kRow = kv_row_bytes(FMT);
-  const bool whole = range == (16 << 8);
+  constexpr int kWhole = 16 << 8;
+  bool whole = true;
+#pragma unroll
+  for (int c = 0; c < C; ++c) whole = whole && range[c] == kWhole;
   // ---- S^T = K Q^T ----
-  float sa[NT][4];
+  float sa[C][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sa[n][e] = 0.f;
-  const uint32_t ka = base + off.k;
-  if constexpr (FMT == LOCKS_KV_I4) {
-    const uint4 A = lds128(ka), C = lds128(ka + 8 * kRow);
-    const uint32_t ga = lds_u8(sbase + off.gk), gb = lds_u8(sbase + off.gk + 32);
-    const I4Scale s0 = i4_scale(e4m3x2_to_f16x2(ga | (ga << 8)));
-    const I4Scale s1 = i4_scale(e4m3x2_to_f16x2(gb | (gb << 8)));
-    const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, cw[4] = {C.x, C.y, C.z, C.w};
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t x[4], y[4];
-      i4_pairs(aw[w], s0, x);
-      i4_pairs(cw[w], s1, y);
+      for (int e = 0; e < 4; ++e) sa[c][n][e] = 0.f;
+    const uint32_t ka = base[c] + off.k;
+    if constexpr (FMT == LOCKS_KV_I4) {
+      const uint4 A = lds128(ka), D = lds128(ka + 8 * kRow);
+      const uint32_t ga = lds_u8(sbase[c] + off.gk), gb = lds_u8(sbase[c] + off.gk + 32);
+      const I4Scale s0 = i4_scale(e4m3x2_to_f16x2(ga | (ga << 8)));
+      const I4Scale s1 = i4_scale(e4m3x2_to_f16x2(gb | (gb << 8)));
+      const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, dw[4] = {D.x, D.y, D.z, D.w};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 q = lds128(qa + (n * 4 + w) * 512);
-        mma_f16(sa[n], x[0], y[0], x[1], y[1], q.x, q.y);
-        mma_f16(sa[n], x[2], y[2], x[3], y[3], q.z, q.w);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint32_t kc = ka ^ (16 * c);
-      const uint4 A = lds128(kc), C = lds128(kc + 8 * kRow);
-      const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, cw[4] = {C.x, C.y, C.z, C.w};
-#pragma unroll
-      for (int w = 0; w < 4; w += 2) {
-        const uint32_t a0 = pair8<FMT, 0>(aw[w]), a2 = pair8<FMT, 1>(aw[w]);
-        const uint32_t a1 = pair8<FMT, 0>(cw[w]), a3 = pair8<FMT, 1>(cw[w]);
-        const uint32_t b0 = pair8<FMT, 0>(aw[w + 1]), b2 = pair8<FMT, 1>(aw[w + 1]);
-        const uint32_t b1 = pair8<FMT, 0>(cw[w + 1]), b3 = pair8<FMT, 1>(cw[w + 1]);
+      for (int w = 0; w < 4; ++w) {
+        uint32_t x[4], y[4];
+        i4_pairs(aw[w], s0, x);
+        i4_pairs(dw[w], s1, y);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 q = lds128(qa + (n * 4 + 2 * c + w / 2) * 512);
-          mma_f16(sa[n], a0, a1, a2, a3, q.x, q.y);
-          mma_f16(sa[n], b0, b1, b2, b3, q.z, q.w);
+          const uint4 q = lds128(qa + (n * 4 + w) * 512);
+          mma_f16(sa[c][n], x[0], y[0], x[1], y[1], q.x, q.y);
+          mma_f16(sa[c][n], x[2], y[2], x[3], y[3], q.z, q.w);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t kc = ka ^ (16 * h);
+        const uint4 A = lds128(kc), D = lds128(kc + 8 * kRow);
+        const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, dw[4] = {D.x, D.y, D.z, D.w};
+#pragma unroll
+        for (int w = 0; w < 4; w += 2) {
+          const uint32_t a0 = pair8<FMT, 0>(aw[w]), a2 = pair8<FMT, 1>(aw[w]);
+          const uint32_t a1 = pair8<FMT, 0>(dw[w]), a3 = pair8<FMT, 1>(dw[w]);
+          const uint32_t b0 = pair8<FMT, 0>(aw[w + 1]), b2 = pair8<FMT, 1>(aw[w + 1]);
+          const uint32_t b1 = pair8<FMT, 0>(dw[w + 1]), b3 = pair8<FMT, 1>(dw[w + 1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 q = lds128(qa + (n * 4 + 2 * h + w / 2) * 512);
+            mma_f16(sa[c][n], a0, a1, a2, a3, q.x, q.y);
+            mma_f16(sa[c][n], b0, b1, b2, b3, q.z, q.w);
+          }
         }
       }
     }
   }
-  // ---- weights: y = logit (log2 units) - m, p = 2^y, w = p v_scale f ----
-  float ks0 = lds_f(sbase + off.scale), ks1 = lds_f(sbase + off.scale + 32);
-  float vs0 = lds_f(sbase + off.scale + kV), vs1 = lds_f(sbase + off.scale + kV + 32);
-  float y[2 * NT][2], p[2 * NT][2], w[2 * NT][2];
+  // ---- weights: z = logit in log2 units, p = 2^(z - m), w = p v_scale f ----
+  float vs[C][2], z[C][2 * NT][2], w[C][2 * NT][2], sum[2 * NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = 2 * n + e;
-      y[j][0] = fmaf(sa[n][e], qs[j] * ks0, -st.m[j]);
-      y[j][1] = fmaf(sa[n][2 + e], qs[j] * ks1, -st.m[j]);
+    for (int r = 0; r < 2; ++r) {
+      const float ks = lds_f(sbase[c] + off.scale + 32 * r);
+      vs[c][r] = lds_f(sbase[c] + off.scale + kV + 32 * r);
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) z[c][j][r] = sa[c][j >> 1][2 * r + (j & 1)] * (qs[j] * ks);
     }
   if (!whole) {
     // rows outside the attended range may hold anything: no value of theirs is used
-    const int lo = range & 255, hi = range >> 8;
-    const bool on0 = g >= lo && g < hi, on1 = g + 8 >= lo && g + 8 < hi;
-    if (!on0) vs0 = 0.f;
-    if (!on1) vs1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) {
-      if (!on0) y[j][0] = -INFINITY;
-      if (!on1) y[j][1] = -INFINITY;
-    }
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        if (row < (range[c] & 255) || row >= (range[c] >> 8)) {
+          vs[c][r] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2 * NT; ++j) z[c][j][r] = -INFINITY;
+        }
+      }
   }
   float pmax = 0.f, wmax = 0.f;
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-    p[j][0] = ex2_approx(y[j][0]);
-    p[j][1] = ex2_approx(y[j][1]);
-    w[j][0] = p[j][0] * vs0 * st.f[j];
-    w[j][1] = p[j][1] * vs1 * st.f[j];
-    pmax = fmaxf(pmax, fmaxf(p[j][0], p[j][1]));
-    wmax = fmaxf(wmax, fmaxf(fabsf(w[j][0]), fabsf(w[j][1])));
+    sum[j] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float p = ex2_approx(z[c][j][r] - st.m[j]);
+        sum[j] += p;
+        w[c][j][r] = p * vs[c][r] * st.f[j];
+        wmax = fmaxf(wmax, fabsf(w[c][j][r]));
+      }
+    pmax = fmaxf(pmax, sum[j]);
   }
-  // The references move only when a logit passes its reference by 2^8 or a
+  // The references move only when a logit passes its reference by about 2^8 or a
   // weight leaves f16's range: a few times per sequence, so most chunks do no
   // rescaling.  (Before the first token m is the lowest float and p infinite.)
   if (__any_sync(kFull, pmax > 256.f || wmax > 32768.f)) {
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-      float up_m = fmaxf(0.f, fmaxf(y[j][0], y[j][1]));
-      // y is relative to m; before the first token it is logit + FLT_MAX, whose
-      // logit is lost to rounding: take the logits themselves there
-      const bool fresh = st.m[j] == kNone;
       const int n = j >> 1, e = j & 1;
-      const float z0 = y[j][0] == -INFINITY ? -INFINITY : sa[n][e] * (qs[j] * ks0);
-      const float z1 = y[j][1] == -INFINITY ? -INFINITY : sa[n][2 + e] * (qs[j] * ks1);
-      float mx = fresh ? fmaxf(z0, z1) : st.m[j] + up_m;
+      float mx = kNone, xm = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) mx = fmaxf(mx, fmaxf(z[c][j][0], z[c][j][1]));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-      mx = fmaxf(mx, kNone);                       // (no token of this head yet)
+      mx = fmaxf(mx, st.m[j]);
       const float alpha = ex2_approx(st.m[j] - mx);
       st.m[j] = mx;
       st.l[j] *= alpha;
-      p[j][0] = ex2_approx(z0 - mx);
-      p[j][1] = ex2_approx(z1 - mx);
-      float xm = fmaxf(fabsf(p[j][0] * vs0), fabsf(p[j][1] * vs1));
+      sum[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p = ex2_approx(z[c][j][r] - mx);
+          sum[j] += p;
+          w[c][j][r] = p * vs[c][r];
+          xm = fmaxf(xm, fabsf(w[c][j][r]));
+        }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
       const float f = st.f[j];
@@ -321,8 +356,11 @@ __device__ __forceinline__ void attend16(uint32_t base, uint32_t sbase, const La
       const float fn = fminf(128.f / xm, 1.2676506e30f);
       const float up = f > 0.f ? alpha * (fn / f) : 0.f;
       st.f[j] = fn;
-      w[j][0] = p[j][0] * vs0 * fn;
-      w[j][1] = p[j][1] * vs1 * fn;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        w[c][j][0] *= fn;
+        w[c][j][1] *= fn;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         st.acc[n][i][e] *= up;
@@ -331,81 +369,92 @@ __device__ __forceinline__ void attend16(uint32_t base, uint32_t sbase, const La
     }
   }
   // ---- P^T as the second operand ----
-  uint32_t pb[NT][2];
+  uint32_t pb[C][NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int j = 2 * n;
-    st.l[j] += p[j][0] + p[j][1];
-    st.l[j + 1] += p[j + 1][0] + p[j + 1][1];
-    pb[n][0] = transpose8x8(f16x2(w[j][0], w[j + 1][0]));
-    pb[n][1] = transpose8x8(f16x2(w[j][1], w[j + 1][1]));
-  }
+  for (int j = 0; j < 2 * NT; ++j) st.l[j] += sum[j];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        pb[c][n][r] = transpose8x8(f16x2(w[c][2 * n][r], w[c][2 * n + 1][r]));
   // ---- O^T += V^T P^T: this lane's tokens 2t, 2t+1, 2t+8, 2t+9, dims 16g .. 16g+15 ----
-  const uint32_t va = base + off.v;
   constexpr int kTok[4] = {0, 1, 8, 9};            // beyond 2t
-  if constexpr (FMT == LOCKS_KV_I4) {
-    uint2 T[4];
-    uint32_t gs[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      T[i] = lds64(va + kTok[i] * kRow);
-      gs[i] = lds_u8(sbase + off.gv + 4 * kTok[i]);
-    }
-    if (!whole) {                                  // 0 x NaN must not enter the sum
+  for (int c = 0; c < C; ++c) {
+    const uint32_t va = base[c] + off.v;
+    if constexpr (FMT == LOCKS_KV_I4) {
+      uint2 T[4];
+      uint32_t gs[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * t + kTok[i] < (range & 255) || 2 * t + kTok[i] >= (range >> 8)) gs[i] = 0;
-    }
-    const I4Scale s01 = i4_scale(e4m3x2_to_f16x2(gs[0] | (gs[1] << 8)));
-    const I4Scale s23 = i4_scale(e4m3x2_to_f16x2(gs[2] | (gs[3] << 8)));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {       // dims 4q .. 4q + 3: half a word of each token
-      const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
-      const uint32_t a = prmt(q < 2 ? T[0].x : T[0].y, q < 2 ? T[1].x : T[1].y, sel);
-      const uint32_t c = prmt(q < 2 ? T[2].x : T[2].y, q < 2 ? T[3].x : T[3].y, sel);
-      uint32_t x[4], z[4];
-      i4_pairs(a, s01, x);
-      i4_pairs(c, s23, z);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_f16(st.acc[n][2 * q], x[0], x[1], z[0], z[1], pb[n][0], pb[n][1]);
-        mma_f16(st.acc[n][2 * q + 1], x[2], x[3], z[2], z[3], pb[n][0], pb[n][1]);
+      for (int i = 0; i < 4; ++i) {
+        T[i] = lds64(va + kTok[i] * kRow);
+        gs[i] = lds_u8(sbase[c] + off.gv + 4 * kTok[i]);
       }
-    }
-  } else {
-    uint4 T[4];
-    T[0] = lds128(va);
-    T[1] = lds128((va ^ 16) + kRow);               // odd rows: the neighbouring chunk place
-    T[2] = lds128(va + 8 * kRow);
-    T[3] = lds128((va ^ 16) + 9 * kRow);
-    if (FMT == LOCKS_KV_F8 && !whole) {            // e4m3 NaN codes
+      if (!whole) {                                // 0 x NaN must not enter the sum
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * t + kTok[i] < (range & 255) || 2 * t + kTok[i] >= (range >> 8))
-          T[i] = make_uint4(0, 0, 0, 0);
-    }
-    const uint32_t T0[4] = {T[0].x, T[0].y, T[0].z, T[0].w}, T1[4] = {T[1].x, T[1].y, T[1].z, T[1].w};
-    const uint32_t T2[4] = {T[2].x, T[2].y, T[2].z, T[2].w}, T3[4] = {T[3].x, T[3].y, T[3].z, T[3].w};
+        for (int i = 0; i < 4; ++i)
+          if (2 * t + kTok[i] < (range[c] & 255) || 2 * t + kTok[i] >= (range[c] >> 8)) gs[i] = 0;
+      }
+      const I4Scale s01 = i4_scale(e4m3x2_to_f16x2(gs[0] | (gs[1] << 8)));
+      const I4Scale s23 = i4_scale(e4m3x2_to_f16x2(gs[2] | (gs[3] << 8)));
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 4; ++q) {       // dims 4q .. 4q + 3: half a word of each token
+        const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
+        const uint32_t a = prmt(q < 2 ? T[0].x : T[0].y, q < 2 ? T[1].x : T[1].y, sel);
+        const uint32_t d = prmt(q < 2 ? T[2].x : T[2].y, q < 2 ? T[3].x : T[3].y, sel);
+        uint32_t x[4], y[4];
+        i4_pairs(a, s01, x);
+        i4_pairs(d, s23, y);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {     // dims 4q + 2e, 4q + 2e + 1
-        const uint32_t sel = e ? 0x7362u : 0x5140u;
-        const uint32_t x = prmt(T0[q], T1[q], sel), z = prmt(T2[q], T3[q], sel);
-        const uint32_t a0 = pair8<FMT, 0>(x), a1 = pair8<FMT, 1>(x);
-        const uint32_t a2 = pair8<FMT, 0>(z), a3 = pair8<FMT, 1>(z);
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(st.acc[n][2 * q], x[0], x[1], y[0], y[1], pb[c][n][0], pb[c][n][1]);
+          mma_f16(st.acc[n][2 * q + 1], x[2], x[3], y[2], y[3], pb[c][n][0], pb[c][n][1]);
+        }
+      }
+    } else {
+      uint4 T[4];
+      T[0] = lds128(va);
+      T[1] = lds128((va ^ 16) + kRow);             // odd rows: the neighbouring chunk place
+      T[2] = lds128(va + 8 * kRow);
+      T[3] = lds128((va ^ 16) + 9 * kRow);
+      if (FMT == LOCKS_KV_F8 && !whole) {          // e4m3 NaN codes
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma_f16(st.acc[n][2 * q + e], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        for (int i = 0; i < 4; ++i)
+          if (2 * t + kTok[i] < (range[c] & 255) || 2 * t + kTok[i] >= (range[c] >> 8))
+            T[i] = make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t T0[4] = {T[0].x, T[0].y, T[0].z, T[0].w}, T1[4] = {T[1].x, T[1].y, T[1].z, T[1].w};
+      const uint32_t T2[4] = {T[2].x, T[2].y, T[2].z, T[2].w}, T3[4] = {T[3].x, T[3].y, T[3].z, T[3].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {     // dims 4q + 2e, 4q + 2e + 1
+          const uint32_t sel = e ? 0x7362u : 0x5140u;
+          const uint32_t x = prmt(T0[q], T1[q], sel), y = prmt(T2[q], T3[q], sel);
+          const uint32_t a0 = pair8<FMT, 0>(x), a1 = pair8<FMT, 1>(x);
+          const uint32_t a2 = pair8<FMT, 0>(y), a3 = pair8<FMT, 1>(y);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_f16(st.acc[n][2 * q + e], a0, a1, a2, a3, pb[c][n][0], pb[c][n][1]);
+        }
       }
     }
   }
 }
 
+// What a unit costs a block beside its stages, in stages: the warps wait for one
+// another at its end and merge their states.  (16 ragged sequences up to 16K in
+// int8: 69.3 us with 0, 65.3 with 3, 62.5 with 6; equal lengths do not care.)
+constexpr int kUnitCost = 6;
+
 // A sequence as the kernel walks it: its length, the first attended position,
 // its first stage and its number of stages (the same for every KV head).
 struct Seq {
   int n, lo, first, stages;
+  // cost of each of its units, overhead first
+  __device__ __forceinline__ int cost() const { return stages > 0 ? stages + kUnitCost : 0; }
 };
 __device__ __forceinline__ Seq seq_of(const KvDecodeParams& p, int b) {
   Seq s;
@@ -420,6 +469,59 @@ __device__ __forceinline__ Seq seq_of(const KvDecodeParams& p, int b) {
     s.stages = (s.n + kStageTok - 1) / kStageTok - s.first;
   }
   return s;
+}
+
+// The unit after (b, h), which starts at u in the list.
+__device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& sq, int& h, int& u,
+                                          int end) {
+  u += sq.cost();
+  if (++h < p.n_kv_heads || u >= end) return;     // (beyond `end` there may be no sequence)
+  h = 0;
+  do sq = seq_of(p, ++b);
+  while (sq.stages == 0);
+}
+
+// A unit's query for heads h0 .. h0 + 7 (lane 4g + t: head h0 + g, dims 32t ..
+// 32t + 31): brought to a largest magnitude in [2^14, 2^15) by a power of two,
+// rounded to f16 (exact but for elements below 2^-28 of it) and laid out as the
+// second operand of the eight k-steps.
+template <int FMT>
+__device__ __forceinline__ void put_query(const KvDecodeParams& p, int unit, int h0, int lane,
+                                          uint4 (*to)[32], float* scale) {
+  const int head = h0 + (lane >> 2), t = lane & 3;
+  uint4 raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (head < p.group)
+      raw[i] = *reinterpret_cast<const uint4*>(p.q + (size_t(unit) * p.group + head) * kHeadDim +
+                                               32 * t + 8 * i);
+  }
+  uint32_t mx = 0;                                // largest magnitude, as bf16 bits
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    mx = __vmaxu2(__vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                           __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)), mx);
+  mx = max(mx & 0xffffu, mx >> 16);
+  mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
+  mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
+  const int ex = int(mx >> 7);                    // biased exponent
+  // factor 2^(14 - (ex - 127)), at most 2^126; infinities and NaN stay what they are
+  const int up = ex == 255 ? 0 : min(126, 141 - ex);
+  const float f = __uint_as_float(uint32_t(127 + up) << 23);
+  constexpr float kScale = 0.08838834764831845f * kLog2e * (FMT == LOCKS_KV_I4 ? 256.f : 1.f);
+  if (t == 0) scale[head] = __uint_as_float(uint32_t(127 - up) << 23) * kScale;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {                   // k-steps 2w, 2w + 1: dims 8w .. 8w + 7 of the lane's
+    const float x0 = bf16_lo(raw[w].x) * f, x1 = bf16_hi(raw[w].x) * f;
+    const float x2 = bf16_lo(raw[w].y) * f, x3 = bf16_hi(raw[w].y) * f;
+    const float x4 = bf16_lo(raw[w].z) * f, x5 = bf16_hi(raw[w].z) * f;
+    const float x6 = bf16_lo(raw[w].w) * f, x7 = bf16_hi(raw[w].w) * f;
+    // 4 bits: nibbles (n, n + 4) of word w; 8 bits: bytes (0, 1), (2, 3) of words 2w, 2w + 1
+    to[w][lane] = FMT == LOCKS_KV_I4
+                      ? make_uint4(f16x2(x0, x4), f16x2(x1, x5), f16x2(x2, x6), f16x2(x3, x7))
+                      : make_uint4(f16x2(x0, x1), f16x2(x2, x3), f16x2(x4, x5), f16x2(x6, x7));
+  }
 }
 
 // A warp's state for heads 8n .. 8n + 7 into shared memory: float4 x of a lane
@@ -442,18 +544,32 @@ __device__ __forceinline__ void put_state(const State<NT>& st, int n, float4* to
   }
 }
 
+// Two dims of an output row from sum p v, the reference and sum p.
+__device__ __forceinline__ void store_out(const KvDecodeParams& p, size_t row, int dim, float2 A,
+                                          float M, float L) {
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<__nv_bfloat162*>(p.out + row * kHeadDim + dim) =
+      __floats2bfloat162_rn(A.x * inv, A.y * inv);
+  if (p.out_lse && dim == 0) p.out_lse[row] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
+}
+
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(const KvDecodeParams p) {
-  constexpr int STAGES = kv_stages(FMT, NT);
+__global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDecodeParams p) {
+  constexpr int STAGES = kv_stages(FMT);
+  constexpr int C = kv_chunks(FMT, NT), JOBS = 4 / C;   // chunks of a job, jobs of a stage
   constexpr int kStageBytes = kv_stage_bytes(FMT);
+  constexpr int kKvWarps = kv_warps(NT), kKvThreads = kv_threads(NT);
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* ring = smem;
   float4* mbuf = reinterpret_cast<float4*>(smem + STAGES * kStageBytes);    // [warp][8][32]
   __shared__ uint64_t s_full[STAGES], s_empty[STAGES];
   __shared__ uint2 s_chunk[4];                    // a chunk's codes and scales in a stage
   __shared__ int s_range[STAGES][4];              // valid rows of each 16-token chunk: lo | hi << 8
-  __shared__ uint4 s_q[NT][4][32];                // query operands of the k-steps
-  __shared__ float s_qs[8 * NT];                  // what brings their products to log2 units
+  // of this unit and the next: query operands of the k-steps, and what brings their
+  // products to log2 units
+  __shared__ uint4 s_q[2][NT][4][32];
+  __shared__ float s_qs[2][8 * NT];
+  __shared__ uint64_t s_qfull[2], s_qempty[2];
   __shared__ float s_m[kKvWarps][8 * NT], s_l[kKvWarps][8 * NT];
   __shared__ int s_scan[kKvThreads / 32], s_base, s_first, s_last;
 
@@ -462,7 +578,11 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(s_full + s, 1);
-      mbar_init(s_empty + s, 4);
+      mbar_init(s_empty + s, JOBS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_qfull + i, NT);
+      mbar_init(s_qempty + i, kKvWarps);
     }
     mbar_fence_init();
   }
@@ -474,7 +594,7 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
   int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    mine += seq_of(p, b).stages;
+    mine += seq_of(p, b).cost();
     if (blockIdx.x == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.max_pages * B))
       flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
   }
@@ -492,14 +612,14 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
     if (w == warp) incl += total;
     total += s_scan[w];
   }
-  const int W = total * hk;                       // below 2^31: the host has checked
+  const int W = total * hk;                       // cost of all units; below 2^31: the host has checked
   const int N = min(int(gridDim.x), max(W, 1));
   const int w_lo = int(blockIdx.x) < N ? int(int64_t(W) * blockIdx.x / N) : 0;
   const int w_hi = int(blockIdx.x) < N ? int(int64_t(W) * (blockIdx.x + 1) / N) : 0;
   if (w_lo < w_hi && (incl - mine) * hk <= w_lo && w_lo < incl * hk) {
     int at = (incl - mine) * hk;
     for (int b = b_lo; b < b_hi; ++b) {
-      const int n = seq_of(p, b).stages * hk;
+      const int n = seq_of(p, b).cost() * hk;
       if (w_lo - at < n) {
         s_first = b;
         s_base = at;
@@ -523,28 +643,45 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
   const size_t rec = size_t(kv_rec_bytes(FMT, B));
   int b = s_first;
   Seq sq = seq_of(p, b);
-  int base = s_base;                              // first stage of sequence b in the list
-  int h = (w_lo - base) / sq.stages;
-  int i0 = (w_lo - base) % sq.stages;
-  int left = w_hi - w_lo;
+  int h = (w_lo - s_base) / sq.cost();
+  int u = s_base + h * sq.cost();                 // where unit (b, h) starts in the list
   int it = 0;                                     // stages of this block so far
   if (tid < 4) {                                  // (one barrier before its first use is below)
     const int e = 16 * tid / B, r0 = 16 * tid - e * B;
     s_chunk[tid] = make_uint2(e * uint32_t(rec) + r0 * kv_row_bytes(FMT), e * uint32_t(rec) + 4 * r0);
   }
 
-  if (warp == kKvWarps) {
+  if (warp >= kKvWarps) {
     // ---------------- producer ----------------
+    if constexpr (NT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     const uint64_t pol = l2_evict_first();
+    const int pw = warp - kKvWarps;
+    const int e = lane & (pps - 1), mine = lane / pps;   // this lane's page of a stage, and its stage
+    const int cpp = B / 16;                       // chunks of a page
+    const int looked = 32 / pps;                  // stages looked up at a time
+    int s = pw, phase = 1;                        // ring slot of the warp's next stage; nothing to wait for yet
     bool ok = true;
-    while (left > 0 && ok) {
-      const int cnt = min(sq.stages - i0, left);
+    for (int seg = 0; ok; next_unit(p, b, sq, h, u, w_hi)) {
+      if (u >= w_hi) break;
+      const int i0 = max(0, w_lo - u - kUnitCost);
+      const int cnt = min(sq.stages, w_hi - u - kUnitCost) - i0;
+      if (cnt <= 0) continue;
+      if (pw >= 4 - NT) {                         // the last warps bring the unit's query
+        const int n = pw - (4 - NT);
+        if (!__all_sync(kFull, mbar_wait_bounded(s_qempty + (seg & 1), ((seg >> 1) & 1) ^ 1))) {
+          if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
+          break;
+        }
+        put_query<FMT>(p, b * hk + h, 8 * n, lane, s_q[seg & 1][n], s_qs[seg & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_qfull + (seg & 1));
+      }
       const int32_t* row = p.block_table + size_t(b) * p.max_pages;
       const int32_t* sel = p.selected ? p.selected + (size_t(b) * hk + h) * p.k : nullptr;
       const int pages = (sq.n + B - 1) / B;
-      const int batch_st = 32 / pps;              // stages looked up at a time
-      for (int s0 = 0; s0 < cnt && ok; s0 += batch_st) {
-        const int e = lane & (pps - 1), st = s0 + lane / pps;
+      // this warp's stages of the segment: those whose number in the block is pw mod 4
+      for (int s0 = (pw - it) & 3; s0 < cnt && ok; s0 += 4 * looked) {
+        const int st = s0 + 4 * mine;
         int blk = -1, r_lo = 0, r_hi = 0;
         if (st < cnt) {
           const int slot = (sq.first + i0 + st) * pps + e;
@@ -567,110 +704,80 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
           }
           if (blk < 0) r_lo = r_hi = 0;
         }
-        const int todo = min(batch_st, cnt - s0);
-        for (int x = 0; x < todo; ++x, ++it) {
-          const int s = it % STAGES;
-          if (it >= STAGES &&
-              !__all_sync(kFull, mbar_wait_bounded(s_empty + s, ((it / STAGES) - 1) & 1))) {
+        const size_t src = (size_t(max(blk, 0)) * hk + h) * rec;
+        const unsigned char *ksrc = p.k_pool + src, *vsrc = p.v_pool + src;
+        int range[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          range[c] = min(16, max(0, r_lo - 16 * c)) | (min(16, max(0, r_hi - 16 * c)) << 8);
+        const unsigned live = __ballot_sync(kFull, blk >= 0);
+        const int todo = min(looked, (cnt - s0 + 3) / 4);
+        for (int x = 0; x < todo; ++x) {
+          if (!mbar_wait_bounded(s_empty + s, phase)) ok = false;
+          if (!__all_sync(kFull, ok)) {
             if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
             ok = false;
             break;
           }
-          const bool me = lane / pps == x;
-          if (me)
-            for (int c = 0; c < B / 16; ++c)
-              s_range[s][e * (B / 16) + c] =
-                  min(16, max(0, r_lo - 16 * c)) | (min(16, max(0, r_hi - 16 * c)) << 8);
-          const unsigned live = __ballot_sync(kFull, me && blk >= 0);
-          // (the ballot does not order the lanes' stores of s_range)
+          if (mine == x) {
+            int* r = s_range[s] + e * cpp;
+            r[0] = range[0];
+            if (cpp > 1) r[1] = range[1];
+            if (cpp > 2) {
+              r[2] = range[2];
+              r[3] = range[3];
+            }
+          }
           __syncwarp();
           if (lane == 0) {
-            if (live) mbar_arrive_expect_tx(s_full + s, uint32_t(__popc(live) * 2 * rec));
+            const int n = __popc((live >> (x * pps)) & ((1u << pps) - 1));
+            if (n) mbar_arrive_expect_tx(s_full + s, uint32_t(n * 2 * rec));
             else mbar_arrive(s_full + s);
           }
           __syncwarp();
-          if (me && blk >= 0) {
+          if (mine == x && blk >= 0) {
             unsigned char* dst = ring + s * kStageBytes + e * rec;
-            const size_t src = (size_t(blk) * hk + h) * rec;
-            bulk_g2s_hint(dst, p.k_pool + src, uint32_t(rec), s_full + s, pol);
-            bulk_g2s_hint(dst + kStageBytes / 2, p.v_pool + src, uint32_t(rec), s_full + s, pol);
+            bulk_g2s_hint(dst, ksrc, uint32_t(rec), s_full + s, pol);
+            bulk_g2s_hint(dst + kStageBytes / 2, vsrc, uint32_t(rec), s_full + s, pol);
+          }
+          s += 4;
+          if (s >= STAGES) {
+            s -= STAGES;
+            phase ^= 1;
           }
         }
       }
-      left -= cnt;
-      i0 = 0;
-      if (++h == hk && left > 0) {
-        h = 0;
-        do {
-          base += sq.stages * hk;
-          sq = seq_of(p, ++b);
-        } while (sq.stages == 0);
-      }
+      it += cnt;
+      ++seg;
     }
     return;
   }
 
   // ---------------- consumers ----------------
+  if constexpr (NT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
   const int g = lane >> 2, t = lane & 3, G = p.group;
   const LaneOff off = lane_off<FMT>(B, g, t);
-  const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(s_q) + 16 * lane;
+  const uint32_t ring_at = smem_u32(ring);
   bool ok = true;
-  // 16-token chunks go round the warps: chunk `job` of this block, in ring slot s
-  int job = warp, s = warp >> 2, phase = 0;
+  // jobs of C 16-token chunks go round the warps: job `job` of this block, in ring slot s
+  int job = warp, s = warp / JOBS, phase = 0;
   while (s >= STAGES) {
     s -= STAGES;
     phase ^= 1;
   }
-  while (left > 0) {
-    const int cnt = min(sq.stages - i0, left);
+  for (int seg = 0; u < w_hi; next_unit(p, b, sq, h, u, w_hi)) {
+    const int i0 = max(0, w_lo - u - kUnitCost);
+    const int cnt = min(sq.stages, w_hi - u - kUnitCost) - i0;
+    if (cnt <= 0) continue;
     const int unit = b * hk + h;
-    // ---- the query, by warp n for heads 8n + g, dims 32t .. 32t + 31: brought to a largest
-    // magnitude in [2^14, 2^15) by a power of two, rounded to f16 (exact but for elements below
-    // 2^-28 of it) and laid out as the second operand of the eight k-steps ----
-    if (warp < NT) {
-      const int head = 8 * warp + g;
-      float x[32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (head < G)
-          w = *reinterpret_cast<const uint4*>(p.q + (size_t(unit) * G + head) * kHeadDim + 32 * t + 8 * i);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[8 * i + 2 * e] = bf16_lo(ww[e]);
-          x[8 * i + 2 * e + 1] = bf16_hi(ww[e]);
-        }
-      }
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const int ex = int(__float_as_uint(mx) >> 23);          // biased exponent
-      // factor 2^(14 - (ex - 127)), at most 2^126; an infinity keeps its value
-      const int up = ex == 255 ? 0 : min(126, 141 - ex);
-      const float factor = __uint_as_float(uint32_t(127 + up) << 23);
-      constexpr float kScale = 0.08838834764831845f * kLog2e * (FMT == LOCKS_KV_I4 ? 256.f : 1.f);
-      if (t == 0) s_qs[head] = __uint_as_float(uint32_t(127 - up) << 23) * kScale;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] *= factor;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {                           // k-steps 2w, 2w + 1
-        const int d = 8 * w;
-        // 4 bits: nibbles (n, n + 4) of word w; 8 bits: bytes (0, 1), (2, 3) of words 2w, 2w + 1
-        s_q[warp][w][lane] =
-            FMT == LOCKS_KV_I4
-                ? make_uint4(f16x2(x[d], x[d + 4]), f16x2(x[d + 1], x[d + 5]),
-                             f16x2(x[d + 2], x[d + 6]), f16x2(x[d + 3], x[d + 7]))
-                : make_uint4(f16x2(x[d], x[d + 1]), f16x2(x[d + 2], x[d + 3]),
-                             f16x2(x[d + 4], x[d + 5]), f16x2(x[d + 6], x[d + 7]));
-      }
+    if (ok && !__all_sync(kFull, mbar_wait_bounded(s_qfull + (seg & 1), (seg >> 1) & 1))) {
+      if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
+      ok = false;
     }
-    consumers_sync();
+    const uint32_t q_at = smem_u32(s_q[seg & 1]) + 16 * lane;
     float qs[2 * NT];
 #pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) qs[j] = s_qs[8 * (j >> 1) + 2 * t + (j & 1)];
+    for (int j = 0; j < 2 * NT; ++j) qs[j] = s_qs[seg & 1][8 * (j >> 1) + 2 * t + (j & 1)];
     State<NT> st;
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
@@ -685,22 +792,29 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
         for (int e = 0; e < 4; ++e) st.acc[n][i][e] = 0.f;
 
     it += cnt;
-    for (; (job >> 2) < it; job += kKvWarps) {
-      const int c = job & 3;
+    for (; job / JOBS < it; job += kKvWarps) {
+      const int c0 = job % JOBS * C;
       if (ok && !__all_sync(kFull, mbar_wait_bounded(s_full + s, phase))) {
         if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
         ok = false;                               // the rest counts as empty: tickets stay right
       }
       if (ok) {
-        const int range = s_range[s][c];
-        const uint2 at = s_chunk[c];
-        if ((range >> 8) > (range & 255))
-          attend16<FMT, NT>(ring_at + s * kStageBytes + at.x, ring_at + s * kStageBytes + at.y, off,
-                            range, g, t, q_at, qs, st);
+        uint32_t base[C], sbase[C];
+        int range[C];
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const uint2 at = s_chunk[c0 + c];
+          base[c] = ring_at + s * kStageBytes + at.x;
+          sbase[c] = ring_at + s * kStageBytes + at.y;
+          range[c] = s_range[s][c0 + c];
+          any |= (range[c] >> 8) > (range[c] & 255);
+        }
+        if (any) attend<FMT, NT, C>(base, sbase, range, off, g, t, q_at, qs, st);
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty + s);
       }
-      s += ((job + kKvWarps) >> 2) - (job >> 2);
+      s += (job + kKvWarps) / JOBS - job / JOBS;
       if (s >= STAGES) {
         s -= STAGES;
         phase ^= 1;
@@ -708,7 +822,8 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
     }
 
     // ---- merge the warps' states; finish the unit or leave a partial ----
-    const int u_lo = base + h * sq.stages, u_hi = u_lo + sq.stages;
+    // the blocks of the unit's first and last stage
+    const int u_lo = u + kUnitCost, u_hi = u_lo + sq.stages;
     const int c_lo = int((int64_t(u_lo + 1) * N - 1) / W), c_hi = int((int64_t(u_hi) * N - 1) / W);
     const bool alone = c_lo == c_hi;
     const int slot = int(blockIdx.x) == c_lo ? 1 : 0;
@@ -727,131 +842,89 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
         st.acc[j >> 1][i][2 + (j & 1)] *= f;
       }
     }
-    // item of this thread: head parity and 4 dims of a lane's 16
-    const int odd = warp >> 2, dq = warp & 3;
+    if (lane == 0) mbar_arrive(s_qempty + (seg & 1));
+    consumers_sync<NT>();                         // the buffer's last readers are done
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      // warps from kMergeWarps on hand their states to the first ones ...
-      float4* mine = mbuf + (warp % kMergeWarps) * 256 + lane;
-      if (warp >= kMergeWarps) put_state<NT>(st, n, mine, s_m[warp], s_l[warp], g, t);
-      consumers_sync();
-      if (warp + kMergeWarps < kKvWarps) {
+      if (n) consumers_sync<NT>();
+      put_state<NT>(st, n, mbuf + warp * 256 + lane, s_m[warp], s_l[warp], g, t);
+      consumers_sync<NT>();
+      // a thread's items: float2 pairs of the 1024 floats, as the lanes laid them out
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = 2 * n + e, head = 8 * n + 2 * t + e;
-          const float m2 = s_m[warp + kMergeWarps][head], M = fmaxf(st.m[j], m2);
-          const float fa = exp2f(st.m[j] - M), fb = exp2f(m2 - M);
-          st.m[j] = M;
-          st.l[j] = st.l[j] * fa + s_l[warp + kMergeWarps][head] * fb;
+      for (int i = 0; i < 512 / (kKvWarps * 32); ++i) {
+        const int x = i * kKvWarps * 32 + tid, q4 = x >> 6, l2 = (x >> 1) & 31;
+        const int head = 8 * n + 2 * (l2 & 3) + (q4 >> 2);
+        const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
+        float M = kNone, L = 0.f;
+        float2 A = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float4 o = mine[(4 * e + x) * 32];
-            float (&a0)[4] = st.acc[n][2 * x], (&a1)[4] = st.acc[n][2 * x + 1];
-            a0[e] = a0[e] * fa + o.x * fb;
-            a0[2 + e] = a0[2 + e] * fa + o.y * fb;
-            a1[e] = a1[e] * fa + o.z * fb;
-            a1[2 + e] = a1[2 + e] * fa + o.w * fb;
-          }
+        for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, s_m[w][head]);
+#pragma unroll
+        for (int w = 0; w < kKvWarps; ++w) {
+          const float f = ex2_approx(s_m[w][head] - M);
+          const float2 a = reinterpret_cast<const float2*>(mbuf + w * 256)[x];
+          L += s_l[w][head] * f;
+          A.x += a.x * f;
+          A.y += a.y * f;
+        }
+        if (alone) {
+          if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
+        } else {
+          reinterpret_cast<float2*>(part)[n * 512 + x] = A;
+          if (dim == 0) *reinterpret_cast<float2*>(part + NT * 1024 + 2 * head) = make_float2(M, L);
         }
       }
-      consumers_sync();
-      // ... whose sums are taken item by item
-      if (warp < kMergeWarps) put_state<NT>(st, n, mine, s_m[warp], s_l[warp], g, t);
-      consumers_sync();
-      const int head = 8 * n + 2 * t + odd;
-      float M = kNone, L = 0.f;
-      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w][head]);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        const float f = exp2f(s_m[w][head] - M);
-        const float4 a = mbuf[(w * 8 + warp) * 32 + lane];
-        L += s_l[w][head] * f;
-        A.x += a.x * f; A.y += a.y * f; A.z += a.z * f; A.w += a.w * f;
-      }
-      if (alone) {
-        if (head < G) {
-          const float inv = L != 0.f ? 1.f / L : 0.f;
-          uint2 o;
-          const __nv_bfloat162 o0 = __floats2bfloat162_rn(A.x * inv, A.y * inv);
-          const __nv_bfloat162 o1 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
-          o.x = *reinterpret_cast<const uint32_t*>(&o0);
-          o.y = *reinterpret_cast<const uint32_t*>(&o1);
-          *reinterpret_cast<uint2*>(p.out + (size_t(unit) * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
-          if (p.out_lse && g == 0 && dq == 0)
-            p.out_lse[size_t(unit) * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
-        }
-      } else {
-        reinterpret_cast<float4*>(part)[(n * 8 + warp) * 32 + lane] = A;
-        if (g == 0 && dq == 0)
-          *reinterpret_cast<float2*>(part + NT * 1024 + 2 * head) = make_float2(M, L);
-      }
-      consumers_sync();                           // mbuf is free again
     }
     if (!alone) {
       __threadfence();
-      consumers_sync();
+      consumers_sync<NT>();
       if (tid == 0) s_last = atomicAdd(tickets + unit, 1) == c_hi - c_lo;
-      consumers_sync();
+      consumers_sync<NT>();
       if (s_last) {
         __threadfence();
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int head = 8 * n + 2 * t + odd;
-          float M = kNone, L = 0.f;
-          float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = c_lo; c <= c_hi; c += 8) {
-            float2 ml[8];
-            float4 a[8];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ml[i] = make_float2(kNone, 0.f);
-              a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (c + i <= c_hi) {
-                const float* src = parts + (size_t(c + i) * 2 + (c + i == c_lo)) * (kv_part_bytes(NT) / 4);
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(src + NT * 1024 + 2 * head));
-                a[i] = __ldcg(reinterpret_cast<const float4*>(src) + (n * 8 + warp) * 32 + lane);
+          for (int i = 0; i < 512 / (kKvWarps * 32); ++i) {
+            const int x = i * kKvWarps * 32 + tid, q4 = x >> 6, l2 = (x >> 1) & 31;
+            const int head = 8 * n + 2 * (l2 & 3) + (q4 >> 2);
+            const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
+            float M = kNone, L = 0.f;
+            float2 A = make_float2(0.f, 0.f);
+            for (int c = c_lo; c <= c_hi; c += 8) {
+              float2 ml[8], a[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                ml[k] = make_float2(kNone, 0.f);
+                a[k] = make_float2(0.f, 0.f);
+                if (c + k <= c_hi) {
+                  const float* src = parts + (size_t(c + k) * 2 + (c + k == c_lo)) * (kv_part_bytes(NT) / 4);
+                  ml[k] = __ldcg(reinterpret_cast<const float2*>(src + NT * 1024 + 2 * head));
+                  a[k] = __ldcg(reinterpret_cast<const float2*>(src) + n * 512 + x);
+                }
+              }
+              float Mn = M;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, ml[k].x);
+              const float f0 = ex2_approx(M - Mn);
+              L *= f0;
+              A.x *= f0;
+              A.y *= f0;
+              M = Mn;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float f = ex2_approx(ml[k].x - Mn);
+                L += ml[k].y * f;
+                A.x += a[k].x * f;
+                A.y += a[k].y * f;
               }
             }
-            float Mn = M;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) Mn = fmaxf(Mn, ml[i].x);
-            const float f0 = exp2f(M - Mn);
-            L *= f0;
-            A.x *= f0; A.y *= f0; A.z *= f0; A.w *= f0;
-            M = Mn;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = exp2f(ml[i].x - Mn);
-              L += ml[i].y * f;
-              A.x += a[i].x * f; A.y += a[i].y * f; A.z += a[i].z * f; A.w += a[i].w * f;
-            }
+            if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
           }
-          if (head < G) {
-            const float inv = L != 0.f ? 1.f / L : 0.f;
-            uint2 o;
-            const __nv_bfloat162 o0 = __floats2bfloat162_rn(A.x * inv, A.y * inv);
-            const __nv_bfloat162 o1 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
-            o.x = *reinterpret_cast<const uint32_t*>(&o0);
-            o.y = *reinterpret_cast<const uint32_t*>(&o1);
-            *reinterpret_cast<uint2*>(p.out + (size_t(unit) * G + head) * kHeadDim + 16 * g + 4 * dq) = o;
-            if (p.out_lse && g == 0 && dq == 0)
-              p.out_lse[size_t(unit) * G + head] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
-          }
-        }
         if (tid == 0) tickets[unit] = 0;
       }
     }
-    left -= cnt;
-    i0 = 0;
-    if (++h == hk && left > 0) {
-      h = 0;
-      do {
-        base += sq.stages * hk;
-        sq = seq_of(p, ++b);
-      } while (sq.stages == 0);
-    }
+    ++seg;
   }
   // a wait that ran out: no block leaves while copies into its memory may be in flight
   if (!ok)
@@ -860,11 +933,11 @@ __global__ void __launch_bounds__(kKvThreads, NT == 1 ? 2 : 1) kv_decode_kernel(
 
 template <int FMT, int NT>
 int launch_nt(const KvDecodeParams& p, cudaStream_t stream) {
-  constexpr size_t smem = size_t(kv_stages(FMT, NT)) * kv_stage_bytes(FMT) + kKvMergeBytes;
+  constexpr size_t smem = size_t(kv_stages(FMT)) * kv_stage_bytes(FMT) + kv_merge_bytes(NT);
   if (cudaFuncSetAttribute(kv_decode_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess)
     return LOCKS_ERR_CUDA;
-  return launch_dependent(kv_decode_kernel<FMT, NT>, dim3(kv_blocks(NT)), kKvThreads, smem, p, stream);
+  return launch_dependent(kv_decode_kernel<FMT, NT>, dim3(kSms), kv_threads(NT), smem, p, stream);
 }
 
 template <int FMT>
@@ -877,7 +950,7 @@ int launch_fmt(const KvDecodeParams& p, cudaStream_t stream) {
 size_t kv_decode_workspace(int batch, int n_kv_heads, int group) {
   const int nt = group <= 8 ? 1 : 2;
   return (size_t(batch) * n_kv_heads * 4 + 255) / 256 * 256 +
-         size_t(kv_blocks(nt)) * 2 * kv_part_bytes(nt);
+         size_t(kSms) * 2 * kv_part_bytes(nt);
 }
 
 int launch_kv_decode(const KvDecodeParams& p, int fmt, cudaStream_t stream) {
