@@ -10,6 +10,7 @@ calling a kernel entry point does, and a missing library raises
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -146,6 +147,11 @@ class LocksKvConfig:
     def group(self) -> int:
         return self.n_q_heads // self.n_kv_heads
 
+    @functools.cached_property
+    def pool_bytes(self) -> int:
+        """Bytes of the K (or the V) pool; 0 for a configuration the library refuses."""
+        return self.num_blocks * self.n_kv_heads * kv_record_bytes(self)
+
 
 _lib = None
 
@@ -210,6 +216,27 @@ def load_library(path: Optional[str] = None):
 # --------------------------------------------------------------------------
 # marshalling helpers
 # --------------------------------------------------------------------------
+_torch = None                 # torch, from the first call that needs it
+_current_raw_stream = None    # device index -> cudaStream_t of torch's current stream
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _find_raw_stream():
+    """torch's own accessor where it has one (a microsecond less a call than building a
+    torch.cuda.Stream), else through the Stream object."""
+    global _current_raw_stream
+    torch = _load_torch()
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _current_raw_stream
+
+
 def _ptr(x) -> Optional[int]:
     if x is None:
         return None
@@ -224,8 +251,8 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = _current_raw_stream or _find_raw_stream()
+        return raw(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -345,27 +372,31 @@ def rope_frequencies(spec: locks_rope_spec_t) -> Tuple:
 
 def _typed(x, dtype: str, what: str):
     """x, if it is a tensor (or None, or a raw pointer) of the dtype of that name."""
-    if x is not None and not isinstance(x, int):
-        import torch
-        if x.dtype is not getattr(torch, dtype):
-            raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
+    if x is not None and type(x) is not int and \
+            x.dtype is not getattr(_torch or _load_torch(), dtype):
+        raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
     return x
 
 
 def _sized(x, dtype: str, shape: Tuple, what: str) -> Optional[int]:
     """Pointer of a contiguous device tensor of that type and shape; None stays None."""
-    _typed(x, dtype, what)
-    if x is not None and not isinstance(x, int) and tuple(x.shape) != shape:
+    if x is None or type(x) is int:
+        return x
+    if x.dtype is not getattr(_torch or _load_torch(), dtype):
+        raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
+    if x.shape != shape:
         raise ValueError(f"{what}: shape {shape} expected, got {tuple(x.shape)}")
-    return _ptr(x)
+    if not x.is_cuda:
+        raise ValueError(f"{what}: device tensor expected")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: contiguous tensor expected")
+    return x.data_ptr()
 
 
 def _pool(x, cfg: LocksKvConfig, what: str) -> Optional[int]:
     """Pointer of a pool tensor, if it holds the records of every block of cfg."""
-    if x is not None and not isinstance(x, int):
-        need = cfg.num_blocks * cfg.n_kv_heads * kv_record_bytes(cfg)
-        if x.numel() * x.element_size() < need:
-            raise ValueError(f"{what}: {need} bytes expected, got {x.numel() * x.element_size()}")
+    if x is not None and type(x) is not int and x.nbytes < cfg.pool_bytes:
+        raise ValueError(f"{what}: {cfg.pool_bytes} bytes expected, got {x.nbytes}")
     return _ptr(x)
 
 
@@ -448,7 +479,7 @@ def locks_kv_decode(cfg: LocksKvConfig, q, k_pool, v_pool, block_table, seq_lens
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
     """Attention of one new token per sequence over the quantised pools: every page, or the
     pages listed in `selected` (int32 [batch][H_kv][k]), and with `window` the last positions."""
-    wsb = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
     rows = (cfg.batch, cfg.n_q_heads, cfg.head_dim)
     k = 0 if selected is None else selected.shape[-1]
     rc = load_library().locks_kv_decode(
