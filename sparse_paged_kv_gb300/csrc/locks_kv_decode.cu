@@ -473,6 +473,24 @@ __device__ __forceinline__ Seq seq_of(const KvDecodeParams& p, int b) {
   return s;
 }
 
+// Outputs of the sequences with nothing to attend, this block's share of them (one warp).
+__device__ __forceinline__ void zero_empty(const KvDecodeParams& p, int lane) {
+  const size_t rows = size_t(p.n_kv_heads) * p.group;
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (seq_of(p, b).stages > 0) continue;
+    const size_t row0 = b * rows;
+    for (size_t i = lane; i < rows * (kHeadDim / 8); i += 32)
+      reinterpret_cast<uint4*>(p.out + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+    if (p.out_lse)
+      for (size_t i = lane; i < rows; i += 32) p.out_lse[row0 + i] = -INFINITY;
+  }
+}
+
+// x / n; n is nearly always the number of blocks, and a constant divides faster
+__device__ __forceinline__ int64_t div_blocks(int64_t x, int n) {
+  return n == kSms ? int64_t(uint64_t(x) / kSms) : x / n;
+}
+
 // The unit after (b, h), which starts at u in the list.
 __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& sq, int& h, int& u,
                                           int end) {
@@ -487,11 +505,9 @@ __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& 
 // 32t + 31): brought to a largest magnitude in [2^14, 2^15) by a power of two,
 // rounded to f16 (exact but for elements below 2^-28 of it) and laid out as the
 // second operand of the eight k-steps.
-template <int FMT>
-__device__ __forceinline__ void put_query(const KvDecodeParams& p, int unit, int h0, int lane,
-                                          uint4 (*to)[32], float* scale) {
+__device__ __forceinline__ void load_query(const KvDecodeParams& p, int unit, int h0, int lane,
+                                           uint4 (&raw)[4]) {
   const int head = h0 + (lane >> 2), t = lane & 3;
-  uint4 raw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
@@ -499,6 +515,11 @@ __device__ __forceinline__ void put_query(const KvDecodeParams& p, int unit, int
       raw[i] = *reinterpret_cast<const uint4*>(p.q + (size_t(unit) * p.group + head) * kHeadDim +
                                                32 * t + 8 * i);
   }
+}
+template <int FMT>
+__device__ __forceinline__ void put_query(const uint4 (&raw)[4], int h0, int lane, uint4 (*to)[32],
+                                          float* scale) {
+  const int head = h0 + (lane >> 2), t = lane & 3;
   uint32_t mx = 0;                                // largest magnitude, as bf16 bits
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -526,24 +547,10 @@ __device__ __forceinline__ void put_query(const KvDecodeParams& p, int unit, int
   }
 }
 
-// A warp's state for heads 8n .. 8n + 7 into shared memory: float4 x of a lane
-// is head parity x / 4, dims 4 (x % 4) .. + 3 of its 16.
-template <int NT>
-__device__ __forceinline__ void put_state(const State<NT>& st, int n, float4* to, float* m, float* l,
-                                          int g, int t) {
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    const int i = 2 * (x & 3), e = x >> 2;
-    to[x * 32] = make_float4(st.acc[n][i][e], st.acc[n][i][2 + e], st.acc[n][i + 1][e],
-                             st.acc[n][i + 1][2 + e]);
-  }
-  if (g == 0) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m[8 * n + 2 * t + e] = st.m[2 * n + e];
-      l[8 * n + 2 * t + e] = st.l[2 * n + e];
-    }
-  }
+__device__ __forceinline__ int ticket_add(int* t) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(t) : "memory");
+  return old;
 }
 
 // Two dims of an output row from sum p v, the reference and sum p.
@@ -553,6 +560,42 @@ __device__ __forceinline__ void store_out(const KvDecodeParams& p, size_t row, i
   *reinterpret_cast<__nv_bfloat162*>(p.out + row * kHeadDim + dim) =
       __floats2bfloat162_rn(A.x * inv, A.y * inv);
   if (p.out_lse && dim == 0) p.out_lse[row] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
+}
+
+// The partials of blocks c_lo .. c_hi of a unit, in that order, K loaded at a
+// time: item x (two dims of a head) of each.  The unit starts in block c_lo,
+// whose second partial it is; in the others it is the first.
+template <int NT, int K>
+__device__ __forceinline__ void join_partials(const float* parts, int c_lo, int c_hi, int head, int x,
+                                              float2& A, float& M, float& L) {
+  for (int c = c_lo; c <= c_hi; c += K) {
+    float2 ml[K], a[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      ml[k] = make_float2(kNone, 0.f);
+      a[k] = make_float2(0.f, 0.f);
+      if (c + k <= c_hi) {
+        const float* src = parts + (size_t(c + k) * 2 + (c + k == c_lo)) * (kv_part_bytes(NT) / 4);
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(src + NT * 1024 + 2 * head));
+        a[k] = __ldcg(reinterpret_cast<const float2*>(src) + x);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int k = 0; k < K; ++k) Mn = fmaxf(Mn, ml[k].x);
+    const float f0 = ex2_approx(M - Mn);
+    L *= f0;
+    A.x *= f0;
+    A.y *= f0;
+    M = Mn;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float f = ex2_approx(ml[k].x - Mn);
+      L += ml[k].y * f;
+      A.x += a[k].x * f;
+      A.y += a[k].y * f;
+    }
+  }
 }
 
 template <int FMT, int NT>
@@ -572,8 +615,9 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
   __shared__ uint4 s_q[2][NT][4][32];
   __shared__ float s_qs[2][8 * NT];
   __shared__ uint64_t s_qfull[2], s_qempty[2];
-  __shared__ float s_m[kKvWarps][8 * NT], s_l[kKvWarps][8 * NT];
-  __shared__ int s_scan[kKvThreads / 32], s_base, s_first, s_last;
+  __shared__ __align__(16) float s_m[kKvWarps][8 * NT], s_l[kKvWarps][8 * NT];   // of each warp's state
+  __shared__ float s_ref[8 * NT];                 // their largest m
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.page_size, pps = kStageTok / B, hk = p.n_kv_heads;
@@ -588,70 +632,52 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
     mbar_fence_init();
   }
+  if (tid < 4) {
+    const int e = 16 * tid / B, r0 = 16 * tid - e * B;
+    s_chunk[tid] = make_uint2(e * uint32_t(kv_rec_bytes(FMT, B)) + r0 * kv_row_bytes(FMT),
+                              e * uint32_t(kv_rec_bytes(FMT, B)) + 4 * r0);
+  }
+  __syncthreads();
   griddep_launch();
   griddep_wait();
 
-  // ---- this block's share of the stages of all units ----
-  const int per = (p.batch + kKvThreads - 1) / kKvThreads;
-  const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
+  // ---- this block's share of the units' cost, which every warp works out for itself ----
+  const int per = (p.batch + 31) / 32;
+  const int b_lo = min(p.batch, lane * per), b_hi = min(p.batch, b_lo + per);
   int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    mine += seq_of(p, b).cost();
-    if (blockIdx.x == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.max_pages * B))
-      flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
-  }
+#pragma unroll 4
+  for (int i = b_lo; i < b_hi; ++i) mine += seq_of(p, i).cost();
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kKvThreads / 32; ++w) {
-    if (w == warp) incl += total;
-    total += s_scan[w];
-  }
-  const int W = total * hk;                       // cost of all units; below 2^31: the host has checked
+  const int W = __shfl_sync(kFull, incl, 31) * hk; // below 2^31: the host has checked
   const int N = min(int(gridDim.x), max(W, 1));
-  const int w_lo = int(blockIdx.x) < N ? int(int64_t(W) * blockIdx.x / N) : 0;
-  const int w_hi = int(blockIdx.x) < N ? int(int64_t(W) * (blockIdx.x + 1) / N) : 0;
-  if (w_lo < w_hi && (incl - mine) * hk <= w_lo && w_lo < incl * hk) {
-    int at = (incl - mine) * hk;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int n = seq_of(p, b).cost() * hk;
-      if (w_lo - at < n) {
-        s_first = b;
-        s_base = at;
-        break;
-      }
-      at += n;
-    }
+  const int w_lo = int(blockIdx.x) < N ? int(div_blocks(int64_t(W) * blockIdx.x, N)) : 0;
+  const int w_hi = int(blockIdx.x) < N ? int(div_blocks(int64_t(W) * (blockIdx.x + 1), N)) : 0;
+  int b = b_lo, u = (incl - mine) * hk;           // the sequence of w_lo and where it starts in the list
+  const bool here = u <= w_lo && w_lo < incl * hk;
+  if (here) {
+    for (int c; u + (c = seq_of(p, b).cost() * hk) <= w_lo; ++b) u += c;
   }
-  // sequences with nothing to attend: their outputs are written here
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (seq_of(p, b).stages > 0) continue;
-    const size_t rows = size_t(hk) * p.group, row0 = size_t(b) * rows;
-    for (size_t i = tid; i < rows * (kHeadDim / 8); i += kKvThreads)
-      reinterpret_cast<uint4*>(p.out + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
-    if (p.out_lse)
-      for (size_t i = tid; i < rows; i += kKvThreads) p.out_lse[row0 + i] = -INFINITY;
+  const int who = __ffs(__ballot_sync(kFull, here)) - 1;
+  b = __shfl_sync(kFull, b, max(who, 0));
+  u = __shfl_sync(kFull, u, max(who, 0));
+  if (blockIdx.x == 0 && warp == 0)
+    for (int i = b_lo; i < b_hi; ++i)
+      if (p.seq_lens[i] < 0 || p.seq_lens[i] > p.max_pages * B) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
+  if (w_lo >= w_hi) {
+    if (warp == 0) zero_empty(p, lane);
+    return;
   }
-  __syncthreads();
-  if (w_lo >= w_hi) return;
 
   const size_t rec = size_t(kv_rec_bytes(FMT, B));
-  int b = s_first;
   Seq sq = seq_of(p, b);
-  int h = (w_lo - s_base) / sq.cost();
-  int u = s_base + h * sq.cost();                 // where unit (b, h) starts in the list
+  int h = (w_lo - u) / sq.cost();
+  u += h * sq.cost();                             // where unit (b, h) starts in the list
   int it = 0;                                     // stages of this block so far
-  if (tid < 4) {                                  // (one barrier before its first use is below)
-    const int e = 16 * tid / B, r0 = 16 * tid - e * B;
-    s_chunk[tid] = make_uint2(e * uint32_t(rec) + r0 * kv_row_bytes(FMT), e * uint32_t(rec) + 4 * r0);
-  }
 
   if (warp >= kKvWarps) {
     // ---------------- producer ----------------
@@ -668,16 +694,23 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
       const int i0 = max(0, w_lo - u - kUnitCost);
       const int cnt = min(sq.stages, w_hi - u - kUnitCost) - i0;
       if (cnt <= 0) continue;
-      if (pw >= 4 - NT) {                         // the last warps bring the unit's query
+      // the last warps also bring the unit's query, whose loads are on their way
+      // while the first pages are looked up
+      bool bring = pw >= 4 - NT;
+      uint4 raw[4];
+      if (bring) load_query(p, b * hk + h, 8 * (pw - (4 - NT)), lane, raw);
+      const auto bring_query = [&] {
         const int n = pw - (4 - NT);
+        bring = false;
         if (!__all_sync(kFull, mbar_wait_bounded(s_qempty + (seg & 1), ((seg >> 1) & 1) ^ 1))) {
           if (lane == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
-          break;
+          ok = false;
+          return;
         }
-        put_query<FMT>(p, b * hk + h, 8 * n, lane, s_q[seg & 1][n], s_qs[seg & 1]);
+        put_query<FMT>(raw, 8 * n, lane, s_q[seg & 1][n], s_qs[seg & 1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(s_qfull + (seg & 1));
-      }
+      };
       const int32_t* row = p.block_table + size_t(b) * p.max_pages;
       const int32_t* sel = p.selected ? p.selected + (size_t(b) * hk + h) * p.k : nullptr;
       const int pages = (sq.n + B - 1) / B;
@@ -713,6 +746,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
         for (int c = 0; c < 4; ++c)
           range[c] = min(16, max(0, r_lo - 16 * c)) | (min(16, max(0, r_hi - 16 * c)) << 8);
         const unsigned live = __ballot_sync(kFull, blk >= 0);
+        if (bring) bring_query();
         const int todo = min(looked, (cnt - s0 + 3) / 4);
         for (int x = 0; x < todo; ++x) {
           if (!mbar_wait_bounded(s_empty + s, phase)) ok = false;
@@ -749,9 +783,11 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
           }
         }
       }
+      if (bring) bring_query();                   // (no stage of the segment was this warp's)
       it += cnt;
       ++seg;
     }
+    if (pw == 0) zero_empty(p, lane);
     return;
   }
 
@@ -832,24 +868,41 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
     int* tickets = reinterpret_cast<int*>(p.ws);
     float* part = parts + (size_t(blockIdx.x) * 2 + slot) * (kv_part_bytes(NT) / 4);
-    // a warp's state from here on: m, l over its tokens, acc = sum p v (this lane's dims)
-#pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) st.l[j] += __shfl_xor_sync(kFull, st.l[j], o);
-      const float f = st.f[j] > 0.f ? (FMT == LOCKS_KV_I4 ? 256.f : 1.f) / st.f[j] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        st.acc[j >> 1][i][j & 1] *= f;
-        st.acc[j >> 1][i][2 + (j & 1)] *= f;
-      }
-    }
     if (lane == 0) mbar_arrive(s_qempty + (seg & 1));
-    consumers_sync<NT>();                         // the buffer's last readers are done
+    // every warp brings its sums to the block's reference M, then they are added up item by item
+    if (g == 0) {
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) s_m[warp][8 * (j >> 1) + 2 * t + (j & 1)] = st.m[j];
+    }
+    consumers_sync<NT>();                         // (and the buffer's last readers are done)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (n) consumers_sync<NT>();
-      put_state<NT>(st, n, mbuf + warp * 256 + lane, s_m[warp], s_l[warp], g, t);
+      float2 M = make_float2(kNone, kNone);
+#pragma unroll
+      for (int w = 0; w < kKvWarps; ++w) {
+        const float2 m = *reinterpret_cast<const float2*>(&s_m[w][8 * n + 2 * t]);
+        M.x = fmaxf(M.x, m.x);
+        M.y = fmaxf(M.y, m.y);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * n + e;
+        const float a = ex2_approx(st.m[j] - (e ? M.y : M.x));
+        const float f = st.f[j] > 0.f ? a * (FMT == LOCKS_KV_I4 ? 256.f : 1.f) / st.f[j] : 0.f;
+        float l = st.l[j] * a;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+        if (g == 0) {
+          s_l[warp][8 * n + 2 * t + e] = l;
+          if (warp == 0) s_ref[8 * n + 2 * t + e] = e ? M.y : M.x;
+        }
+        // float4 x of a lane: head parity e = x / 4, dims 4 (x % 4) .. + 3 of its 16
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mbuf[warp * 256 + (4 * e + x) * 32 + lane] =
+              make_float4(st.acc[n][2 * x][e] * f, st.acc[n][2 * x][2 + e] * f,
+                          st.acc[n][2 * x + 1][e] * f, st.acc[n][2 * x + 1][2 + e] * f);
+      }
       consumers_sync<NT>();
       // a thread's items: float2 pairs of the 1024 floats, as the lanes laid them out
 #pragma unroll
@@ -857,17 +910,15 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
         const int x = i * kKvWarps * 32 + tid, q4 = x >> 6, l2 = (x >> 1) & 31;
         const int head = 8 * n + 2 * (l2 & 3) + (q4 >> 2);
         const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
-        float M = kNone, L = 0.f;
+        const float M = s_ref[head];
+        float L = 0.f;
         float2 A = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, s_m[w][head]);
-#pragma unroll
         for (int w = 0; w < kKvWarps; ++w) {
-          const float f = ex2_approx(s_m[w][head] - M);
           const float2 a = reinterpret_cast<const float2*>(mbuf + w * 256)[x];
-          L += s_l[w][head] * f;
-          A.x += a.x * f;
-          A.y += a.y * f;
+          L += s_l[w][head];
+          A.x += a.x;
+          A.y += a.y;
         }
         if (alone) {
           if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
@@ -876,14 +927,14 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
           if (dim == 0) *reinterpret_cast<float2*>(part + NT * 1024 + 2 * head) = make_float2(M, L);
         }
       }
+      if (n + 1 < NT) consumers_sync<NT>();
     }
     if (!alone) {
-      __threadfence();
       consumers_sync<NT>();
-      if (tid == 0) s_last = atomicAdd(tickets + unit, 1) == c_hi - c_lo;
+      // releases this block's partial (ordered before by the barrier), acquires the others'
+      if (tid == 0) s_last = ticket_add(tickets + unit) == c_hi - c_lo;
       consumers_sync<NT>();
       if (s_last) {
-        __threadfence();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -893,34 +944,9 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
             const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
             float M = kNone, L = 0.f;
             float2 A = make_float2(0.f, 0.f);
-            for (int c = c_lo; c <= c_hi; c += 8) {
-              float2 ml[8], a[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                ml[k] = make_float2(kNone, 0.f);
-                a[k] = make_float2(0.f, 0.f);
-                if (c + k <= c_hi) {
-                  const float* src = parts + (size_t(c + k) * 2 + (c + k == c_lo)) * (kv_part_bytes(NT) / 4);
-                  ml[k] = __ldcg(reinterpret_cast<const float2*>(src + NT * 1024 + 2 * head));
-                  a[k] = __ldcg(reinterpret_cast<const float2*>(src) + n * 512 + x);
-                }
-              }
-              float Mn = M;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, ml[k].x);
-              const float f0 = ex2_approx(M - Mn);
-              L *= f0;
-              A.x *= f0;
-              A.y *= f0;
-              M = Mn;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float f = ex2_approx(ml[k].x - Mn);
-                L += ml[k].y * f;
-                A.x += a[k].x * f;
-                A.y += a[k].y * f;
-              }
-            }
+            // (a unit cut in two or three is the usual case, one cut in many the latency-bound one)
+            if (c_hi - c_lo < 4) join_partials<NT, 4>(parts, c_lo, c_hi, head, n * 512 + x, A, M, L);
+            else join_partials<NT, 16>(parts, c_lo, c_hi, head, n * 512 + x, A, M, L);
             if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
           }
         if (tid == 0) tickets[unit] = 0;
