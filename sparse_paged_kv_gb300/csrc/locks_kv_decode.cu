@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
   __shared__ uint64_t s_qfull[2], s_qempty[2];
   __shared__ __align__(16) float s_m[kKvWarps][8 * NT], s_l[kKvWarps][8 * NT];   // of each warp's state
   __shared__ float s_ref[8 * NT];                 // their largest m
-  __shared__ int s_last;
+  __shared__ int2 s_join;                         // blocks whose partials this block merges
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.page_size, pps = kStageTok / B, hk = p.n_kv_heads;
@@ -860,14 +860,11 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
 
     // ---- merge the warps' states; finish the unit or leave a partial ----
-    // the blocks of the unit's first and last stage
-    const int u_lo = u + kUnitCost, u_hi = u_lo + sq.stages;
-    const int c_lo = int((int64_t(u_lo + 1) * N - 1) / W), c_hi = int((int64_t(u_hi) * N - 1) / W);
-    const bool alone = c_lo == c_hi;
-    const int slot = int(blockIdx.x) == c_lo ? 1 : 0;
+    const int u_lo = u + kUnitCost, u_hi = u_lo + sq.stages;     // its stages in the list
+    const bool alone = u_lo >= w_lo && u_hi <= w_hi;
     float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
-    int* tickets = reinterpret_cast<int*>(p.ws);
-    float* part = parts + (size_t(blockIdx.x) * 2 + slot) * (kv_part_bytes(NT) / 4);
+    // a block's first partial goes on with an earlier block's unit, its second begins one
+    float* part = parts + (size_t(blockIdx.x) * 2 + (u_lo >= w_lo)) * (kv_part_bytes(NT) / 4);
     if (lane == 0) mbar_arrive(s_qempty + (seg & 1));
     // every warp brings its sums to the block's reference M, then they are added up item by item
     if (g == 0) {
@@ -888,7 +885,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
       for (int e = 0; e < 2; ++e) {
         const int j = 2 * n + e;
         const float a = ex2_approx(st.m[j] - (e ? M.y : M.x));
-        const float f = st.f[j] > 0.f ? a * (FMT == LOCKS_KV_I4 ? 256.f : 1.f) / st.f[j] : 0.f;
+        const float f = st.f[j] > 0.f ? __fdividef(a * (FMT == LOCKS_KV_I4 ? 256.f : 1.f), st.f[j]) : 0.f;
         float l = st.l[j] * a;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
@@ -931,10 +928,17 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
     if (!alone) {
       consumers_sync<NT>();
-      // releases this block's partial (ordered before by the barrier), acquires the others'
-      if (tid == 0) s_last = ticket_add(tickets + unit) == c_hi - c_lo;
+      int* ticket = reinterpret_cast<int*>(p.ws) + unit;
+      if (tid == 0) {
+        // releases this block's partial (ordered before by the barrier), acquires the others'
+        const int before = ticket_add(ticket);
+        // the blocks of the unit's first and last stage
+        const int c_lo = int((int64_t(u_lo + 1) * N - 1) / W), c_hi = int((int64_t(u_hi) * N - 1) / W);
+        s_join = before == c_hi - c_lo ? make_int2(c_lo, c_hi) : make_int2(0, -1);
+      }
       consumers_sync<NT>();
-      if (s_last) {
+      const int c_lo = s_join.x, c_hi = s_join.y;
+      if (c_hi >= 0) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -949,7 +953,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
             else join_partials<NT, 16>(parts, c_lo, c_hi, head, n * 512 + x, A, M, L);
             if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
           }
-        if (tid == 0) tickets[unit] = 0;
+        if (tid == 0) *ticket = 0;
       }
     }
     ++seg;
