@@ -3,6 +3,8 @@
 // floats.  Internal to the library; the record is described in locks.h.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -84,6 +86,22 @@ int launch_kv_write(KvWriteParams p, int fmt, cudaStream_t stream);
 int launch_kv_read(const KvReadParams& p, int fmt, cudaStream_t stream);
 size_t kv_decode_workspace(int batch, int n_kv_heads, int group);
 int launch_kv_decode(const KvDecodeParams& p, int fmt, cudaStream_t stream);
+
+// A kernel attribute holds for the device it was set on: `run` calls set() on
+// the first launch there (and again after a failure).
+struct LaunchOnce {
+  std::atomic<uint64_t> ready{0};
+  template <typename F>
+  bool run(F set) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (ready.load(std::memory_order_acquire) & bit) return true;
+    if (!set()) return false;
+    ready.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+};
 
 // Launches with the programmatic-serialization attribute: the kernel may start
 // while the one before it on the stream drains, and waits (griddep_wait) before

@@ -35,8 +35,6 @@
 // Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 310 us (7.1 TB/s), 8 x
 // 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 122 us (4.95 TB/s): instructions,
 // of which the unpacking of codes is over half.
-#include <atomic>
-
 #include "locks_kv.cuh"
 
 namespace locks {
@@ -966,17 +964,12 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
 template <int FMT, int NT>
 int launch_nt(const KvDecodeParams& p, cudaStream_t stream) {
   constexpr size_t smem = size_t(kv_stages(FMT)) * kv_stage_bytes(FMT) + kv_merge_bytes(NT);
-  // the attribute holds for the device it was set on: set at its first launch there
-  static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return LOCKS_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(kv_decode_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem)) != cudaSuccess)
-      return LOCKS_ERR_CUDA;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
+  static LaunchOnce once;
+  if (!once.run([] {
+        return cudaFuncSetAttribute(kv_decode_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(smem)) == cudaSuccess;
+      }))
+    return LOCKS_ERR_CUDA;
   return launch_dependent(kv_decode_kernel<FMT, NT>, dim3(kSms), kv_threads(NT), smem, p, stream);
 }
 

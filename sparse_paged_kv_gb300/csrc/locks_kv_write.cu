@@ -7,11 +7,12 @@
 // 64-byte) line.
 //
 // Write: a block takes a few tokens and a run of their rows (queries, then keys,
-// then values), computes the tokens' cos and sin once, one pair a thread, into
-// shared memory, and its half-warps take a row each, the loads of several rows
-// ahead of their arithmetic.  In the half layout a lane's partner elements (dims
-// +- r/2) belong to another lane; it loads them itself (they are in L1 already),
-// which keeps every lane's 8 dims contiguous for the codes.
+// then values).  One thread asks for all of them (cp.async.bulk: a token's heads
+// are contiguous), so that 50 KB a block are on their way at once and no register
+// waits for them; meanwhile the tokens' cos and sin are computed once, one pair a
+// thread.  Then every half-warp takes rows in turn; in the half layout it reads a
+// lane's partner elements (dims +- r/2) from shared memory a second time, which
+// keeps every lane's 8 dims contiguous for the codes.
 #include "locks_kv.cuh"
 
 namespace locks {
@@ -20,6 +21,7 @@ namespace {
 
 constexpr int kWriteThreads = 256;
 constexpr int kHalfWarps = kWriteThreads / 16;
+constexpr int kMaxWriteSmem = 52 * 1024;              // of rows a block: four blocks an SM
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x);
@@ -157,22 +159,6 @@ __device__ __forceinline__ int partner_dim(int rot, int e0) {
   return LAYOUT != kHalf || e0 >= rot ? e0 : (e0 >= rot / 2 ? e0 - rot / 2 : e0 + rot / 2);
 }
 
-// N rows of 128 dims, STEP apart from `row` on, those before `end`: this lane's
-// 8 dims and their partners
-template <int LAYOUT, int N, int STEP>
-__device__ __forceinline__ void load_rows(const __nv_bfloat16* src, int row, int end, int e0,
-                                          int partner, uint4 (&own)[N], uint4 (&other)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    own[i] = other[i] = make_uint4(0, 0, 0, 0);
-    if (row + STEP * i < end) {
-      const __nv_bfloat16* at = src + (row + STEP * i) * kHeadDim;
-      own[i] = *reinterpret_cast<const uint4*>(at + e0);
-      if (LAYOUT == kHalf) other[i] = *reinterpret_cast<const uint4*>(at + partner);
-    }
-  }
-}
-
 // own and other: this lane's 8 elements and (half layout) their partners
 template <int LAYOUT>
 __device__ __forceinline__ void rotate8(float (&x)[8], const uint4& own, const uint4& other,
@@ -202,32 +188,48 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const uint4& own, const u
   }
 }
 
-constexpr int kAhead = 3;                             // rows a half-warp loads at a time
 constexpr int kWriteWarps = kWriteThreads / 32;
+constexpr int kRowBytes = kHeadDim * 2;
 
 // TOKENS tokens a block: 8 / TOKENS warps a token
 template <int FMT, int LAYOUT, int TOKENS>
 __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWriteParams p) {
+  extern __shared__ __align__(128) unsigned char rows_in[];   // [TOKENS][run][128] bf16
   __shared__ float2 table[TOKENS][kHeadDim / 2 + 1];
+  __shared__ uint64_t landed;
   constexpr int kPer = kWriteWarps / TOKENS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l16 = lane & 15, hw = 2 * (warp % kPer) + (lane >> 4), e0 = 8 * l16;   // hw: this half-warp of the token's
   const int group = blockIdx.x / p.n_chunks, chunk = blockIdx.x % p.n_chunks;
-  griddep_launch();
-  griddep_wait();
-  const int rot = p.rope.rotary_dim;
-  const int token = group * TOKENS + warp / kPer;
-  // this block's run of the token's rows; a half-warp takes every (2 kPer)-th
-  constexpr int kStep = 2 * kPer;
+  // this block's run of each token's rows
   const int hq = p.q_out ? p.n_q_heads : 0, hk = p.n_kv_heads;
   const int rows = hq + 2 * hk;
-  const int lo = rows * chunk / p.n_chunks, hi = rows * (chunk + 1) / p.n_chunks;
-  // the first queries are on their way while the angles are computed
-  const int q_end = token < p.n_tokens ? min(hi, hq) : 0;
-  const int partner = partner_dim<LAYOUT>(rot, e0);
-  const __nv_bfloat16* q_src = p.q_new + int64_t(token) * p.q_stride;
-  uint4 own[kAhead], other[kAhead];
-  load_rows<LAYOUT, kAhead, kStep>(q_src, lo + hw, q_end, e0, partner, own, other);
+  const int lo = rows * chunk / p.n_chunks, hi = rows * (chunk + 1) / p.n_chunks, run = hi - lo;
+  if (threadIdx.x == 0) {
+    mbar_init(&landed, 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  griddep_launch();
+  griddep_wait();
+  if (threadIdx.x == 0) {
+    const int n = min(TOKENS, p.n_tokens - group * TOKENS);
+    mbar_arrive_expect_tx(&landed, uint32_t(n * run * kRowBytes));
+    for (int t = 0; t < n; ++t) {
+      const int64_t token = group * TOKENS + t;
+      unsigned char* to = rows_in + t * run * kRowBytes;
+      const int q_end = min(hi, hq), k_lo = max(lo, hq), k_end = min(hi, hq + hk), v_lo = max(lo, hq + hk);
+      if (lo < q_end)
+        bulk_g2s(to, p.q_new + token * p.q_stride + lo * kHeadDim, (q_end - lo) * kRowBytes, &landed);
+      if (k_lo < k_end)
+        bulk_g2s(to + (k_lo - lo) * kRowBytes, p.k_new + token * p.k_stride + (k_lo - hq) * kHeadDim,
+                 (k_end - k_lo) * kRowBytes, &landed);
+      if (v_lo < hi)
+        bulk_g2s(to + (v_lo - lo) * kRowBytes, p.v_new + token * p.v_stride + (v_lo - hq - hk) * kHeadDim,
+                 (hi - v_lo) * kRowBytes, &landed);
+    }
+  }
+  const int rot = p.rope.rotary_dim;
   if constexpr (LAYOUT != kNoTurn) {
     for (int i = threadIdx.x; i < TOKENS * (kHeadDim / 2); i += kWriteThreads) {
       const int t = i / (kHeadDim / 2), pair = i % (kHeadDim / 2), tok = group * TOKENS + t;
@@ -238,12 +240,12 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
       }
     }
   }
-  if (LAYOUT != kNoTurn) __syncthreads();
-  if (token >= p.n_tokens) return;                    // (whole warps)
-  const int seq = p.token_seq ? p.token_seq[token] : token;
-  const int pos = p.token_pos[token];
+  const int token = group * TOKENS + warp / kPer;
+  const bool exists = token < p.n_tokens;
+  const int seq = !exists ? -1 : (p.token_seq ? p.token_seq[token] : token);
+  const int pos = exists ? p.token_pos[token] : 0;
   const int B = p.page_size, shift = __ffs(B) - 1;    // B is a power of two
-  const bool first = chunk == 0 && hw == 0 && l16 == 0;
+  const bool first = exists && chunk == 0 && hw == 0 && l16 == 0;
   int blk = -1;
   if (seq >= 0) {
     int32_t bits = 0;
@@ -265,62 +267,52 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
   }
   const int slot = pos & (B - 1);
   if (first && p.completed) p.completed[token] = (blk >= 0 && slot == B - 1) ? blk : -1;
-  if (seq < 0) return;
 
+  // every thread waits (no block may end before its copies have landed)
+  const bool here = mbar_wait_bounded(&landed, 0);
+  if (__syncthreads_or(!here)) {
+    if (threadIdx.x == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
+    return;
+  }
+  if (seq < 0) return;                                // (whole warps)
+  constexpr int kStep = 2 * kPer;                     // a half-warp takes every kStep-th row
   const Turn turn = make_turn<LAYOUT>(table[warp / kPer], rot, e0);
+  const unsigned char* mine = rows_in + (warp / kPer) * run * kRowBytes + e0 * 2;
+  const int away = 2 * (partner_dim<LAYOUT>(rot, e0) - e0);   // bytes to the partner elements
 
   // queries
   {
     __nv_bfloat16* dst = p.q_out + int64_t(token) * hq * kHeadDim + e0;
-    for (int r = lo; r < q_end; r += kStep * kAhead) {
-      if (r > lo) load_rows<LAYOUT, kAhead, kStep>(q_src, r + hw, q_end, e0, partner, own, other);
-      __syncwarp();                                   // q_out may be q_new: a row's loads, then its stores
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int row = r + kStep * i + hw;
-        if (row < q_end) {
-          float x[8];
-          rotate8<LAYOUT>(x, own[i], other[i], turn);
-          *reinterpret_cast<uint4*>(dst + row * kHeadDim) = pack8(x);
-        }
-      }
+    const int end = min(hi, hq);
+#pragma unroll 4
+    for (int r = lo + hw; r < end; r += kStep) {
+      const unsigned char* at = mine + (r - lo) * kRowBytes;
+      float x[8];
+      rotate8<LAYOUT>(x, *reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + away), turn);
+      *reinterpret_cast<uint4*>(dst + r * kHeadDim) = pack8(x);
     }
   }
   if (blk < 0) return;
-  // keys, then values (the shuffles of store_row name every lane: rows past the end are not stored)
+  // keys, then values (the shuffles of store_row name every lane: a row past the end is not stored)
   const size_t rec_bytes = size_t(kv_rec_bytes(FMT, B));
   {
-    const __nv_bfloat16* src = p.k_new + int64_t(token) * p.k_stride;
     unsigned char* dst = p.k_pool + size_t(blk) * hk * rec_bytes;
-    const int end = min(hi, hq + hk) - hq;
-    for (int r = max(lo - hq, 0); r < end; r += 2 * kStep) {
-      uint4 own[2], other[2];
-      load_rows<LAYOUT, 2, kStep>(src, r + hw, end, e0, partner, own, other);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = r + kStep * i + hw;
-        if (r + kStep * i + (hw & ~1) >= end) break;  // neither half of the warp has a row
-        float x[8];
-        rotate8<LAYOUT>(x, own[i], other[i], turn);
-        store_row<FMT>(x, dst + (h < end ? h : 0) * rec_bytes, slot, B, l16, h < end);
-      }
+    const int end = min(hi, hq + hk);
+#pragma unroll 2
+    for (int r = max(lo, hq) + hw; r - (hw & 1) < end; r += kStep) {
+      const unsigned char* at = mine + (min(r, end - 1) - lo) * kRowBytes;
+      float x[8];
+      rotate8<LAYOUT>(x, *reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + away), turn);
+      store_row<FMT>(x, dst + (min(r, end - 1) - hq) * rec_bytes, slot, B, l16, r < end);
     }
   }
   {
-    const __nv_bfloat16* src = p.v_new + int64_t(token) * p.v_stride;
     unsigned char* dst = p.v_pool + size_t(blk) * hk * rec_bytes;
-    const int end = hi - hq - hk;
-    for (int r = max(lo - hq - hk, 0); r < end; r += 2 * kStep) {
-      uint4 own[2], other[2];
-      load_rows<kNoTurn, 2, kStep>(src, r + hw, end, e0, e0, own, other);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = r + kStep * i + hw;
-        if (r + kStep * i + (hw & ~1) >= end) break;
-        float x[8];
-        unpack8(own[i], x);
-        store_row<FMT>(x, dst + (h < end ? h : 0) * rec_bytes, slot, B, l16, h < end);
-      }
+#pragma unroll 2
+    for (int r = max(lo, hq + hk) + hw; r - (hw & 1) < hi; r += kStep) {
+      float x[8];
+      unpack8(*reinterpret_cast<const uint4*>(mine + (min(r, hi - 1) - lo) * kRowBytes), x);
+      store_row<FMT>(x, dst + (min(r, hi - 1) - hq - hk) * rec_bytes, slot, B, l16, r < hi);
     }
   }
 }
@@ -396,22 +388,32 @@ __global__ void __launch_bounds__(kWriteThreads) kv_read_kernel(const KvReadPara
 }
 
 template <int FMT, int LAYOUT, int TOKENS>
-int launch_write_tokens(KvWriteParams p, int chunks, cudaStream_t stream) {
+int launch_write_tokens(KvWriteParams p, int rows, int chunks, cudaStream_t stream) {
   p.n_chunks = chunks;
   const int64_t blocks = (int64_t(p.n_tokens) + TOKENS - 1) / TOKENS * chunks;
   if (blocks > 0x7fffffff) return LOCKS_ERR_UNSUPPORTED;
-  return launch_dependent(kv_write_kernel<FMT, LAYOUT, TOKENS>, dim3(unsigned(blocks)), kWriteThreads,
-                          0, p, stream);
+  const size_t smem = size_t(TOKENS) * ((rows + chunks - 1) / chunks) * kRowBytes;
+  // above 48 KB a kernel has to be told, once a device
+  auto kern = kv_write_kernel<FMT, LAYOUT, TOKENS>;
+  static LaunchOnce once;
+  if (!once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWriteSmem) ==
+               cudaSuccess;
+      }))
+    return LOCKS_ERR_CUDA;
+  return launch_dependent(kern, dim3(unsigned(blocks)), kWriteThreads, smem, p, stream);
 }
 
 template <int FMT, int LAYOUT>
 int launch_write_layout(const KvWriteParams& p, cudaStream_t stream) {
-  // Four tokens a block and all their rows when that gives every SM four blocks
-  // (a prompt); otherwise (a decode step) one token a block and its rows spread
-  // over blocks of a row per half-warp.
+  // A prompt: all rows of four tokens a block (or of as many as leave room for
+  // four blocks an SM), when that gives every SM four blocks.  A decode step:
+  // one token a block and its rows spread over blocks of a row per half-warp.
   const int rows = (p.q_out ? p.n_q_heads : 0) + 2 * p.n_kv_heads;
-  if (p.n_tokens >= 4 * 4 * 152) return launch_write_tokens<FMT, LAYOUT, 4>(p, 1, stream);
-  return launch_write_tokens<FMT, LAYOUT, 1>(p, (rows + kHalfWarps - 1) / kHalfWarps, stream);
+  const int fits = kMaxWriteSmem / (rows * kRowBytes);
+  if (p.n_tokens >= 4 * 4 * 152 && fits >= 4) return launch_write_tokens<FMT, LAYOUT, 4>(p, rows, 1, stream);
+  if (p.n_tokens >= 2 * 4 * 152 && fits >= 2) return launch_write_tokens<FMT, LAYOUT, 2>(p, rows, 1, stream);
+  return launch_write_tokens<FMT, LAYOUT, 1>(p, rows, (rows + kHalfWarps - 1) / kHalfWarps, stream);
 }
 
 template <int FMT>
