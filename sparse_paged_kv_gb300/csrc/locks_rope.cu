@@ -16,6 +16,7 @@ namespace locks {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int64_t kRopeStreamBytes = int64_t(64) << 20;   // read and written, half of L2
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
@@ -34,30 +35,41 @@ __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
 
-// N consecutive elements, N * sizeof(T) a multiple of 8 or one element
+// N consecutive elements, N * sizeof(T) a multiple of 8 or one element.  STREAM:
+// with the hint that the line is used once.
 template <typename T, int N>
 struct Pack {
   static constexpr int kBytes = N * int(sizeof(T));
   T e[N];
+  template <bool STREAM>
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (kBytes % 16 == 0) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4* at = reinterpret_cast<const uint4*>(p) + i;
+        reinterpret_cast<uint4*>(e)[i] = STREAM ? __ldcs(at) : *at;
+      }
     } else if constexpr (kBytes % 8 == 0) {
-      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+      const uint2* at = reinterpret_cast<const uint2*>(p);
+      *reinterpret_cast<uint2*>(e) = STREAM ? __ldcs(at) : *at;
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) e[i] = p[i];
     }
   }
+  template <bool STREAM>
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (kBytes % 16 == 0) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
+      for (int i = 0; i < kBytes / 16; ++i) {
+        uint4* at = reinterpret_cast<uint4*>(p) + i;
+        if (STREAM) __stcs(at, reinterpret_cast<const uint4*>(e)[i]);
+        else *at = reinterpret_cast<const uint4*>(e)[i];
+      }
     } else if constexpr (kBytes % 8 == 0) {
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+      uint2* at = reinterpret_cast<uint2*>(p);
+      if (STREAM) __stcs(at, *reinterpret_cast<const uint2*>(e));
+      else *at = *reinterpret_cast<const uint2*>(e);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i] = e[i];
@@ -65,7 +77,34 @@ struct Pack {
   }
 };
 
+// u and v in place: VEC pairs, in the half layout (u, v) element by element, in
+// the interleaved one neighbours
 template <typename T, int VEC>
+__device__ __forceinline__ void turn_pairs(Pack<T, VEC>& u, Pack<T, VEC>& v, const float (&c)[VEC],
+                                           const float (&s)[VEC], bool half) {
+  if (half || VEC == 1) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float fu = to_f(u.e[i]), fv = to_f(v.e[i]);
+      u.e[i] = from_f<T>(rope_u(fu, fv, c[i], s[i]));
+      v.e[i] = from_f<T>(rope_v(fu, fv, c[i], s[i]));
+    }
+  } else {
+    constexpr int kHalfVec = VEC / 2;
+#pragma unroll
+    for (int i = 0; i < kHalfVec; ++i) {
+      float fu = to_f(u.e[2 * i]), fv = to_f(u.e[2 * i + 1]);
+      u.e[2 * i] = from_f<T>(rope_u(fu, fv, c[i], s[i]));
+      u.e[2 * i + 1] = from_f<T>(rope_v(fu, fv, c[i], s[i]));
+      fu = to_f(v.e[2 * i]);
+      fv = to_f(v.e[2 * i + 1]);
+      v.e[2 * i] = from_f<T>(rope_u(fu, fv, c[kHalfVec + i], s[kHalfVec + i]));
+      v.e[2 * i + 1] = from_f<T>(rope_v(fu, fv, c[kHalfVec + i], s[kHalfVec + i]));
+    }
+  }
+}
+
+template <typename T, int VEC, bool STREAM>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   const int n = p.rope.rotary_dim / 2;
   const int items = n / VEC + (p.head_dim - 2 * n) / (2 * VEC);
@@ -102,38 +141,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const T* x = static_cast<const T*>(p.x) + token * p.x_ts;
   T* o = static_cast<T*>(p.out) + token * p.o_ts;
   const bool half = p.rope.layout == LOCKS_ROPE_HALF;
-#pragma unroll 2
-  for (int h = first; h < p.n_heads; h += p.n_chunks) {
-    alignas(16) Pack<T, VEC> u, v;
-    u.load(x + h * p.x_hs + a);
-    v.load(x + h * p.x_hs + b);
-    if (turn) {
-      if (half) {
+  constexpr int kAhead = STREAM ? 4 : 1;          // heads loaded before any is stored
+#pragma unroll 1
+  for (int h0 = first; h0 < p.n_heads; h0 += kAhead * p.n_chunks) {
+    alignas(16) Pack<T, VEC> u[kAhead], v[kAhead];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float fu = to_f(u.e[i]), fv = to_f(v.e[i]);
-          u.e[i] = from_f<T>(rope_u(fu, fv, c[i], s[i]));
-          v.e[i] = from_f<T>(rope_v(fu, fv, c[i], s[i]));
-        }
-      } else if constexpr (VEC > 1) {
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-          float fu = to_f(u.e[2 * i]), fv = to_f(u.e[2 * i + 1]);
-          u.e[2 * i] = from_f<T>(rope_u(fu, fv, c[i], s[i]));
-          u.e[2 * i + 1] = from_f<T>(rope_v(fu, fv, c[i], s[i]));
-          fu = to_f(v.e[2 * i]);
-          fv = to_f(v.e[2 * i + 1]);
-          v.e[2 * i] = from_f<T>(rope_u(fu, fv, c[i + VEC / 2], s[i + VEC / 2]));
-          v.e[2 * i + 1] = from_f<T>(rope_v(fu, fv, c[i + VEC / 2], s[i + VEC / 2]));
-        }
-      } else {
-        const float fu = to_f(u.e[0]), fv = to_f(v.e[0]);
-        u.e[0] = from_f<T>(rope_u(fu, fv, c[0], s[0]));
-        v.e[0] = from_f<T>(rope_v(fu, fv, c[0], s[0]));
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * p.n_chunks;
+      if (h < p.n_heads) {
+        u[i].template load<STREAM>(x + h * p.x_hs + a);
+        v[i].template load<STREAM>(x + h * p.x_hs + b);
       }
     }
-    u.store(o + h * p.o_hs + a);
-    v.store(o + h * p.o_hs + b);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * p.n_chunks;
+      if (h < p.n_heads) {
+        if (turn) turn_pairs(u[i], v[i], c, s, half);
+        u[i].template store<STREAM>(o + h * p.o_hs + a);
+        v[i].template store<STREAM>(o + h * p.o_hs + b);
+      }
+    }
   }
 }
 
@@ -150,7 +178,14 @@ int launch_rope_vec(RopeParams p, cudaStream_t stream) {
   p.n_chunks = int((p.n_heads + per - 1) / per);
   const int64_t blocks = (int64_t(p.n_tokens) * p.n_chunks + slots - 1) / slots;
   if (blocks > 0x7fffffff) return LOCKS_ERR_UNSUPPORTED;
-  return launch_dependent(rope_kernel<T, VEC>, dim3(unsigned(blocks)), kRopeThreads, 0, p, stream);
+  // Tensors too large to stay in L2: four heads in flight a thread, and every
+  // line marked as used once.  Smaller ones are left in L2 for the call that reads
+  // them next.  40 heads of 128 in bf16, us with and without: 32768 tokens 100.4,
+  // 104.7 (the copy rate is 99); 8192 28.3, 30.3; 4096 (84 MB) 15.9, 17.3; 2048
+  // (42 MB) 11.2, 10.8; 1024 9.0, 7.2.
+  const int64_t bytes = 2 * rows * p.head_dim * int64_t(sizeof(T));
+  auto kern = bytes > kRopeStreamBytes ? rope_kernel<T, VEC, true> : rope_kernel<T, VEC, false>;
+  return launch_dependent(kern, dim3(unsigned(blocks)), kRopeThreads, 0, p, stream);
 }
 
 // Widest pack that divides the pairs, the copied rest and the addresses.
