@@ -302,7 +302,9 @@ int locks_select_noalloc(const locks_cfg_t* cfg, const void* q, const void* summ
  * The conventions above hold (device pointers, no allocation, no
  * synchronisation, status bits).  The calls take their own configuration:
  * supported are head_dim = 128; page_size 64, 32 or 16; any G from 1 to 16;
- * max_pages < 2^24; num_blocks * n_kv_heads < 2^31; batch * n_kv_heads < 2^24.
+ * max_pages < 2^24; num_blocks * n_kv_heads < 2^31; batch * n_kv_heads < 2^24;
+ * and for the attention batch * n_kv_heads * (ceil(max_pages * page_size / 64) + 8)
+ * < 2^31 (with a page list, k in place of max_pages).
  * =========================================================================== */
 
 /* element type of a quantised cache */

@@ -35,7 +35,7 @@ __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
 
-// N consecutive elements, N * sizeof(T) a multiple of 8 or one element.  STREAM:
+// N consecutive elements, N * sizeof(T) a multiple of 4 or one element.  STREAM:
 // with the hint that the line is used once.
 template <typename T, int N>
 struct Pack {
@@ -52,6 +52,9 @@ struct Pack {
     } else if constexpr (kBytes % 8 == 0) {
       const uint2* at = reinterpret_cast<const uint2*>(p);
       *reinterpret_cast<uint2*>(e) = STREAM ? __ldcs(at) : *at;
+    } else if constexpr (kBytes % 4 == 0) {
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(p);
+      *reinterpret_cast<uint32_t*>(e) = STREAM ? __ldcs(at) : *at;
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) e[i] = p[i];
@@ -70,6 +73,10 @@ struct Pack {
       uint2* at = reinterpret_cast<uint2*>(p);
       if (STREAM) __stcs(at, *reinterpret_cast<const uint2*>(e));
       else *at = *reinterpret_cast<const uint2*>(e);
+    } else if constexpr (kBytes % 4 == 0) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(p);
+      if (STREAM) __stcs(at, *reinterpret_cast<const uint32_t*>(e));
+      else *at = *reinterpret_cast<const uint32_t*>(e);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i] = e[i];
@@ -201,6 +208,7 @@ int launch_rope_t(const RopeParams& p, cudaStream_t stream) {
   };
   if (fits(8)) return launch_rope_vec<T, 8>(p, stream);
   if (fits(4)) return launch_rope_vec<T, 4>(p, stream);
+  if (fits(2)) return launch_rope_vec<T, 2>(p, stream);
   return launch_rope_vec<T, 1>(p, stream);
 }
 

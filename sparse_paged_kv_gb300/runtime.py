@@ -7,6 +7,7 @@ library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 import math
 from typing import Optional
@@ -197,6 +198,154 @@ class LocksLayer:
         c = self.cfg
         return self.torch.full((c.batch, c.n_kv_heads, c.max_pages), float("nan"),
                                dtype=self.torch.float32, device=self.device)
+
+
+class QuantCache:
+    """The quantised paged cache of one attention layer: pools of e4m3, int8 or
+    int4 records, their block table and lengths, and the buffers of a decode
+    step.  Queries and keys are rotated by `rope` (a RopeTable, or None) as
+    tokens are written; attention reads the codes.
+
+    With `budget_tokens` the steps attend only the pages that the Locks
+    selection keeps: summaries are built from complete pages read back out of
+    the cache (what the attention will see of them), and each step selects
+    before it attends."""
+
+    def __init__(self, cfg: B.LocksKvConfig, block_table, rope: Optional[RopeTable] = None,
+                 budget_tokens: int = 0, rank: int = 8,
+                 summary_dtype: int = B.LOCKS_SUMMARY_F32, device: str = "cuda"):
+        import torch
+        self.torch, self.cfg, self.rope, self.device = torch, cfg, rope, device
+        rec = B.kv_record_bytes(cfg)
+        if rec == 0:
+            raise B.LocksError("locks_kv_record_bytes", B.LOCKS_ERR_UNSUPPORTED, "unsupported cfg")
+
+        def zeros(*shape, dtype=torch.uint8):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        self.k_pool = zeros(cfg.num_blocks, cfg.n_kv_heads, rec)
+        self.v_pool = zeros(cfg.num_blocks, cfg.n_kv_heads, rec)
+        self.block_table = torch.as_tensor(np.asarray(block_table, np.int32)).to(device)
+        self.seq_lens = zeros(cfg.batch, dtype=torch.int32)
+        self.positions = zeros(cfg.batch, dtype=torch.int32)    # of a step's tokens
+        self.workspace = zeros(max(1, B.kv_decode_workspace_bytes(cfg)))
+        rows = (cfg.batch, cfg.n_q_heads, cfg.head_dim)
+        self.q = zeros(*rows, dtype=torch.bfloat16)             # rotated query of a step
+        self.out = zeros(*rows, dtype=torch.bfloat16)
+        self.out_lse = zeros(*rows[:2], dtype=torch.float32)
+        self.completed = torch.full((cfg.batch,), -1, dtype=torch.int32, device=device)
+        self.status = zeros(1, dtype=torch.int32)
+        self.selected = None
+        if budget_tokens:
+            self.budget = int(budget_tokens)
+            self.locks_cfg = B.LocksConfig(
+                batch=cfg.batch, n_q_heads=cfg.n_q_heads, n_kv_heads=cfg.n_kv_heads,
+                head_dim=cfg.head_dim, page_size=cfg.page_size, rank=rank,
+                max_pages=cfg.max_pages, num_blocks=cfg.num_blocks, summary_dtype=summary_dtype)
+            summary = B.summary_record_bytes(self.locks_cfg)
+            if summary == 0:
+                raise B.LocksError("locks_summary_record_bytes", B.LOCKS_ERR_UNSUPPORTED,
+                                   "unsupported cfg")
+            # one record row more than blocks: where "no page" entries of a step's list go
+            self.summaries = zeros(cfg.num_blocks + 1, cfg.n_kv_heads, summary)
+            self.ws_select = zeros(max(1, B.select_workspace_bytes(self.locks_cfg, self.budget)))
+            k = self.locks_cfg.page_budget(self.budget)
+            self.selected = torch.full((cfg.batch, cfg.n_kv_heads, k), -1, dtype=torch.int32,
+                                       device=device)
+
+    # ---- writing ----------------------------------------------------------------
+    def write(self, q, k, v, token_seq, token_pos, q_out=None, completed=None, stream=None):
+        """Tokens of prompts or chunks of them: k, v (and q, rotated into q_out) bf16
+        [tokens][heads][d], slices of one projection's output allowed; token_seq, token_pos
+        int32 [tokens] on the device.  Raises seq_lens to cover them."""
+        B.locks_kv_write(self.cfg, k, v, token_pos, self.k_pool, self.v_pool, self.block_table,
+                         token_seq=token_seq, rope=self.rope, q=q, q_out=q_out,
+                         seq_lens=self.seq_lens, completed=completed, status=self.status,
+                         stream=stream)
+
+    def append(self, q, k, v, stream=None):
+        """One token per sequence at its current length: q rotated into self.q, the blocks of
+        pages it completed in self.completed (-1 for none)."""
+        with self._on(stream):
+            self.positions.copy_(self.seq_lens)
+        B.locks_kv_write(self.cfg, k, v, self.positions, self.k_pool, self.v_pool,
+                         self.block_table, rope=self.rope, q=q, q_out=self.q,
+                         seq_lens=self.seq_lens, completed=self.completed, status=self.status,
+                         stream=stream)
+
+    def read(self, block_ids, values: bool = True, stream=None):
+        """(keys, values) of the listed blocks as bf16 pages [blocks][H_kv][page_size][d]."""
+        c, n = self.cfg, block_ids.numel()
+        with self._on(stream):
+            out = [self.torch.zeros((n, c.n_kv_heads, c.page_size, c.head_dim),
+                                    dtype=self.torch.bfloat16, device=self.device)
+                   for _ in range(2 if values else 1)]
+        B.locks_kv_read(c, self.k_pool, self.v_pool if values else None, block_ids, out[0],
+                        out[1] if values else None, status=self.status, stream=stream)
+        return (out[0], out[1]) if values else out[0]
+
+    # ---- attention ----------------------------------------------------------------
+    def attend(self, q=None, selected=None, window: int = 0, stream=None):
+        """Attention of q (self.q where it is None) over the cache, into self.out and
+        self.out_lse: every page, the pages in `selected`, or the last `window` positions."""
+        B.locks_kv_decode(self.cfg, self.q if q is None else q, self.k_pool, self.v_pool,
+                          self.block_table, self.seq_lens, self.out, self.workspace,
+                          selected=selected, window=window, out_lse=self.out_lse,
+                          status=self.status, stream=stream)
+
+    def step(self, q, k, v, window: int = 0, stream=None):
+        """One decode step: rotate and write each sequence's token, select pages (with a
+        budget), attend."""
+        self.append(q, k, v, stream=stream)
+        if self.selected is not None:
+            B.locks_select(self.locks_cfg, self.q, self.summaries, self.block_table, self.seq_lens,
+                           self.budget, self.selected, self.ws_select, status=self.status,
+                           stream=stream)
+        self.attend(selected=self.selected, window=window, stream=stream)
+
+    def capture_step(self, q, k, v, window: int = 0):
+        """A CUDA graph of step() over these buffers: fill q, k, v and replay.  The step runs
+        once before the capture, on the sequences as they are, and its token is taken back
+        (lengths restored; the slot is written again by the first replay)."""
+        torch = self.torch
+        keep = self.seq_lens.clone()
+        cur = torch.cuda.current_stream(self.device)
+        side = torch.cuda.Stream(device=self.device)
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            self.step(q, k, v, window)
+        cur.wait_stream(side)
+        self.seq_lens.copy_(keep)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.step(q, k, v, window)
+        return graph
+
+    # ---- summaries ------------------------------------------------------------------
+    def build(self, block_ids, pages_at_once: int = 1024, stream=None):
+        """Summaries of complete pages (int32 block ids on the device; entries < 0 are
+        skipped), from their keys as the cache holds them."""
+        torch, c = self.torch, self.locks_cfg
+        with self._on(stream):
+            for at in range(0, block_ids.numel(), pages_at_once):
+                ids = block_ids[at:at + pages_at_once].contiguous()
+                n = ids.numel()
+                cfg = dataclasses.replace(c, num_blocks=n)
+                pages = self.read(ids, values=False)
+                made = torch.zeros((n, *self.summaries.shape[1:]), dtype=torch.uint8,
+                                   device=self.device)
+                there = ids >= 0
+                slots = torch.where(there, torch.arange(n, dtype=torch.int32, device=self.device), -1)
+                B.locks_build_completed(cfg, pages, slots, made)
+                self.summaries.index_copy_(0, torch.where(there, ids, c.num_blocks).long(), made)
+
+    def build_completed(self, stream=None):
+        """Summaries of the pages that the last append completed; needed before the next
+        step selects.  The list stays on the device."""
+        self.build(self.completed, stream=stream)
+
+    def _on(self, stream):
+        return self.torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 class DecodeLoop:

@@ -102,6 +102,9 @@ def test_decode_refusals(lib):
     assert _decode(lib, c, window=-1) == B.LOCKS_ERR_INVALID_ARG
     assert _decode(lib, c, sel=FAKE, k=0) == B.LOCKS_ERR_INVALID_ARG
     assert _decode(lib, c, wsb=B.kv_decode_workspace_bytes(c) - 1) == B.LOCKS_ERR_WORKSPACE
+    wide = cfg(batch=1 << 16, max_pages=1 << 20, num_blocks=1 << 20)     # 2^37 stages of 64 tokens
+    assert _decode(lib, wide) == B.LOCKS_ERR_UNSUPPORTED
+    assert _decode(lib, wide, sel=FAKE, k=1 << 20) == B.LOCKS_ERR_UNSUPPORTED
     assert _decode(lib, cfg(batch=0)) == B.LOCKS_OK
 
 
