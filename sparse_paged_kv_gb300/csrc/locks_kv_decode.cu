@@ -489,6 +489,17 @@ __device__ __forceinline__ int64_t div_blocks(int64_t x, int n) {
   return n == kSms ? int64_t(uint64_t(x) / kSms) : x / n;
 }
 
+// The block whose share [W c / N, W (c + 1) / N) holds x < W: the largest c with
+// W c <= (x + 1) N - 1.  The float quotient (N <= 152) is off by less than one,
+// and is put right in integers; a 64-bit division takes about a thousand cycles.
+__device__ __forceinline__ int block_of(int x, int N, int W) {
+  const int64_t most = int64_t(x + 1) * N - 1;
+  int c = int(__fdividef(float(most), float(W)));
+  if (int64_t(W) * c > most) --c;
+  if (int64_t(W) * (c + 1) <= most) ++c;
+  return c;
+}
+
 // The unit after (b, h), which starts at u in the list.
 __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& sq, int& h, int& u,
                                           int end) {
@@ -931,7 +942,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
         // releases this block's partial (ordered before by the barrier), acquires the others'
         const int before = ticket_add(ticket);
         // the blocks of the unit's first and last stage
-        const int c_lo = int((int64_t(u_lo + 1) * N - 1) / W), c_hi = int((int64_t(u_hi) * N - 1) / W);
+        const int c_lo = block_of(u_lo, N, W), c_hi = block_of(u_hi - 1, N, W);
         s_join = before == c_hi - c_lo ? make_int2(c_lo, c_hi) : make_int2(0, -1);
       }
       consumers_sync<NT>();
