@@ -46,77 +46,121 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
 }
 
-// largest over the aligned group of W lanes
+// largest of magnitudes, a NaN if there is one
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 template <int W>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
+__device__ __forceinline__ float lanes_max(float m) {   // over the aligned group of W lanes
 #pragma unroll
-  for (int o = W / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  for (int o = W / 2; o; o >>= 1) m = max_abs(m, __shfl_xor_sync(kFull, m, o));
   return m;
 }
-
-// largest magnitude of 8 floats, as bits (ordered like the magnitudes, a NaN above infinity)
-__device__ __forceinline__ uint32_t magnitude(const float (&x)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  return m;
+__device__ __forceinline__ float magnitude(const float (&x)[8]) {
+  return max_abs(max_abs(max_abs(x[0], x[1]), max_abs(x[2], x[3])),
+                 max_abs(max_abs(x[4], x[5]), max_abs(x[6], x[7])));
 }
 
-// The row x (8 dims a lane) quantised into row `r` of record `rec`.  Every lane
-// of the warp calls it; `live` says whether this half-warp's row is stored.
-template <int FMT>
-__device__ __forceinline__ void store_row(const float (&x)[8], unsigned char* rec, int r, int B,
-                                          int l16, bool live) {
-  const uint32_t mb = lanes_max<16>(magnitude(x));
-  const float m = __uint_as_float(mb);
-  const bool odd = mb >= 0x7f800000u;                 // an infinity or a NaN
-  const bool dead = odd || m < kKvTiny;
+// rint(y) + k in the low bits of the result, for |y| + k < 2^22: the sum with
+// 1.5 * 2^23 has a unit of 1, and rounds ties to even as rint does (k even).
+// (A conversion to an integer runs at a quarter of an addition's rate.)
+__device__ __forceinline__ uint32_t round_bits(float y, float k) {
+  return __float_as_uint(__fadd_rn(y, 12582912.f + k));
+}
+__device__ __forceinline__ float round_float(float y) {
+  return __fadd_rn(__fadd_rn(y, 12582912.f), -12582912.f);
+}
+
+// N rows (8 dims a lane each) quantised into row `r` of their records.  Every
+// lane of the warp calls it; `live` says whether this half-warp's row is stored.
+// The rows go side by side through each step, whose latencies then overlap.
+template <int FMT, int N>
+__device__ __forceinline__ void store_rows(const float (&x)[N][8], unsigned char* const (&rec)[N], int r,
+                                           int B, int l16, const bool (&live)[N]) {
+  float m[N], y[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n) m[n] = magnitude(x[n]);
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) m[n] = max_abs(m[n], __shfl_xor_sync(kFull, m[n], o));
   constexpr float kInvTop = FMT == LOCKS_KV_F8 ? float(1.0 / 448.0)
                             : FMT == LOCKS_KV_I8 ? float(1.0 / 127.0)
                                                  : float(1.0 / (7.0 * 448.0));
-  const float scale = __fmul_rn(m, kInvTop);
-  const float inv = __frcp_rn(scale);
-  float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
-  if (dead) {                                         // (rare: the whole half-warp)
+  for (int n = 0; n < N; ++n) {
+    const bool odd = !(m[n] <= 3.402823466e38f);      // an infinity or a NaN in the row
+    const bool dead = odd || m[n] < kKvTiny;
+    const float scale = __fmul_rn(m[n], kInvTop);
+    const float inv = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = 0.f;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 t = fmul2(make_float2(x[n][i], x[n][i + 1]), make_float2(inv, inv));
+      y[n][i] = t.x;
+      y[n][i + 1] = t.y;
+    }
+    if (dead) {                                       // (rare)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[n][i] = 0.f;
+    }
+    if (live[n] && l16 == 0)
+      *reinterpret_cast<float*>(rec[n] + kv_scale_off(FMT, B) + 4 * r) =
+          odd ? __int_as_float(0x7fffffff) : (dead ? 0.f : scale);
   }
-  if constexpr (FMT == LOCKS_KV_F8) {
-    uint2 w;
-    w.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
-    w.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
-    if (live) *reinterpret_cast<uint2*>(rec + kv_chunk_off<FMT>(r, l16 >> 1) + 8 * (l16 & 1)) = w;
-  } else if constexpr (FMT == LOCKS_KV_I8) {
-    // |y| <= 127 (1 + 2^-22): rounding to integers keeps to -127 .. 127
-    uint32_t c[8];
+  if constexpr (FMT == LOCKS_KV_I4) {
+    float gm[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = uint32_t(__float2int_rn(y[i]) + 128);
-    uint2 w;
-    w.x = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-    w.y = c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24);
-    if (live) *reinterpret_cast<uint2*>(rec + kv_chunk_off<FMT>(r, l16 >> 1) + 8 * (l16 & 1)) = w;
+    for (int n = 0; n < N; ++n) gm[n] = magnitude(y[n]);
+#pragma unroll
+    for (int o = 2; o; o >>= 1)                       // dims 32j .. 32j + 31
+#pragma unroll
+      for (int n = 0; n < N; ++n) gm[n] = max_abs(gm[n], __shfl_xor_sync(kFull, gm[n], o));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t gbits = e4m3x2(__fmul_rn(gm[n], float(1.0 / 7.0)), 0.f) & 0xff;
+      const float g = e4m3x2_to_f2(gbits).x;
+      const float ginv = g > 0.f ? __frcp_rn(g) : 0.f;
+      float c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = __fmul_rn(y[n][i], ginv);
+      // e4m3 rounds a normal scale down by at most 2^-4, which leaves 7 * 16 / 15 < 7.5;
+      // only below its normal range can a code pass 7
+      if (gbits < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = fminf(7.f, fmaxf(-7.f, c[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = round_float(c[i]);
+      // four codes + 8 as hexadecimal digits of an exact float sum (0x8888 = 34952)
+      float lo = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
+      float hi = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
+      const uint32_t w = __byte_perm(round_bits(lo, 34952.f), round_bits(hi, 34952.f), 0x5410);
+      if (live[n]) {
+        *reinterpret_cast<uint32_t*>(rec[n] + kv_chunk_off<FMT>(r, l16 >> 2) + 4 * (l16 & 3)) = w;
+        if ((l16 & 3) == 0) rec[n][kv_group_off(FMT, B) + 4 * r + (l16 >> 2)] = (unsigned char)gbits;
+      }
+    }
   } else {
-    const float gm = __uint_as_float(lanes_max<4>(magnitude(y)));   // dims 32j .. 32j + 31
-    const uint32_t gbits = e4m3x2(__fmul_rn(gm, float(1.0 / 7.0)), 0.f) & 0xff;
-    const float g = e4m3x2_to_f2(gbits).x;
-    const float ginv = g > 0.f ? __frcp_rn(g) : 0.f;
-    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // (the group's scale may be rounded down by 2^-4: codes up to 7.47)
-      const int c = min(7, max(-7, __float2int_rn(__fmul_rn(y[i], ginv))));
-      w |= uint32_t(c + 8) << (4 * i);
-    }
-    if (live) {
-      *reinterpret_cast<uint32_t*>(rec + kv_chunk_off<FMT>(r, l16 >> 2) + 4 * (l16 & 3)) = w;
-      if ((l16 & 3) == 0) rec[kv_group_off(FMT, B) + 4 * r + (l16 >> 2)] = (unsigned char)gbits;
+    for (int n = 0; n < N; ++n) {
+      uint2 w;
+      if constexpr (FMT == LOCKS_KV_F8) {
+        w.x = e4m3x2(y[n][0], y[n][1]) | (e4m3x2(y[n][2], y[n][3]) << 16);
+        w.y = e4m3x2(y[n][4], y[n][5]) | (e4m3x2(y[n][6], y[n][7]) << 16);
+      } else {
+        // |y| <= 127 (1 + 2^-22): codes + 128 are bytes
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = round_bits(y[n][i], 128.f);
+        w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+      }
+      if (live[n])
+        *reinterpret_cast<uint2*>(rec[n] + kv_chunk_off<FMT>(r, l16 >> 1) + 8 * (l16 & 1)) = w;
     }
   }
-  if (live && l16 == 0)
-    *reinterpret_cast<float*>(rec + kv_scale_off(FMT, B) + 4 * r) =
-        odd ? __int_as_float(0x7fffffff) : (dead ? 0.f : scale);
 }
 
 enum { kNoTurn = 0, kHalf = 1, kInterleaved = 2 };
@@ -293,27 +337,29 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
     }
   }
   if (blk < 0) return;
-  // keys, then values (the shuffles of store_row name every lane: a row past the end is not stored)
+  // keys and values, two rows at a time (the shuffles of store_rows name every
+  // lane: a row past the end is not stored)
   const size_t rec_bytes = size_t(kv_rec_bytes(FMT, B));
-  {
-    unsigned char* dst = p.k_pool + size_t(blk) * hk * rec_bytes;
-    const int end = min(hi, hq + hk);
-#pragma unroll 2
-    for (int r = max(lo, hq) + hw; r - (hw & 1) < end; r += kStep) {
-      const unsigned char* at = mine + (min(r, end - 1) - lo) * kRowBytes;
-      float x[8];
-      rotate8<LAYOUT>(x, *reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + away), turn);
-      store_row<FMT>(x, dst + (min(r, end - 1) - hq) * rec_bytes, slot, B, l16, r < end);
+  const size_t page = size_t(blk) * hk * rec_bytes;
+  for (int r0 = max(lo, hq) + hw; r0 - (hw & 1) < hi; r0 += 2 * kStep) {
+    float x[2][8];
+    unsigned char* rec[2];
+    bool live[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int r = min(r0 + n * kStep, hi - 1);
+      live[n] = r == r0 + n * kStep;
+      const unsigned char* at = mine + (r - lo) * kRowBytes;
+      const uint4 own = *reinterpret_cast<const uint4*>(at);
+      if (r < hq + hk) {
+        rotate8<LAYOUT>(x[n], own, *reinterpret_cast<const uint4*>(at + away), turn);
+        rec[n] = p.k_pool + page + (r - hq) * rec_bytes;
+      } else {
+        unpack8(own, x[n]);
+        rec[n] = p.v_pool + page + (r - hq - hk) * rec_bytes;
+      }
     }
-  }
-  {
-    unsigned char* dst = p.v_pool + size_t(blk) * hk * rec_bytes;
-#pragma unroll 2
-    for (int r = max(lo, hq + hk) + hw; r - (hw & 1) < hi; r += kStep) {
-      float x[8];
-      unpack8(*reinterpret_cast<const uint4*>(mine + (min(r, hi - 1) - lo) * kRowBytes), x);
-      store_row<FMT>(x, dst + (min(r, hi - 1) - hq - hk) * rec_bytes, slot, B, l16, r < hi);
-    }
+    store_rows<FMT, 2>(x, rec, slot, B, l16, live);
   }
 }
 
