@@ -111,6 +111,7 @@ int locks_kv_write(const locks_kv_cfg_t* cfg, const void* k_new, int64_t k_strid
       (q_new == nullptr) != (q_out == nullptr) || token_pos == seq_lens)
     return LOCKS_ERR_INVALID_ARG;
   if (!token_seq && n_tokens > cfg->batch) return LOCKS_ERR_INVALID_ARG;
+  if (n_tokens > (1 << 30)) return LOCKS_ERR_UNSUPPORTED;     // token numbers are ints, rounded up to groups
   if (misaligned(k_new) || misaligned(v_new) || misaligned(k_pool) || misaligned(v_pool) ||
       misaligned(q_new) || misaligned(q_out) || k_stride % 8 || v_stride % 8 ||
       (q_new && q_stride % 8))
@@ -179,6 +180,7 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
   if (rc != LOCKS_OK) return rc;
   if (window < 0 || (selected && k <= 0)) return LOCKS_ERR_INVALID_ARG;
   // the kernel counts the 64-token stages of all units (and 8 more a unit) in an int
+  if (selected && k >= (1 << 24)) return LOCKS_ERR_UNSUPPORTED;
   const int64_t pages = selected ? k : cfg->max_pages;
   if (((pages * cfg->page_size + 63) / 64 + 8) * cfg->batch * cfg->n_kv_heads >= (int64_t(1) << 31))
     return LOCKS_ERR_UNSUPPORTED;

@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
     // a block's first partial goes on with an earlier block's unit, its second begins one
     float* part = parts + (size_t(blockIdx.x) * 2 + (u_lo >= w_lo)) * (kv_part_bytes(NT) / 4);
+    __syncwarp();
     if (lane == 0) mbar_arrive(s_qempty + (seg & 1));
     // every warp brings its sums to the block's reference M, then they are added up item by item
     if (g == 0) {
@@ -967,9 +968,14 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
     ++seg;
   }
-  // a wait that ran out: no block leaves while copies into its memory may be in flight
+  // a wait ran out: the copies asked for are waited for once more, until one fails again
+  // (no block should leave while copies into its memory are in flight)
   if (!ok)
-    for (int s = 0; s < STAGES; ++s) mbar_wait_bounded(s_full + s, 1);
+    for (int i = 0; i < STAGES && mbar_wait_bounded(s_full + s, phase); ++i)
+      if (++s == STAGES) {
+        s = 0;
+        phase ^= 1;
+      }
 }
 
 template <int FMT, int NT>

@@ -105,6 +105,7 @@ def test_decode_refusals(lib):
     wide = cfg(batch=1 << 16, max_pages=1 << 20, num_blocks=1 << 20)     # 2^37 stages of 64 tokens
     assert _decode(lib, wide) == B.LOCKS_ERR_UNSUPPORTED
     assert _decode(lib, wide, sel=FAKE, k=1 << 20) == B.LOCKS_ERR_UNSUPPORTED
+    assert _decode(lib, c, sel=FAKE, k=1 << 24) == B.LOCKS_ERR_UNSUPPORTED
     assert _decode(lib, cfg(batch=0)) == B.LOCKS_OK
 
 
@@ -126,6 +127,7 @@ def test_write_refusals(lib):
     for bad in (_table(130), _table(0), _table(15), _table(128, 2), _table(turns=None),
                 _table(mscale=0.0), _table(mscale=float("nan"))):
         assert _write(lib, c, rope=bad) == B.LOCKS_ERR_INVALID_ARG
+    assert _write(lib, c, n=(1 << 30) + 1) == B.LOCKS_ERR_UNSUPPORTED
     assert _write(lib, c, n=0) == B.LOCKS_OK
 
 
