@@ -448,13 +448,17 @@ __device__ __forceinline__ void attend(const uint32_t (&base)[C], const uint32_t
 // another at its end and merge their states.  (16 ragged sequences up to 16K in
 // int8: 69.3 us with 0, 65.3 with 3, 62.5 with 6; equal lengths do not care.)
 constexpr int kUnitCost = 6;
+// What a block's second end costs against parts that are shorter by so many
+// stages.  (Lists and contexts of one length: equal parts are 4 to 20% faster below
+// 37 stages a unit's idle share, 5% slower at 46 in int4; measured for 40 to 144 units.)
+constexpr float kEndCost = 36.f;
 
 // A sequence as the kernel walks it: its length, the first attended position,
 // its first stage and its number of stages (the same for every KV head).
 struct Seq {
   int n, lo, first, stages;
-  // cost of each of its units, overhead first
-  __device__ __forceinline__ int cost() const { return stages > 0 ? stages + kUnitCost : 0; }
+  // cost of each of its units, the fixed part first
+  __device__ __forceinline__ int cost(int fixed) const { return stages > 0 ? stages + fixed : 0; }
 };
 __device__ __forceinline__ Seq seq_of(const KvDecodeParams& p, int b) {
   Seq s;
@@ -484,9 +488,10 @@ __device__ __forceinline__ void zero_empty(const KvDecodeParams& p, int lane) {
   }
 }
 
-// x / n; n is nearly always the number of blocks, and a constant divides faster
-__device__ __forceinline__ int64_t div_blocks(int64_t x, int n) {
-  return n == kSms ? int64_t(uint64_t(x) / kSms) : x / n;
+// x / y for 0 <= x < 2^19, y > 0, in floats: half a step off the borders, where
+// the approximate quotient is certain
+__device__ __forceinline__ int small_div(int x, int y) {
+  return int(__fdividef(float(x) + 0.5f, float(y)));
 }
 
 // The block whose share [W c / N, W (c + 1) / N) holds x < W: the largest c with
@@ -502,8 +507,8 @@ __device__ __forceinline__ int block_of(int x, int N, int W) {
 
 // The unit after (b, h), which starts at u in the list.
 __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& sq, int& h, int& u,
-                                          int end) {
-  u += sq.cost();
+                                          int end, int fixed) {
+  u += sq.cost(fixed);
   if (++h < p.n_kv_heads || u >= end) return;     // (beyond `end` there may be no sequence)
   h = 0;
   do sq = seq_of(p, ++b);
@@ -653,23 +658,61 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
   // ---- this block's share of the units' cost, which every warp works out for itself ----
   const int per = (p.batch + 31) / 32;
   const int b_lo = min(p.batch, lane * per), b_hi = min(p.batch, b_lo + per);
-  int mine = 0;
+  int stages = 0, units = 0, least = 0x7fffffff, most = 0;   // of this lane's sequences; units: with stages
 #pragma unroll 4
-  for (int i = b_lo; i < b_hi; ++i) mine += seq_of(p, i).cost();
-  int incl = mine;
+  for (int i = b_lo; i < b_hi; ++i) {
+    const int n = seq_of(p, i).stages;
+    stages += n;
+    units += n > 0;
+    least = min(least, n > 0 ? n : least);
+    most = max(most, n);
+  }
+  least = __reduce_min_sync(kFull, least);
+  most = __reduce_max_sync(kFull, most);
+  int stages_to = stages, units_to = units;       // up to and with this lane
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += x;
+    const int x = __shfl_up_sync(kFull, stages_to, o), y = __shfl_up_sync(kFull, units_to, o);
+    if (lane >= o) {
+      stages_to += x;
+      units_to += y;
+    }
   }
-  const int W = __shfl_sync(kFull, incl, 31) * hk; // below 2^31: the host has checked
-  const int N = min(int(gridDim.x), max(W, 1));
-  const int w_lo = int(blockIdx.x) < N ? int(div_blocks(int64_t(W) * blockIdx.x, N)) : 0;
-  const int w_hi = int(blockIdx.x) < N ? int(div_blocks(int64_t(W) * (blockIdx.x + 1), N)) : 0;
-  int b = b_lo, u = (incl - mine) * hk;           // the sequence of w_lo and where it starts in the list
-  const bool here = u <= w_lo && w_lo < incl * hk;
+  const int all_stages = __shfl_sync(kFull, stages_to, 31) * hk;   // below 2^31: the host has checked
+  const int all_units = __shfl_sync(kFull, units_to, 31) * hk;
+  // Units of one length that m blocks each come close to filling the SMs: equal
+  // parts, no block with two units' ends (64 lists of 32 pages in int4: 16.1 -> 13.7
+  // us with 128 blocks).  Taken when a part's extra stages cost less than the second
+  // end that a block has on average otherwise.
+  int m = least == most ? min(small_div(kSms, all_units), most) : 0;
+  if (float(most) * float(kSms - m * all_units) > kEndCost * float(m * all_units)) m = 0;
+  const int fixed = m ? 0 : kUnitCost;
+  const int W = all_stages + fixed * all_units;
+  const int N = m ? m * all_units : min(kSms, max(W, 1));
+  int w_lo = 0, w_hi = 0;
+  if (int(blockIdx.x) < N) {
+    if (m) {
+      const int unit = small_div(blockIdx.x, m), part = int(blockIdx.x) - unit * m;
+      // most = each * m + rest, with an `each` a little below the quotient (the float one is
+      // within 2^-22 of it): 0 <= rest < 16 m
+      const int each = max(int(__fdividef(float(most), float(m)) * (1.f - 4.8e-7f)) - 1, 0);
+      const int rest = most - each * m;
+      w_lo = unit * most + part * each + small_div(part * rest, m);
+      w_hi = unit * most + (part + 1) * each + small_div((part + 1) * rest, m);
+    } else if (N == kSms) {                       // W c / kSms
+      const unsigned c = blockIdx.x, each = unsigned(W) / kSms, rest = unsigned(W) % kSms;
+      w_lo = each * c + rest * c / kSms;
+      w_hi = each * (c + 1) + rest * (c + 1) / kSms;
+    } else {
+      w_lo = blockIdx.x;                          // W = N
+      w_hi = blockIdx.x + 1;
+    }
+  }
+  // the sequence of w_lo and where it starts in the list
+  int b = b_lo, u = (stages_to - stages + fixed * (units_to - units)) * hk;
+  const bool here = u <= w_lo && w_lo < (stages_to + fixed * units_to) * hk;
   if (here) {
-    for (int c; u + (c = seq_of(p, b).cost() * hk) <= w_lo; ++b) u += c;
+    for (int c; u + (c = seq_of(p, b).cost(fixed) * hk) <= w_lo; ++b) u += c;
   }
   const int who = __ffs(__ballot_sync(kFull, here)) - 1;
   b = __shfl_sync(kFull, b, max(who, 0));
@@ -684,8 +727,8 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
 
   const size_t rec = size_t(kv_rec_bytes(FMT, B));
   Seq sq = seq_of(p, b);
-  int h = (w_lo - u) / sq.cost();
-  u += h * sq.cost();                             // where unit (b, h) starts in the list
+  int h = (w_lo - u) / sq.cost(fixed);
+  u += h * sq.cost(fixed);                             // where unit (b, h) starts in the list
   int it = 0;                                     // stages of this block so far
 
   if (warp >= kKvWarps) {
@@ -698,10 +741,10 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     const int looked = 32 / pps;                  // stages looked up at a time
     int s = pw, phase = 1;                        // ring slot of the warp's next stage; nothing to wait for yet
     bool ok = true;
-    for (int seg = 0; ok; next_unit(p, b, sq, h, u, w_hi)) {
+    for (int seg = 0; ok; next_unit(p, b, sq, h, u, w_hi, fixed)) {
       if (u >= w_hi) break;
-      const int i0 = max(0, w_lo - u - kUnitCost);
-      const int cnt = min(sq.stages, w_hi - u - kUnitCost) - i0;
+      const int i0 = max(0, w_lo - u - fixed);
+      const int cnt = min(sq.stages, w_hi - u - fixed) - i0;
       if (cnt <= 0) continue;
       // the last warps also bring the unit's query, whose loads are on their way
       // while the first pages are looked up
@@ -812,9 +855,9 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     s -= STAGES;
     phase ^= 1;
   }
-  for (int seg = 0; u < w_hi; next_unit(p, b, sq, h, u, w_hi)) {
-    const int i0 = max(0, w_lo - u - kUnitCost);
-    const int cnt = min(sq.stages, w_hi - u - kUnitCost) - i0;
+  for (int seg = 0; u < w_hi; next_unit(p, b, sq, h, u, w_hi, fixed)) {
+    const int i0 = max(0, w_lo - u - fixed);
+    const int cnt = min(sq.stages, w_hi - u - fixed) - i0;
     if (cnt <= 0) continue;
     const int unit = b * hk + h;
     if (ok && !__all_sync(kFull, mbar_wait_bounded(s_qfull + (seg & 1), (seg >> 1) & 1))) {
@@ -869,7 +912,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
 
     // ---- merge the warps' states; finish the unit or leave a partial ----
-    const int u_lo = u + kUnitCost, u_hi = u_lo + sq.stages;     // its stages in the list
+    const int u_lo = u + fixed, u_hi = u_lo + sq.stages;     // its stages in the list
     const bool alone = u_lo >= w_lo && u_hi <= w_hi;
     float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
     // a block's first partial goes on with an earlier block's unit, its second begins one
@@ -943,7 +986,8 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
         // releases this block's partial (ordered before by the barrier), acquires the others'
         const int before = ticket_add(ticket);
         // the blocks of the unit's first and last stage
-        const int c_lo = block_of(u_lo, N, W), c_hi = block_of(u_hi - 1, N, W);
+        const int c_lo = m ? u / most * m : block_of(u_lo, N, W);
+        const int c_hi = m ? c_lo + m - 1 : block_of(u_hi - 1, N, W);
         s_join = before == c_hi - c_lo ? make_int2(c_lo, c_hi) : make_int2(0, -1);
       }
       consumers_sync<NT>();

@@ -676,3 +676,17 @@ def test_pools_past_four_gigabytes():
         o, l, bounds = R.attend(q[0, h:h + 1].double().cpu().numpy(), k, v)
         tol, _ = attend_tol(o, l, bounds, n)
         assert (np.abs(out[0, h:h + 1].double().cpu().numpy() - o) <= tol).all()
+
+
+@pytest.mark.parametrize("batch,hkv,n", [(16, 8, 500), (1, 8, 1000), (4, 2, 777), (19, 8, 130), (3, 1, 20000),
+                                         (76, 2, 90), (1, 1, 64), (38, 4, 65)])
+@pytest.mark.parametrize("name,fmt", FMTS)
+def test_decode_equal_lengths(name, fmt, batch, hkv, n):
+    """Sequences of one length, whose units are cut in equal parts, with and without empty ones."""
+    c = Cache(fmt, 32, [n] * batch, hkv * 2, hkv, seed=n + fmt)
+    c.check(c.run())
+    lens = [n] * batch
+    lens[0] = 0
+    lens[batch // 2] = 0
+    c = Cache(fmt, 32, lens, hkv * 2, hkv, seed=n)
+    c.check(c.run())
