@@ -362,12 +362,14 @@ def kv_decode_workspace_bytes(cfg: LocksKvConfig) -> int:
 
 
 def rope_frequencies(spec: locks_rope_spec_t) -> Tuple:
-    """(turns as a list of ints, mscale) of a rotary specification (host only)."""
-    turns = (ctypes.c_uint64 * max(1, min(256, spec.rotary_dim // 2)))()
+    """(turns as a uint64 array, mscale) of a rotary specification (host only)."""
+    import numpy as np
+    turns = np.empty(max(1, min(256, spec.rotary_dim // 2)), dtype=np.uint64)
     mscale = ctypes.c_float()
-    rc = load_library().locks_rope_frequencies(ctypes.byref(spec), turns, ctypes.byref(mscale))
+    rc = load_library().locks_rope_frequencies(ctypes.byref(spec), turns.ctypes.data,
+                                               ctypes.byref(mscale))
     _check("locks_rope_frequencies", rc)
-    return list(turns), mscale.value
+    return turns, mscale.value
 
 
 def _typed(x, dtype: str, what: str):
@@ -413,26 +415,29 @@ def _rows(x, heads: int, dim: int, what: str) -> Tuple[int, int]:
     return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else heads * dim)
 
 
-_ROPE_DTYPES = {"torch.bfloat16": LOCKS_BF16, "torch.float16": LOCKS_F16, "torch.float32": LOCKS_F32}
+@functools.lru_cache(maxsize=None)
+def _rope_dtype(dtype) -> Optional[int]:
+    return {"torch.bfloat16": LOCKS_BF16, "torch.float16": LOCKS_F16,
+            "torch.float32": LOCKS_F32}.get(str(dtype))
 
 
 def locks_rope(rope, x, positions, out, inverse: bool = False, stream=None) -> None:
     """Rotary positions of x [tokens][heads][head_dim] (bf16, f16 or f32; any token and head
     strides, also x is out) into `out`; `rope` is a runtime.RopeTable, `inverse` the gradient."""
-    dtype = _ROPE_DTYPES.get(str(x.dtype))
-    if dtype is None or out.dtype != x.dtype:
+    dtype = _rope_dtype(x.dtype)
+    if dtype is None or out.dtype is not x.dtype:
         raise ValueError("x, out: bf16, f16 or f32 tensors of one type expected")
     if x.dim() != 3 or out.shape != x.shape:
         raise ValueError("x, out: [tokens][heads][head_dim] tensors of one shape expected")
     if not (x.is_cuda and out.is_cuda):
         raise ValueError("x, out: device tensors expected")
     n, heads, dim = x.shape
-    if dim > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+    (xt, xh, xe), (ot, oh, oe) = x.stride(), out.stride()
+    if dim > 1 and (xe != 1 or oe != 1):
         raise ValueError("x, out: contiguous last dimension expected")
     rc = load_library().locks_rope(
-        rope.ref, dtype, dim, x.data_ptr(), x.stride(0), x.stride(1),
-        _sized(positions, "int32", (n,), "positions"), n, heads, out.data_ptr(), out.stride(0),
-        out.stride(1), 1 if inverse else 0, _stream(stream))
+        rope.ref, dtype, dim, x.data_ptr(), xt, xh, _sized(positions, "int32", (n,), "positions"),
+        n, heads, out.data_ptr(), ot, oh, 1 if inverse else 0, _stream(stream))
     _check("locks_rope", rc)
 
 

@@ -51,7 +51,7 @@ class RopeTable:
                                    beta_fast, beta_slow)
         turns, self.mscale = B.rope_frequencies(spec)
         self.rotary_dim, self.layout = rotary_dim, layout
-        self.turns = torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(device)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self._c = B.locks_rope_table_t(self.turns.data_ptr(), rotary_dim, self.LAYOUTS[layout],
                                        self.mscale)
         self.ref = ctypes.byref(self._c)
