@@ -13,7 +13,8 @@
 // Work split.  The 64-token stages of all (sequence, KV head) units form one
 // list, each unit preceded by its fixed cost; block c of 152 (one per SM) takes
 // the c-th part of it, whatever the lengths of the sequences, so that ragged
-// batches load every SM alike.  A unit that lies in one block is finished there;
+// batches load every SM alike.  (Units of one length that so many blocks each
+// nearly fill the SMs are cut in equal parts instead.)  A unit that lies in one block is finished there;
 // one that is cut is left as partials (running maximum, sum, weighted values) in
 // the workspace, and the last of its blocks to arrive (atomic ticket) merges them
 // in the blocks' order, so results do not depend on the order of arrival.  The
@@ -32,9 +33,10 @@
 // that Q shares); V's are two tokens' bytes interleaved by a byte permute; P is
 // turned from S^T's layout into an operand by movmatrix.
 //
-// Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 310 us (7.1 TB/s), 8 x
-// 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 122 us (4.95 TB/s): instructions,
-// of which the unpacking of codes is over half.
+// Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 314 us (7.05 TB/s), 8 x
+// 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 120 us (5.0 TB/s): instructions,
+// 370 for 16 tokens of a head, of which the unpacking of codes is over half.  One
+// sequence of 1000 tokens 9.3 us: a chain of latencies.
 #include "locks_kv.cuh"
 
 namespace locks {

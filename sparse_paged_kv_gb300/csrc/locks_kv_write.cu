@@ -1,7 +1,10 @@
 // locks_kv_write and locks_kv_read: tokens into a quantised paged cache, with
 // the rotation of their queries and keys, and pages back out of it.
 //
-// Both move every byte once and are bound by memory.  Half a warp (16 lanes of
+// Both move every byte once.  Measured (one GB300, 32 / 8 heads, e4m3, half
+// layout): 8192 tokens written in 35 us (5.3 TB/s of 6.78 copy; the blocks of a
+// wave load and compute in step), read back in 10 us (issue slots); 16 tokens of
+// a decode step in 7 us (latency).  Half a warp (16 lanes of
 // 8 dims) owns a row of 128 dims: its largest magnitude is four shuffles, a
 // group of 32 dims is four lanes, and its codes leave as one 128-byte (or
 // 64-byte) line.
