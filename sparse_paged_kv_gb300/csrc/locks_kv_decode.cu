@@ -44,15 +44,26 @@ namespace locks {
 namespace {
 
 // One block per SM.  For up to 8 heads a group 16 consumer warps of 104
-// registers; for up to 16, whose accumulators are twice as large, 8 of 168.
+// registers; for up to 16, whose accumulators are twice as large, 12 of 136 (2 KV
+// heads of 16 heads, us, with 12 and with 8 warps of 168: 16 x 128K tokens int4
+// 190, 216, e4m3 171, 186; 4 x 20000 e4m3 23.2, 22.5; 1 x 1000 13.0, 11.6: long
+// caches have the most to gain).
 constexpr int kSms = 152;
-__host__ __device__ constexpr int kv_warps(int nt) { return nt == 1 ? 16 : 8; }
-// and four producer warps: among busy consumers a warp issues an instruction in
-// about seven cycles, and one producer could not keep up with the stages (1M e4m3:
-// 415 us)
+__host__ __device__ constexpr int kv_warps(int nt) { return nt == 1 ? 16 : 12; }
+// And a warpgroup of producers: among busy consumers a warp issues an instruction
+// in about seven cycles, and one producer could not keep up with the stages (1M
+// e4m3: 415 us).  All four copy; with 12 consumers three do, as the ring's length
+// has to suit both.
 __host__ __device__ constexpr int kv_threads(int nt) { return kv_warps(nt) * 32 + 128; }
-constexpr int kConsumerRegs = 104, kProducerRegs = 64;
-static_assert(16 * 32 * kConsumerRegs + 128 * kProducerRegs <= 640 * 96, "registers of the launch");
+constexpr int kv_copiers(int nt) { return nt == 1 ? 4 : 3; }
+constexpr int kv_consumer_regs(int nt) { return nt == 1 ? 104 : 136; }   // of a thread
+constexpr int kv_producer_regs(int nt) { return nt == 1 ? 64 : 96; }
+// the launch has 65536 / threads, rounded down to 8
+constexpr bool kv_regs_fit(int nt) {
+  return kv_warps(nt) * 32 * kv_consumer_regs(nt) + 128 * kv_producer_regs(nt) <=
+         kv_threads(nt) * (65536 / kv_threads(nt) / 8 * 8);
+}
+static_assert(kv_regs_fit(1) && kv_regs_fit(2), "registers of the launch");
 constexpr int kStageTok = 64;
 constexpr float kNone = -3.402823466e38f;         // running maximum before any token
 // merge buffer: the warps' states of 8 heads x 128 floats
@@ -72,17 +83,16 @@ constexpr int kv_chunks(int fmt, int nt) { return nt == 1 && fmt == LOCKS_KV_I4 
 // slot at every use of it, as waiting by the barrier's parity requires (copies
 // land out of order, so having seen a later stage full says nothing about a
 // slot's earlier use).
-constexpr int kv_stages(int fmt) {
-  return fmt == LOCKS_KV_I4 ? 16 : 8;
+constexpr int kv_stages(int fmt, int nt) {
+  return nt == 1 ? (fmt == LOCKS_KV_I4 ? 16 : 8) : (fmt == LOCKS_KV_I4 ? 12 : 9);
 }
 constexpr bool kv_rounds(int fmt, int nt) {
-  return 4 / kv_chunks(fmt, nt) * kv_stages(fmt) % kv_warps(nt) == 0;
+  return 4 / kv_chunks(fmt, nt) * kv_stages(fmt, nt) % kv_warps(nt) == 0 &&
+         kv_stages(fmt, nt) % kv_copiers(nt) == 0;     // (and a slot belongs to one producer warp)
 }
 static_assert(kv_rounds(LOCKS_KV_F8, 1) && kv_rounds(LOCKS_KV_I4, 1) && kv_rounds(LOCKS_KV_F8, 2) &&
                   kv_rounds(LOCKS_KV_I4, 2),
               "every warp must see every use of the ring slots it visits");
-static_assert(kv_stages(LOCKS_KV_F8) % 4 == 0 && kv_stages(LOCKS_KV_I4) % 4 == 0,
-              "a ring slot belongs to one producer warp");
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -616,10 +626,11 @@ __device__ __forceinline__ void join_partials(const float* parts, int c_lo, int 
 
 template <int FMT, int NT>
 __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDecodeParams p) {
-  constexpr int STAGES = kv_stages(FMT);
+  constexpr int STAGES = kv_stages(FMT, NT);
   constexpr int C = kv_chunks(FMT, NT), JOBS = 4 / C;   // chunks of a job, jobs of a stage
   constexpr int kStageBytes = kv_stage_bytes(FMT);
-  constexpr int kKvWarps = kv_warps(NT), kKvThreads = kv_threads(NT);
+  constexpr int kKvWarps = kv_warps(NT), kCopiers = kv_copiers(NT);
+  constexpr int kItems = (512 + kKvWarps * 32 - 1) / (kKvWarps * 32);   // float2 items of 8 heads a thread
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* ring = smem;
   float4* mbuf = reinterpret_cast<float4*>(smem + STAGES * kStageBytes);    // [warp][8][32]
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
 
   if (warp >= kKvWarps) {
     // ---------------- producer ----------------
-    if constexpr (NT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kv_producer_regs(NT)));
     const uint64_t pol = l2_evict_first();
     const int pw = warp - kKvWarps;
     const int e = lane & (pps - 1), mine = lane / pps;   // this lane's page of a stage, and its stage
@@ -768,9 +779,10 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
       const int32_t* row = p.block_table + size_t(b) * p.max_pages;
       const int32_t* sel = p.selected ? p.selected + (size_t(b) * hk + h) * p.k : nullptr;
       const int pages = (sq.n + B - 1) / B;
-      // this warp's stages of the segment: those whose number in the block is pw mod 4
-      for (int s0 = (pw - it) & 3; s0 < cnt && ok; s0 += 4 * looked) {
-        const int st = s0 + 4 * mine;
+      // this warp's stages of the segment: those whose number in the block is pw mod kCopiers
+      const int first = pw < kCopiers ? (pw + kCopiers - it % kCopiers) % kCopiers : cnt;
+      for (int s0 = first; s0 < cnt && ok; s0 += kCopiers * looked) {
+        const int st = s0 + kCopiers * mine;
         int blk = -1, r_lo = 0, r_hi = 0;
         if (st < cnt) {
           const int slot = (sq.first + i0 + st) * pps + e;
@@ -801,7 +813,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
           range[c] = min(16, max(0, r_lo - 16 * c)) | (min(16, max(0, r_hi - 16 * c)) << 8);
         const unsigned live = __ballot_sync(kFull, blk >= 0);
         if (bring) bring_query();
-        const int todo = min(looked, (cnt - s0 + 3) / 4);
+        const int todo = min(looked, (cnt - s0 + kCopiers - 1) / kCopiers);
         for (int x = 0; x < todo; ++x) {
           if (!mbar_wait_bounded(s_empty + s, phase)) ok = false;
           if (!__all_sync(kFull, ok)) {
@@ -830,7 +842,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
             bulk_g2s_hint(dst, ksrc, uint32_t(rec), s_full + s, pol);
             bulk_g2s_hint(dst + kStageBytes / 2, vsrc, uint32_t(rec), s_full + s, pol);
           }
-          s += 4;
+          s += kCopiers;
           if (s >= STAGES) {
             s -= STAGES;
             phase ^= 1;
@@ -846,7 +858,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
   }
 
   // ---------------- consumers ----------------
-  if constexpr (NT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kv_consumer_regs(NT)));
   const int g = lane >> 2, t = lane & 3, G = p.group;
   const LaneOff off = lane_off<FMT>(B, g, t);
   const uint32_t ring_at = smem_u32(ring);
@@ -958,8 +970,10 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
       consumers_sync<NT>();
       // a thread's items: float2 pairs of the 1024 floats, as the lanes laid them out
 #pragma unroll
-      for (int i = 0; i < 512 / (kKvWarps * 32); ++i) {
-        const int x = i * kKvWarps * 32 + tid, q4 = x >> 6, l2 = (x >> 1) & 31;
+      for (int i = 0; i < kItems; ++i) {
+        const int x = i * kKvWarps * 32 + tid;
+        if (512 % (kKvWarps * 32) != 0 && x >= 512) break;
+        const int q4 = x >> 6, l2 = (x >> 1) & 31;
         const int head = 8 * n + 2 * (l2 & 3) + (q4 >> 2);
         const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
         const float M = s_ref[head];
@@ -998,8 +1012,10 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 512 / (kKvWarps * 32); ++i) {
-            const int x = i * kKvWarps * 32 + tid, q4 = x >> 6, l2 = (x >> 1) & 31;
+          for (int i = 0; i < kItems; ++i) {
+            const int x = i * kKvWarps * 32 + tid;
+            if (512 % (kKvWarps * 32) != 0 && x >= 512) break;
+            const int q4 = x >> 6, l2 = (x >> 1) & 31;
             const int head = 8 * n + 2 * (l2 & 3) + (q4 >> 2);
             const int dim = 16 * (l2 >> 2) + 4 * (q4 & 3) + 2 * (x & 1);
             float M = kNone, L = 0.f;
@@ -1026,7 +1042,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
 
 template <int FMT, int NT>
 int launch_nt(const KvDecodeParams& p, cudaStream_t stream) {
-  constexpr size_t smem = size_t(kv_stages(FMT)) * kv_stage_bytes(FMT) + kv_merge_bytes(NT);
+  constexpr size_t smem = size_t(kv_stages(FMT, NT)) * kv_stage_bytes(FMT) + kv_merge_bytes(NT);
   static LaunchOnce once;
   if (!once.run([] {
         return cudaFuncSetAttribute(kv_decode_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
