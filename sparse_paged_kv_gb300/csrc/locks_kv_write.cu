@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
   const bool here = mbar_wait_bounded(&landed, 0);
   if (__syncthreads_or(!here)) {
     if (threadIdx.x == 0) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
+    mbar_wait_bounded(&landed, 0);                    // once more, for what is still in flight
     return;
   }
   if (seq < 0) return;                                // (whole warps)
