@@ -217,21 +217,26 @@ def load_library(path: Optional[str] = None):
 # marshalling helpers
 # --------------------------------------------------------------------------
 _torch = None                 # torch, from the first call that needs it
-_current_raw_stream = None    # device index -> cudaStream_t of torch's current stream
+_DTYPES = {}                  # its dtypes by name
+_current_device = None        # its current device's index
+_current_raw_stream = None    # device index -> cudaStream_t of its current stream
 
 
 def _load_torch():
     global _torch
     import torch
     _torch = torch
+    _DTYPES.update((n, getattr(torch, n)) for n in ("bfloat16", "float16", "float32", "int32"))
     return torch
 
 
 def _find_raw_stream():
-    """torch's own accessor where it has one (a microsecond less a call than building a
+    """torch's own accessors where it has them (a microsecond less a call than building a
     torch.cuda.Stream), else through the Stream object."""
-    global _current_raw_stream
+    global _current_raw_stream, _current_device
     torch = _load_torch()
+    torch.cuda.current_stream()                # (initialises CUDA, which the bare accessors do not)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     return _current_raw_stream
@@ -252,7 +257,7 @@ def _ptr(x) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         raw = _current_raw_stream or _find_raw_stream()
-        return raw(_torch.cuda.current_device())
+        return raw(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -374,8 +379,9 @@ def rope_frequencies(spec: locks_rope_spec_t) -> Tuple:
 
 def _typed(x, dtype: str, what: str):
     """x, if it is a tensor (or None, or a raw pointer) of the dtype of that name."""
-    if x is not None and type(x) is not int and \
-            x.dtype is not getattr(_torch or _load_torch(), dtype):
+    if _torch is None:
+        _load_torch()
+    if x is not None and type(x) is not int and x.dtype is not _DTYPES[dtype]:
         raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
     return x
 
@@ -384,15 +390,12 @@ def _sized(x, dtype: str, shape: Tuple, what: str) -> Optional[int]:
     """Pointer of a contiguous device tensor of that type and shape; None stays None."""
     if x is None or type(x) is int:
         return x
-    if x.dtype is not getattr(_torch or _load_torch(), dtype):
-        raise ValueError(f"{what}: a {dtype} tensor expected, got {x.dtype}")
+    if x.shape == shape and x.dtype is _DTYPES.get(dtype) and x.is_cuda and x.is_contiguous():
+        return x.data_ptr()
+    _typed(x, dtype, what)                     # the call's first tensor, or a wrong one: say which
     if x.shape != shape:
         raise ValueError(f"{what}: shape {shape} expected, got {tuple(x.shape)}")
-    if not x.is_cuda:
-        raise ValueError(f"{what}: device tensor expected")
-    if not x.is_contiguous():
-        raise ValueError(f"{what}: contiguous tensor expected")
-    return x.data_ptr()
+    return _ptr(x)
 
 
 def _pool(x, cfg: LocksKvConfig, what: str) -> Optional[int]:
