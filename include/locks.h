@@ -482,7 +482,9 @@ int locks_kv_read(const locks_kv_cfg_t* cfg, const void* k_pool, const void* v_p
                   const int32_t* block_ids, int32_t n_blocks, void* k_out, void* v_out,
                   int32_t* status, void* stream);
 
-/* Bytes of workspace locks_kv_decode needs for this cfg. */
+/* Bytes of workspace locks_kv_decode needs for this cfg: one of two sizes, by
+ * whether G exceeds 8.  Configurations may share a workspace that is large
+ * enough for each (calls on it one after the other). */
 size_t locks_kv_decode_workspace_bytes(const locks_kv_cfg_t* cfg);
 
 /*

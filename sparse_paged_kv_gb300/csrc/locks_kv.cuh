@@ -84,7 +84,7 @@ struct KvDecodeParams {
 int launch_rope(RopeParams p, int dtype, cudaStream_t stream);
 int launch_kv_write(KvWriteParams p, int fmt, cudaStream_t stream);
 int launch_kv_read(const KvReadParams& p, int fmt, cudaStream_t stream);
-size_t kv_decode_workspace(int batch, int n_kv_heads, int group);
+size_t kv_decode_workspace(int group);
 int launch_kv_decode(const KvDecodeParams& p, int fmt, cudaStream_t stream);
 
 // A kernel attribute holds for the device it was set on: `run` calls set() on

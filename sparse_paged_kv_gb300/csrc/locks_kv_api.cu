@@ -59,7 +59,7 @@ size_t locks_kv_record_bytes(const locks_kv_cfg_t* cfg) {
 
 size_t locks_kv_decode_workspace_bytes(const locks_kv_cfg_t* cfg) {
   if (check_kv_cfg(cfg) != LOCKS_OK) return 0;
-  return locks::kv_decode_workspace(cfg->batch, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads);
+  return locks::kv_decode_workspace(cfg->n_q_heads / cfg->n_kv_heads);
 }
 
 int locks_rope(const locks_rope_table_t* rope, int32_t dtype, int32_t head_dim, const void* x,

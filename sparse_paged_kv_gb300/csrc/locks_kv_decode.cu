@@ -18,7 +18,7 @@
 // one that is cut is left as partials (running maximum, sum, weighted values) in
 // the workspace, and the last of its blocks to arrive (atomic ticket) merges them
 // in the blocks' order, so results do not depend on the order of arrival.  The
-// workspace is about a megabyte for any shape.
+// workspace is a megabyte or two whatever the shape, and shapes may share it.
 //
 // Block.  Four producer warps take the stages in turn: each looks up its next
 // pages (one a lane) and copies their K and V records (cp.async.bulk, one
@@ -36,7 +36,7 @@
 // Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 314 us (7.05 TB/s), 8 x
 // 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 120 us (5.0 TB/s): instructions,
 // 370 for 16 tokens of a head, of which the unpacking of codes is over half.  One
-// sequence of 1000 tokens 9.3 us: a chain of latencies.
+// sequence of 1000 tokens 9.5 us: a chain of latencies.
 #include "locks_kv.cuh"
 
 namespace locks {
@@ -69,6 +69,9 @@ constexpr float kNone = -3.402823466e38f;         // running maximum before any 
 // merge buffer: the warps' states of 8 heads x 128 floats
 constexpr int kv_merge_bytes(int nt) { return kv_warps(nt) * 4096; }
 
+// workspace: a ticket and two partials a block
+constexpr size_t kTicketBytes = 1024;
+static_assert(kSms * sizeof(int) <= kTicketBytes, "tickets");
 __host__ __device__ constexpr size_t kv_part_bytes(int nt) { return size_t(nt) * (4096 + 64); }
 
 __host__ __device__ constexpr int kv_stage_bytes(int fmt) {
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     // ---- merge the warps' states; finish the unit or leave a partial ----
     const int u_lo = u + fixed, u_hi = u_lo + sq.stages;     // its stages in the list
     const bool alone = u_lo >= w_lo && u_hi <= w_hi;
-    float* parts = reinterpret_cast<float*>(p.ws + (size_t(p.batch) * hk * 4 + 255) / 256 * 256);
+    float* parts = reinterpret_cast<float*>(p.ws + kTicketBytes);
     // a block's first partial goes on with an earlier block's unit, its second begins one
     float* part = parts + (size_t(blockIdx.x) * 2 + (u_lo >= w_lo)) * (kv_part_bytes(NT) / 4);
     __syncwarp();
@@ -939,6 +942,9 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
       for (int j = 0; j < 2 * NT; ++j) s_m[warp][8 * (j >> 1) + 2 * t + (j & 1)] = st.m[j];
     }
     consumers_sync<NT>();                         // (and the buffer's last readers are done)
+    if (!alone && tid == 0)                       // the blocks of the unit's first and last stage
+      s_join = m ? make_int2(u / most * m, u / most * m + m - 1)
+                 : make_int2(block_of(u_lo, N, W), block_of(u_hi - 1, N, W));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float2 M = make_float2(kNone, kNone);
@@ -997,14 +1003,11 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
     }
     if (!alone) {
       consumers_sync<NT>();
-      int* ticket = reinterpret_cast<int*>(p.ws) + unit;
       if (tid == 0) {
-        // releases this block's partial (ordered before by the barrier), acquires the others'
-        const int before = ticket_add(ticket);
-        // the blocks of the unit's first and last stage
-        const int c_lo = m ? u / most * m : block_of(u_lo, N, W);
-        const int c_hi = m ? c_lo + m - 1 : block_of(u_hi - 1, N, W);
-        s_join = before == c_hi - c_lo ? make_int2(c_lo, c_hi) : make_int2(0, -1);
+        // at most one unit begins in a block and goes on beyond it: its ticket is that block's.
+        // Releases this block's partial (ordered before by the barrier), acquires the others'
+        const int before = ticket_add(reinterpret_cast<int*>(p.ws) + s_join.x);
+        if (before != s_join.y - s_join.x) s_join.y = -1;
       }
       consumers_sync<NT>();
       const int c_lo = s_join.x, c_hi = s_join.y;
@@ -1025,7 +1028,7 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
             else join_partials<NT, 16>(parts, c_lo, c_hi, head, n * 512 + x, A, M, L);
             if (head < G) store_out(p, size_t(unit) * G + head, dim, A, M, L);
           }
-        if (tid == 0) *ticket = 0;
+        if (tid == 0) reinterpret_cast<int*>(p.ws)[c_lo] = 0;
       }
     }
     ++seg;
@@ -1059,10 +1062,8 @@ int launch_fmt(const KvDecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t kv_decode_workspace(int batch, int n_kv_heads, int group) {
-  const int nt = group <= 8 ? 1 : 2;
-  return (size_t(batch) * n_kv_heads * 4 + 255) / 256 * 256 +
-         size_t(kSms) * 2 * kv_part_bytes(nt);
+size_t kv_decode_workspace(int group) {
+  return kTicketBytes + size_t(kSms) * 2 * kv_part_bytes(group <= 8 ? 1 : 2);
 }
 
 int launch_kv_decode(const KvDecodeParams& p, int fmt, cudaStream_t stream) {

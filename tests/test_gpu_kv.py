@@ -690,3 +690,19 @@ def test_decode_equal_lengths(name, fmt, batch, hkv, n):
     lens[batch // 2] = 0
     c = Cache(fmt, 32, lens, hkv * 2, hkv, seed=n)
     c.check(c.run())
+
+
+def test_decode_shapes_share_a_workspace():
+    """Calls of other batches, groups and formats in between change nothing."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    shapes = [(R.F8, 64, [5000, 300], 8, 2), (R.I4, 16, [700] * 60, 4, 1), (R.I8, 32, [9000], 32, 2),
+              (R.I4, 64, [3, 0, 20000], 16, 4)]
+    caches = [Cache(f, p, n, hq, hkv, seed=i) for i, (f, p, n, hq, hkv) in enumerate(shapes)]
+    ws = torch.zeros(max(B.kv_decode_workspace_bytes(c.cfg) for c in caches), dtype=torch.uint8, device="cuda")
+    first = [c.run(ws=ws) for c in caches]
+    for c, got in zip(caches, first):
+        c.check(got)
+    for i in (2, 0, 3, 1, 0, 2, 1, 3, 3, 1):
+        again = caches[i].run(ws=ws)
+        assert torch.equal(again[0], first[i][0]) and torch.equal(again[1], first[i][1])
