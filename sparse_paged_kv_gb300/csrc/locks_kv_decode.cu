@@ -520,14 +520,21 @@ __device__ __forceinline__ int block_of(int x, int N, int W) {
   return c;
 }
 
-// The unit after (b, h), which starts at u in the list.
+// The unit after (b, h), which starts at u in the list.  Shares end where the list
+// does, so there is one; should the lengths change under the call, the walk still
+// ends with the batch.
 __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& sq, int& h, int& u,
                                           int end, int fixed) {
   u += sq.cost(fixed);
   if (++h < p.n_kv_heads || u >= end) return;     // (beyond `end` there may be no sequence)
   h = 0;
-  do sq = seq_of(p, ++b);
-  while (sq.stages == 0);
+  do {
+    if (++b >= p.batch) {
+      u = end;
+      return;
+    }
+    sq = seq_of(p, b);
+  } while (sq.stages == 0);
 }
 
 // A unit's query for heads h0 .. h0 + 7 (lane 4g + t: head h0 + g, dims 32t ..
@@ -704,7 +711,8 @@ __global__ void __launch_bounds__(kv_threads(NT), 1) kv_decode_kernel(const KvDe
   if (float(most) * float(kSms - m * all_units) > kEndCost * float(m * all_units)) m = 0;
   const int fixed = m ? 0 : kUnitCost;
   const int W = all_stages + fixed * all_units;
-  const int N = m ? m * all_units : min(kSms, max(W, 1));
+  // blocks with a share: none when every sequence is empty (W = 0)
+  const int N = m ? m * all_units : min(kSms, W);
   int w_lo = 0, w_hi = 0;
   if (int(blockIdx.x) < N) {
     if (m) {

@@ -1,0 +1,81 @@
+"""Edges of the quantised cache's calls on the GPU: batches with nothing to attend."""
+import numpy as np
+import pytest
+
+from tests import kv_ref as R
+from tests.test_gpu_kv import Cache
+
+pytestmark = pytest.mark.gpu
+
+FMTS = sorted(R.FORMATS.items())
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import torch
+    from sparse_paged_kv_gb300 import binding, build_lib
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    binding.load_library(build_lib.build())
+
+
+def decode(c, lens, selected=None, window=0):
+    """One call with these lengths, which lie in a longer array: (out, lse, status)."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    batch = c.cfg.batch
+    n = torch.full((batch + 64,), 1, dtype=torch.int32, device="cuda")
+    n[:batch] = torch.tensor(lens, dtype=torch.int32)
+    out = torch.full((batch, c.hq, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((batch, c.hq), 9.0, device="cuda")
+    ws = torch.zeros(B.kv_decode_workspace_bytes(c.cfg), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(c.q).bfloat16().cuda()
+    table = torch.from_numpy(c.table).cuda()
+    if selected is not None:
+        selected = torch.from_numpy(selected).cuda()
+    B.locks_kv_decode(c.cfg, q, c.dev[0], c.dev[1], table, n[:batch], out, ws, selected=selected,
+                      window=window, out_lse=lse, status=status)
+    return out, lse, status.item()
+
+
+@pytest.mark.parametrize("how", ["dense", "listed", "window"])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (1, 1), (32, 2)])
+@pytest.mark.parametrize("batch", [1, 3, 200])
+@pytest.mark.parametrize("name,fmt", FMTS)
+def test_a_batch_of_empty_sequences(name, fmt, batch, hq, hkv, how):
+    """Every length 0: zeros and -inf in every row, whatever the form of the call."""
+    c = Cache(fmt, 16, [0] * batch, hq, hkv, seed=batch)
+    sel = np.zeros((batch, hkv, 5), np.int32) if how == "listed" else None
+    out, lse, status = decode(c, [0] * batch, selected=sel, window=7 if how == "window" else 0)
+    assert status == 0
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+@pytest.mark.parametrize("batch", [1, 40])
+def test_a_batch_of_negative_lengths(batch):
+    """They count as 0, with a flag."""
+    from sparse_paged_kv_gb300 import binding as B
+    c = Cache(R.F8, 64, [0] * batch, 8, 2, seed=1)
+    out, lse, status = decode(c, [-3] * batch)
+    assert status == B.LOCKS_DEV_BAD_SEQ_LEN
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+def test_attention_over_a_cache_that_holds_nothing_yet():
+    """A new QuantCache attends nothing; after a token it attends that one."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    from sparse_paged_kv_gb300 import runtime
+    cfg = B.LocksKvConfig(batch=2, n_q_heads=4, n_kv_heads=2, head_dim=128, page_size=16, max_pages=2,
+                          num_blocks=4, kv_dtype=R.I8)
+    cache = runtime.QuantCache(cfg, np.arange(4).reshape(2, 2))
+    cache.attend()
+    assert (cache.out == 0).all() and (cache.out_lse == float("-inf")).all()
+    x = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    cache.step(x[:, :4], x[:, 4:6], x[:, 6:])
+    want = cache.read(cache.block_table[:, 0].contiguous())[1][:, :, 0].repeat_interleave(2, 1)
+    # one token: its weight is 1 (2^-11 in f16, 2^-20 from the exponential) and the result rounds to
+    # bf16, as the value read back does
+    assert ((cache.out.float() - want.float()).abs() <= want.float().abs() * (2 * 2.0 ** -8 + 2.0 ** -10)).all()
+    assert cache.status.item() == 0
