@@ -324,7 +324,8 @@ class QuantCache:
     # ---- summaries ------------------------------------------------------------------
     def build(self, block_ids, pages_at_once: int = 1024, stream=None):
         """Summaries of complete pages (int32 block ids on the device; entries < 0 are
-        skipped), from their keys as the cache holds them."""
+        skipped, those past the pool also flagged in status), from their keys as the cache
+        holds them."""
         torch, c = self.torch, self.locks_cfg
         with self._on(stream):
             for at in range(0, block_ids.numel(), pages_at_once):
@@ -334,7 +335,8 @@ class QuantCache:
                 pages = self.read(ids, values=False)
                 made = torch.zeros((n, *self.summaries.shape[1:]), dtype=torch.uint8,
                                    device=self.device)
-                there = ids >= 0
+                # (the read has flagged the ids past the pool, which the copy below must not see)
+                there = (ids >= 0) & (ids < c.num_blocks)
                 slots = torch.where(there, torch.arange(n, dtype=torch.int32, device=self.device), -1)
                 B.locks_build_completed(cfg, pages, slots, made)
                 self.summaries.index_copy_(0, torch.where(there, ids, c.num_blocks).long(), made)

@@ -1,4 +1,5 @@
-"""Edges of the quantised cache's calls on the GPU: batches with nothing to attend."""
+"""Edges of the quantised cache's calls on the GPU: batches with nothing to attend,
+block ids outside the pool."""
 import numpy as np
 import pytest
 
@@ -79,3 +80,25 @@ def test_attention_over_a_cache_that_holds_nothing_yet():
     # bf16, as the value read back does
     assert ((cache.out.float() - want.float()).abs() <= want.float().abs() * (2 * 2.0 ** -8 + 2.0 ** -10)).all()
     assert cache.status.item() == 0
+
+
+@pytest.mark.parametrize("name,fmt", FMTS)
+def test_build_skips_block_ids_outside_the_pool(name, fmt):
+    """Flagged; the other summaries are those of a build without them, and no other changes."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    from sparse_paged_kv_gb300 import runtime
+    page, hkv, blocks = 16, 2, 7
+    cfg = B.LocksKvConfig(batch=1, n_q_heads=4, n_kv_heads=hkv, head_dim=128, page_size=page, max_pages=6,
+                          num_blocks=blocks, kv_dtype=fmt)
+    caches = [runtime.QuantCache(cfg, np.arange(6).reshape(1, 6), budget_tokens=4 * page) for _ in range(2)]
+    x = torch.randn(6 * page, 2 * hkv, 128, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    pos = torch.arange(6 * page).int().cuda()
+    for c, ids in zip(caches, ([3, 0, 5], [-1, 3, blocks, 0, blocks + 5, 2 ** 31 - 1, 5, -2 ** 31])):
+        c.write(None, x[:, :hkv], x[:, hkv:], torch.zeros_like(pos), pos)
+        c.summaries.fill_(99)
+        c.build(torch.tensor(ids, dtype=torch.int32).cuda())
+    a, b = caches
+    assert a.status.item() == 0 and b.status.item() == B.LOCKS_DEV_BAD_BLOCK_ID
+    assert torch.equal(a.summaries[:blocks], b.summaries[:blocks])
+    assert (b.summaries[[1, 2, 4, 6]] == 99).all() and (b.summaries[0] != 99).any()

@@ -1,0 +1,63 @@
+"""runtime.QuantCache and the binding on the host: what they hand to the kernels, with the kernels
+replaced by recorders (no GPU)."""
+import numpy as np
+import pytest
+
+from sparse_paged_kv_gb300 import binding as B
+from sparse_paged_kv_gb300 import build_lib, runtime
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    B.load_library(build_lib.build())
+
+
+def make(blocks=6, budget=64, page=16, batch=2, hq=4, hkv=2):
+    cfg = B.LocksKvConfig(batch=batch, n_q_heads=hq, n_kv_heads=hkv, head_dim=128, page_size=page,
+                          max_pages=3, num_blocks=blocks, kv_dtype=B.LOCKS_KV_I4)
+    table = np.arange(batch * 3).reshape(batch, 3) % blocks
+    return runtime.QuantCache(cfg, table, budget_tokens=budget, device="cpu")
+
+
+def fake_kernels(monkeypatch):
+    """locks_kv_read and locks_build_completed on the CPU: a page holds its block's number, a
+    summary the page's number + 1 in every byte; entries outside the pool are skipped and flagged."""
+    def read(cfg, k_pool, v_pool, block_ids, k_out, v_out, status=None, stream=None):
+        for i, b in enumerate(block_ids.tolist()):
+            if b >= cfg.num_blocks:
+                status |= B.LOCKS_DEV_BAD_BLOCK_ID
+            elif b >= 0:
+                k_out[i] = float(b)
+
+    def build(cfg, pages, completed, summaries, **kw):
+        assert pages.shape[0] == cfg.num_blocks == summaries.shape[0]
+        for i, slot in enumerate(completed.tolist()):
+            assert -1 <= slot < cfg.num_blocks
+            if slot >= 0:
+                summaries[slot] = int(pages[slot, 0, 0, 0].item()) + 1
+
+    monkeypatch.setattr(B, "locks_kv_read", read)
+    monkeypatch.setattr(B, "locks_build_completed", build)
+
+
+@pytest.mark.parametrize("at_once", [1, 2, 1024])
+def test_build_skips_block_ids_outside_the_pool(monkeypatch, at_once):
+    """They are flagged, as in every call, and touch no summary (the spare row included)."""
+    import torch
+    fake_kernels(monkeypatch)
+    cache = make()
+    cache.summaries.fill_(99)
+    ids = torch.tensor([4, -1, 6, 1, 11, 2 ** 31 - 1, -2 ** 31, 0], dtype=torch.int32)
+    cache.build(ids, pages_at_once=at_once)
+    assert cache.status.item() == B.LOCKS_DEV_BAD_BLOCK_ID
+    assert [int(cache.summaries[b].unique()) for b in (0, 1, 4)] == [1, 2, 5]
+    assert (cache.summaries[[2, 3, 5]] == 99).all()
+
+
+def test_build_of_valid_blocks_flags_nothing(monkeypatch):
+    import torch
+    fake_kernels(monkeypatch)
+    cache = make()
+    cache.build(torch.tensor([5, 3, -1], dtype=torch.int32))
+    assert cache.status.item() == 0
+    assert [int(cache.summaries[b].unique()) for b in (3, 5)] == [4, 6]
