@@ -305,17 +305,21 @@ class QuantCache:
 
     def capture_step(self, q, k, v, window: int = 0):
         """A CUDA graph of step() over these buffers: fill q, k, v and replay.  The step runs
-        once before the capture, on the sequences as they are, and its token is taken back
-        (lengths restored; the slot is written again by the first replay)."""
+        once before the capture, on the sequences as they are, and is taken back: every buffer
+        of a step holds what it held (a list of completed pages that is still to be built, for
+        one), but the token's slots in the pools, which the first replay writes again, and the
+        bits in status."""
         torch = self.torch
-        keep = self.seq_lens.clone()
+        held = [(x, x.clone()) for x in (self.seq_lens, self.completed, self.positions, self.q,
+                                         self.out, self.out_lse, self.selected) if x is not None]
         cur = torch.cuda.current_stream(self.device)
         side = torch.cuda.Stream(device=self.device)
         side.wait_stream(cur)
         with torch.cuda.stream(side):
             self.step(q, k, v, window)
         cur.wait_stream(side)
-        self.seq_lens.copy_(keep)
+        for x, before in held:
+            x.copy_(before)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             self.step(q, k, v, window)

@@ -1,5 +1,5 @@
 """Edges of the quantised cache's calls on the GPU: batches with nothing to attend,
-block ids outside the pool."""
+block ids outside the pool, the captured step."""
 import numpy as np
 import pytest
 
@@ -102,3 +102,66 @@ def test_build_skips_block_ids_outside_the_pool(name, fmt):
     assert a.status.item() == 0 and b.status.item() == B.LOCKS_DEV_BAD_BLOCK_ID
     assert torch.equal(a.summaries[:blocks], b.summaries[:blocks])
     assert (b.summaries[[1, 2, 4, 6]] == 99).all() and (b.summaries[0] != 99).any()
+
+
+def _budgeted(lens, page=16, pages=8, hq=4, hkv=2, budget=3 * 16):
+    """A cache with a budget, its prompts written and their complete pages summarised."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    from sparse_paged_kv_gb300 import runtime
+    batch = len(lens)
+    cfg = B.LocksKvConfig(batch=batch, n_q_heads=hq, n_kv_heads=hkv, head_dim=128, page_size=page,
+                          max_pages=pages, num_blocks=batch * pages, kv_dtype=R.I8)
+    cache = runtime.QuantCache(cfg, np.arange(batch * pages).reshape(batch, pages), rope=runtime.RopeTable(128),
+                               budget_tokens=budget)
+    n = sum(lens)
+    x = torch.randn(n, 2 * hkv, 128, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    seq = torch.cat([torch.full((m,), b) for b, m in enumerate(lens)]).int().cuda()
+    pos = torch.cat([torch.arange(m) for m in lens]).int().cuda()
+    cache.write(None, x[:, :hkv], x[:, hkv:], seq, pos)
+    cache.build(torch.cat([cache.block_table[b, :m // page] for b, m in enumerate(lens)]))
+    return cache
+
+
+def _token(batch, seed, hq=4, hkv=2):
+    import torch
+    return torch.randn(batch, hq + 2 * hkv, 128, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+def test_capture_takes_back_what_its_first_step_wrote():
+    """Lengths, completed pages, the query and the outputs are what they were before."""
+    import torch
+    cache = _budgeted([79, 90])
+    x = _token(2, 1)
+    cache.step(x[:, :4], x[:, 4:6], x[:, 6:])                # sequence 0 completes page 4
+    names = ("seq_lens", "completed", "positions", "q", "out", "out_lse", "selected", "summaries")
+    before = {n: getattr(cache, n).clone() for n in names}
+    assert before["completed"].tolist() == [4, -1]
+    x.copy_(_token(2, 2))
+    cache.capture_step(x[:, :4], x[:, 4:6], x[:, 6:])
+    torch.cuda.synchronize()
+    for n in names:
+        assert torch.equal(getattr(cache, n), before[n]), n
+
+
+@pytest.mark.parametrize("lens", [[79, 95], [80, 94]])
+def test_captured_budgeted_steps_equal_single_ones(lens):
+    """From one below a page border and from just behind it, the captured step with the summaries of
+    completed pages built before and between its replays gives the bits of steps run one by one."""
+    import torch
+    a, b = _budgeted(lens), _budgeted(lens)
+    x = _token(2, 0)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    for c in (a, b):
+        c.step(q, k, v)                                     # may complete a page, not summarised yet
+    x.copy_(_token(2, 50))
+    graph = a.capture_step(q, k, v)
+    for s in range(18):
+        a.build_completed()
+        b.build_completed()
+        x.copy_(_token(2, 100 + s))
+        graph.replay()
+        b.step(q, k, v)
+        for n in ("seq_lens", "completed", "selected", "q", "out", "out_lse", "summaries", "k_pool", "v_pool"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), (s, n)
+    assert a.status.item() == 0 and b.status.item() == 0
