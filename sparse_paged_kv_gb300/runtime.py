@@ -351,7 +351,13 @@ class QuantCache:
         self.build(self.completed, stream=stream)
 
     def _on(self, stream):
-        return self.torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+        """Torch's work on `stream`: a torch stream, a cudaStream_t as an integer, or None."""
+        if stream is None:
+            return contextlib.nullcontext()
+        cuda = self.torch.cuda
+        if isinstance(stream, int):
+            stream = cuda.ExternalStream(stream) if stream else cuda.default_stream()
+        return cuda.stream(stream)
 
 
 class DecodeLoop:

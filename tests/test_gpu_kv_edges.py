@@ -1,5 +1,5 @@
 """Edges of the quantised cache's calls on the GPU: batches with nothing to attend,
-block ids outside the pool, the captured step."""
+block ids outside the pool, the captured step, raw stream handles."""
 import numpy as np
 import pytest
 
@@ -165,3 +165,28 @@ def test_captured_budgeted_steps_equal_single_ones(lens):
         for n in ("seq_lens", "completed", "selected", "q", "out", "out_lse", "summaries", "k_pool", "v_pool"):
             assert torch.equal(getattr(a, n), getattr(b, n)), (s, n)
     assert a.status.item() == 0 and b.status.item() == 0
+
+
+def test_calls_take_a_raw_stream_handle():
+    """An integer cudaStream_t wherever a stream is taken, the default stream's 0 too."""
+    import torch
+    a, b = _budgeted([79, 30]), _budgeted([79, 30])
+    side = torch.cuda.Stream()
+    for handle in (side.cuda_stream, 0):
+        torch.cuda.synchronize()
+        for s in range(3):
+            x = _token(2, 700 + s)
+            q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+            a.step(q, k, v)
+            a.build_completed()
+            torch.cuda.synchronize()
+            b.step(q, k, v, stream=handle)
+            b.build_completed(stream=handle)
+            b.attend(stream=handle)
+            page = b.read(b.block_table[0, :2].contiguous(), stream=handle)
+            torch.cuda.synchronize()
+            a.attend()
+            want = a.read(a.block_table[0, :2].contiguous())
+            assert torch.equal(page[0], want[0]) and torch.equal(page[1], want[1])
+            for n in ("out", "out_lse", "summaries", "k_pool", "v_pool", "completed"):
+                assert torch.equal(getattr(a, n), getattr(b, n)), (handle, s, n)
