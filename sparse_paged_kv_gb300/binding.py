@@ -13,7 +13,7 @@ import ctypes
 import functools
 import math
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -139,6 +139,10 @@ class LocksKvConfig:
                            self.page_size, self.max_pages, self.num_blocks, self.kv_dtype)
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "ref", ctypes.byref(c))
+
+    def __reduce__(self):
+        # made anew from its fields: a reference to a C structure can't be copied or sent
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
     def c(self) -> locks_kv_cfg_t:
         return self._c

@@ -61,3 +61,22 @@ def test_build_of_valid_blocks_flags_nothing(monkeypatch):
     cache.build(torch.tensor([5, 3, -1], dtype=torch.int32))
     assert cache.status.item() == 0
     assert [int(cache.summaries[b].unique()) for b in (3, 5)] == [4, 6]
+
+
+@pytest.mark.parametrize("how", ["pickle", "copy", "deepcopy"])
+def test_configurations_can_be_copied_and_sent(how):
+    """To another process, say: the copy is equal, works, and has a C structure of its own."""
+    import copy
+    import dataclasses
+    import pickle
+    again = {"pickle": lambda x: pickle.loads(pickle.dumps(x)), "copy": copy.copy,
+             "deepcopy": copy.deepcopy}[how]
+    cache = make()
+    c = cache.cfg
+    assert c.pool_bytes > 0                                # (kept in the instance from here on)
+    d = again(c)
+    assert d == c and hash(d) == hash(c) and type(d) is type(c)
+    assert d.c() is not c.c() and bytes(d.c()) == bytes(c.c())
+    assert B.kv_record_bytes(d) == B.kv_record_bytes(c) and d.pool_bytes == c.pool_bytes
+    assert dataclasses.replace(d, batch=5).c().batch == 5
+    assert again(cache.locks_cfg) == cache.locks_cfg
