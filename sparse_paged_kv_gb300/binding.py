@@ -229,8 +229,8 @@ _current_raw_stream = None    # device index -> cudaStream_t of its current stre
 def _load_torch():
     global _torch
     import torch
-    _torch = torch
     _DTYPES.update((n, getattr(torch, n)) for n in ("bfloat16", "float16", "float32", "int32"))
+    _torch = torch                             # last: another thread's call may look at it now
     return torch
 
 

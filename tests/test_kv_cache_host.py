@@ -80,3 +80,34 @@ def test_configurations_can_be_copied_and_sent(how):
     assert B.kv_record_bytes(d) == B.kv_record_bytes(c) and d.pool_bytes == c.pool_bytes
     assert dataclasses.replace(d, batch=5).c().batch == 5
     assert again(cache.locks_cfg) == cache.locks_cfg
+
+
+def test_a_first_call_in_another_thread_finds_the_types(monkeypatch):
+    """Torch is published once its types are there: a thread that comes in between checks the
+    same tensor as the one that loads it."""
+    import threading
+
+    import torch
+    errors = []
+
+    def check():
+        try:
+            B._typed(torch.zeros(1, dtype=torch.int32), "int32", "x")
+        except Exception as e:
+            errors.append(e)
+
+    class Types(dict):
+        def update(self, *a, **kw):                       # the moment at which they are filled in
+            if not self.entered:
+                self.entered = True
+                other = threading.Thread(target=check)
+                other.start()
+                other.join(10)
+            super().update(*a, **kw)
+
+    types = Types()
+    types.entered = False
+    monkeypatch.setattr(B, "_torch", None)
+    monkeypatch.setattr(B, "_DTYPES", types)
+    check()
+    assert errors == [] and types.entered and B._torch is torch
