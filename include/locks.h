@@ -305,7 +305,8 @@ int locks_select_noalloc(const locks_cfg_t* cfg, const void* q, const void* summ
  * max_pages < 2^24; num_blocks * n_kv_heads < 2^31; batch * n_kv_heads < 2^24;
  * and for the attention batch * n_kv_heads * (ceil(max_pages * page_size / 64) + 8)
  * < 2^31 (with a page list, k in place of max_pages, k < 2^24); at most 2^30
- * tokens a write.
+ * tokens a write, of at most 2^16 rows each (2 n_kv_heads, and n_q_heads where
+ * queries are passed).
  * =========================================================================== */
 
 /* element type of a quantised cache */

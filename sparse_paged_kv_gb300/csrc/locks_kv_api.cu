@@ -9,6 +9,8 @@ namespace {
 
 using locks::kHeadDim;
 
+constexpr int64_t kMaxWriteRows = 1 << 16;     // of a token: query, key and value heads
+
 bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15; }
 
 int check_kv_cfg(const locks_kv_cfg_t* c) {
@@ -112,6 +114,9 @@ int locks_kv_write(const locks_kv_cfg_t* cfg, const void* k_new, int64_t k_strid
     return LOCKS_ERR_INVALID_ARG;
   if (!token_seq && n_tokens > cfg->batch) return LOCKS_ERR_INVALID_ARG;
   if (n_tokens > (1 << 30)) return LOCKS_ERR_UNSUPPORTED;     // token numbers are ints, rounded up to groups
+  // and so are a token's rows and their shares, rows * shares of 16 rows
+  if ((q_new ? int64_t(cfg->n_q_heads) : 0) + 2 * int64_t(cfg->n_kv_heads) > kMaxWriteRows)
+    return LOCKS_ERR_UNSUPPORTED;
   if (misaligned(k_new) || misaligned(v_new) || misaligned(k_pool) || misaligned(v_pool) ||
       misaligned(q_new) || misaligned(q_out) || k_stride % 8 || v_stride % 8 ||
       (q_new && q_stride % 8))

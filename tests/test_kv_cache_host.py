@@ -111,3 +111,19 @@ def test_a_first_call_in_another_thread_finds_the_types(monkeypatch):
     monkeypatch.setattr(B, "_DTYPES", types)
     check()
     assert errors == [] and types.entered and B._torch is torch
+
+FAKE = 0x10000   # never dereferenced: every call below returns before a launch
+
+
+@pytest.mark.parametrize("hq,hkv,with_q", [(1 << 23, 1 << 22, True), (1 << 16, 1 << 16, False),
+                                           ((1 << 15) + 1, (1 << 15) + 1, False), (7 << 13, 1 << 13, True)])
+def test_write_refuses_more_rows_a_token_than_it_can_number(hq, hkv, with_q):
+    """2^16 rows of a token (its key, its value and, where they are passed, its query heads), less
+    than any of these has."""
+    c = B.LocksKvConfig(batch=1, n_q_heads=hq, n_kv_heads=hkv, head_dim=128, page_size=64, max_pages=4,
+                        num_blocks=1, kv_dtype=B.LOCKS_KV_F8)
+    q, q_out = (FAKE, FAKE + 16) if with_q else (None, None)
+    assert B.kv_record_bytes(c) > 0                        # (the other calls take it)
+    assert B.load_library().locks_kv_write(
+        c.ref, FAKE, hkv * 128, FAKE, hkv * 128, q, hq * 128, q_out, FAKE, FAKE, 2, None, FAKE, FAKE, FAKE,
+        None, None, None, None) == B.LOCKS_ERR_UNSUPPORTED
