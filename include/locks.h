@@ -420,6 +420,7 @@ typedef struct locks_rope_table {
  * in float32, rounded once.
  *
  *   head_dim          even, 2 .. 512; rope->rotary_dim <= head_dim
+ *   n_heads           at most 2^24
  *   x, out            [n_tokens][n_heads][head_dim] of dtype, strides in
  *                     elements between tokens and between heads (the last dim
  *                     is contiguous); out may be x with the same strides, and

@@ -72,7 +72,8 @@ int locks_rope(const locks_rope_table_t* rope, int32_t dtype, int32_t head_dim, 
   if (dtype != LOCKS_BF16 && dtype != LOCKS_F16 && dtype != LOCKS_F32) return LOCKS_ERR_INVALID_ARG;
   const int rc = check_rope(rope, head_dim);
   if (rc != LOCKS_OK) return rc;
-  if (head_dim > 512) return LOCKS_ERR_UNSUPPORTED;
+  // (a thread's next head is as many heads on as the others take: an int)
+  if (head_dim > 512 || n_heads > (1 << 24)) return LOCKS_ERR_UNSUPPORTED;
   if (n_tokens == 0 || n_heads == 0) return LOCKS_OK;
   if (!x || !positions || !out) return LOCKS_ERR_INVALID_ARG;
   const uintptr_t size = dtype == LOCKS_F32 ? 4 : 2;

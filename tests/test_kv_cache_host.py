@@ -127,3 +127,12 @@ def test_write_refuses_more_rows_a_token_than_it_can_number(hq, hkv, with_q):
     assert B.load_library().locks_kv_write(
         c.ref, FAKE, hkv * 128, FAKE, hkv * 128, q, hq * 128, q_out, FAKE, FAKE, 2, None, FAKE, FAKE, FAKE,
         None, None, None, None) == B.LOCKS_ERR_UNSUPPORTED
+
+
+def test_rope_refuses_more_heads_than_it_can_number():
+    """2^24 heads: the strides between a thread's heads stay far from 32 bits."""
+    import ctypes
+    table = ctypes.byref(B.locks_rope_table_t(FAKE, 2, 0, 1.0))
+    for heads in ((1 << 24) + 1, (1 << 31) - 1):
+        assert B.load_library().locks_rope(table, B.LOCKS_BF16, 2, FAKE, heads * 2, 2, FAKE, 1, heads, FAKE,
+                                           heads * 2, 2, 0, None) == B.LOCKS_ERR_UNSUPPORTED
