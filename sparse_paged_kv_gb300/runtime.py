@@ -330,6 +330,8 @@ class QuantCache:
         """Summaries of complete pages (int32 block ids on the device; entries < 0 are
         skipped, those past the pool also flagged in status), from their keys as the cache
         holds them."""
+        if self.selected is None:
+            raise ValueError("a QuantCache made without budget_tokens keeps no summaries")
         torch, c = self.torch, self.locks_cfg
         with self._on(stream):
             for at in range(0, block_ids.numel(), pages_at_once):

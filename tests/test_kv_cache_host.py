@@ -136,3 +136,12 @@ def test_rope_refuses_more_heads_than_it_can_number():
     for heads in ((1 << 24) + 1, (1 << 31) - 1):
         assert B.load_library().locks_rope(table, B.LOCKS_BF16, 2, FAKE, heads * 2, 2, FAKE, 1, heads, FAKE,
                                            heads * 2, 2, 0, None) == B.LOCKS_ERR_UNSUPPORTED
+
+
+def test_summaries_without_a_budget_are_refused_by_name():
+    import torch
+    cache = make(budget=0)
+    with pytest.raises(ValueError, match="budget_tokens"):
+        cache.build(torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="budget_tokens"):
+        cache.build_completed()
