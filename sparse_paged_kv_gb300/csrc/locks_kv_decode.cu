@@ -528,13 +528,10 @@ __device__ __forceinline__ void next_unit(const KvDecodeParams& p, int& b, Seq& 
   u += sq.cost(fixed);
   if (++h < p.n_kv_heads || u >= end) return;     // (beyond `end` there may be no sequence)
   h = 0;
-  do {
-    if (++b >= p.batch) {
-      u = end;
-      return;
-    }
-    sq = seq_of(p, b);
-  } while (sq.stages == 0);
+  ++b;
+  while (b < p.batch && p.seq_lens[b] <= 0) ++b;
+  if (b < p.batch) sq = seq_of(p, b);
+  else u = end;
 }
 
 // A unit's query for heads h0 .. h0 + 7 (lane 4g + t: head h0 + g, dims 32t ..
