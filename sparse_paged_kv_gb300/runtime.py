@@ -209,7 +209,8 @@ class QuantCache:
     With `budget_tokens` the steps attend only the pages that the Locks
     selection keeps: summaries are built from complete pages read back out of
     the cache (what the attention will see of them), and each step selects
-    before it attends."""
+    before it attends.  The selection's limits then hold: pages of 64 or 16, 1,
+    2, 4 or 8 query heads a KV head, and 2 to 256 pages of budget."""
 
     def __init__(self, cfg: B.LocksKvConfig, block_table, rope: Optional[RopeTable] = None,
                  budget_tokens: int = 0, rank: int = 8,
@@ -246,10 +247,13 @@ class QuantCache:
             if summary == 0:
                 raise B.LocksError("locks_summary_record_bytes", B.LOCKS_ERR_UNSUPPORTED,
                                    "unsupported cfg")
+            k = self.locks_cfg.page_budget(self.budget)
+            if not 2 <= k <= 256:      # here, and not by a step that has written its token
+                raise B.LocksError("locks_select", B.LOCKS_ERR_UNSUPPORTED,
+                                   f"budget_tokens {budget_tokens}: 2 to 256 pages expected")
             # one record row more than blocks: where "no page" entries of a step's list go
             self.summaries = zeros(cfg.num_blocks + 1, cfg.n_kv_heads, summary)
             self.ws_select = zeros(max(1, B.select_workspace_bytes(self.locks_cfg, self.budget)))
-            k = self.locks_cfg.page_budget(self.budget)
             self.selected = torch.full((cfg.batch, cfg.n_kv_heads, k), -1, dtype=torch.int32,
                                        device=device)
 

@@ -145,3 +145,23 @@ def test_summaries_without_a_budget_are_refused_by_name():
         cache.build(torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="budget_tokens"):
         cache.build_completed()
+
+
+@pytest.mark.parametrize("budget", [-64, 1, 16, 257 * 16])
+def test_a_budget_that_the_selection_refuses_is_refused_at_once(budget):
+    """And not by a step that has written its token already: 2 to 256 pages."""
+    with pytest.raises(B.LocksError):
+        make(budget=budget)
+
+
+@pytest.mark.parametrize("budget,k", [(17, 2), (256 * 16, 256)])
+def test_the_smallest_and_the_largest_budget(budget, k):
+    assert make(budget=budget).selected.shape == (2, 2, k)
+
+
+@pytest.mark.parametrize("over", [dict(page=32, budget=128), dict(hq=6), dict(hq=32)])
+def test_shapes_that_the_selection_refuses_are_refused_with_a_budget_only(over):
+    """Pages of 32, groups of 3 and of 16 heads."""
+    with pytest.raises(B.LocksError):
+        make(**over)
+    assert make(**{**over, "budget": 0}).selected is None
