@@ -391,8 +391,10 @@ typedef struct locks_rope_spec {
  *           [0, rotary_dim - 1], D(t) = rotary_dim ln(original / (2 pi t)) /
  *           (2 ln theta); mscale = 0.1 ln(factor) + 1
  * turns[i] = w_i / (2 pi) as a 64-bit binary fraction of a turn: the kernels
- * multiply it by the position modulo 2^64, so that the angle of any position
- * is exact to 2^-32 of a turn.
+ * multiply it by the position modulo 2^64, which loses nothing, and keep the
+ * top 32 bits.  The rate itself is computed in double and off by about 2^-55 of
+ * a turn at most, so the angle at position p is within 2^-32 + |p| 2^-55 of a
+ * turn: 2^-31 up to 8 million positions, 2^-24 at 2^31.
  *
  *   turns    HOST uint64 [rotary_dim / 2]: written
  *   mscale   HOST float: written, the factor on cos and sin (1 but for YARN)
@@ -417,7 +419,7 @@ typedef struct locks_rope_table {
  * becomes (u c - v s, v c + u s) with c, s = mscale * cos, sin(p w_i); dims
  * from rotary_dim on are copied.  `inverse` != 0 rotates by -p: the transposed
  * map, which is the gradient of the forward call with respect to x.  Computed
- * in float32, rounded once.
+ * in float32 (cos and sin of the angle within 2^-23), rounded once.
  *
  *   head_dim          even, 2 .. 512; rope->rotary_dim <= head_dim
  *   n_heads           at most 2^24
@@ -494,7 +496,11 @@ size_t locks_kv_decode_workspace_bytes(const locks_kv_cfg_t* cfg);
  * cache: out = sum_t p_t v_t, p = softmax(q^T k_t / sqrt(d)) over the attended
  * tokens: those of every page or of the listed pages, and with window > 0 only
  * the last `window` positions.  The codes are read once, and scales multiply
- * logits and weights.
+ * logits and weights.  Logits, running maxima and sums are float32.  A weight
+ * (p_t times the value's scale) is rounded to f16 before its product with the
+ * codes: by 2^-11 of itself, or 2^-31 of the largest where it is smaller than
+ * that; the products are summed in float32 and rounded to bf16 once.  Against 64
+ * bits that adds about 1% to the error of the output's own rounding.
  *
  *   q             bf16 [batch][n_q_heads][d], 16-byte aligned
  *   seq_lens      int32 [batch], the new token included; a length of 0 gives

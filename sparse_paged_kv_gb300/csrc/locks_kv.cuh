@@ -131,12 +131,13 @@ __device__ __forceinline__ void griddep_launch() {
 }
 
 // cos and sin of position * w, times mscale.  `turns` is w / 2 pi as a 64-bit
-// fraction of a turn: the product modulo 2^64 is the fractional turn, exact for
-// any position.  (A float32 product position * w would be off by 2^-24 of up to
-// 10^6 radians.)  Its top 32 bits are split, as integers, into the nearest
+// fraction of a turn: the product modulo 2^64 is the fractional turn, with no
+// error but the rate's own (a double's: 2^-55 of a turn a position).  (A float32
+// product position * w would be off by 2^-24 of up to 10^6 radians.)  Its top 32 bits are split, as integers, into the nearest
 // quarter turn and a remainder within an eighth, whose angle |a| <= pi / 4 goes
 // through the Taylor series of sine and cosine: the first terms left out are
-// a^11 / 11! < 2e-9 and a^12 / 12! < 2e-10.  About 30 instructions, half of what
+// a^11 / 11! < 2e-9 and a^12 / 12! < 2e-10, and with float32's roundings both are
+// within 2^-23.  About 30 instructions, half of what
 // sincospi takes, which has to find the quarter turn in floating point.
 __device__ __forceinline__ void rope_cos_sin(uint64_t turns, int32_t pos, float mscale, float& c,
                                              float& s) {

@@ -8,7 +8,9 @@
 // in 4 bits) are exact in f16, as is the bf16 query scaled by a power of two,
 // so q^T c_t is a float32 sum of exact products on the tensor cores.  The
 // weights p_t s'_t are rounded to f16 (2^-11, an eighth of the output's own
-// rounding); the sum of p_t that divides the result is kept in float32.
+// rounding, and about 1% of the error where the two are together; a second f16 for
+// the rest of a weight would double the second product); the sum of p_t that
+// divides the result is kept in float32.
 //
 // Work split.  The 64-token stages of all (sequence, KV head) units form one
 // list, each unit preceded by its fixed cost; block c of 152 (one per SM) takes
@@ -34,9 +36,11 @@
 // turned from S^T's layout into an operand by movmatrix.
 //
 // Measured (one GB300, of 6.78 TB/s copy): e4m3 1M tokens 314 us (7.05 TB/s), 8 x
-// 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 120 us (5.0 TB/s): instructions,
-// 370 for 16 tokens of a head, of which the unpacking of codes is over half.  One
-// sequence of 1000 tokens 9.5 us: a chain of latencies.
+// 32K 86 us (6.4 TB/s): memory.  int4 4 x 128K 121 us (5.0 TB/s): 370 instructions
+// for 16 tokens of a head, over half of them unpacking codes, issue in 65% of the
+// cycles; the ALU (50%) and memory (55%) are further from their limits, and forms
+// that spill 88, 100 or 212 bytes take the same time.  One sequence of 1000 tokens
+// 9.6 us: a chain of latencies.
 #include "locks_kv.cuh"
 
 namespace locks {
@@ -465,7 +469,8 @@ __device__ __forceinline__ void attend(const uint32_t (&base)[C], const uint32_t
 constexpr int kUnitCost = 6;
 // What a block's second end costs against parts that are shorter by so many
 // stages.  (Lists and contexts of one length: equal parts are 4 to 20% faster below
-// 37 stages a unit's idle share, 5% slower at 46 in int4; measured for 40 to 144 units.)
+// 37 stages a unit's idle share, 5% slower at 46 in int4; measured for 40 to 144 units,
+// taken for any number.)
 constexpr float kEndCost = 36.f;
 
 // A sequence as the kernel walks it: its length, the first attended position,

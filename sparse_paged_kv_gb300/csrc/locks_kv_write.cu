@@ -3,11 +3,11 @@
 //
 // Both move every byte once.  Measured (one GB300, 32 / 8 heads, e4m3, half
 // layout): 8192 tokens written in 35 us (5.3 TB/s of 6.78 copy; the blocks of a
-// wave load and compute in step), read back in 10 us (issue slots); 16 tokens of
-// a decode step in 7 us (latency).  Half a warp (16 lanes of
-// 8 dims) owns a row of 128 dims: its largest magnitude is four shuffles, a
-// group of 32 dims is four lanes, and its codes leave as one 128-byte (or
-// 64-byte) line.
+// wave load and compute in step), read back in 10 us (issue slots); 5001 tokens in
+// int4 written in 24 us and read back in 8; 16 tokens of a decode step in 7 us
+// (latency).  Half a warp (16 lanes of 8 dims) owns a row of 128 dims: its largest
+// magnitude is four shuffles, a group of 32 dims is four lanes, and its codes
+// leave as one 128-byte (or 64-byte) line.
 //
 // Write: a block takes a few tokens and a run of their rows (queries, then keys,
 // then values).  One thread asks for all of them (cp.async.bulk: a token's heads
@@ -54,12 +54,6 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
-}
-template <int W>
-__device__ __forceinline__ float lanes_max(float m) {   // over the aligned group of W lanes
-#pragma unroll
-  for (int o = W / 2; o; o >>= 1) m = max_abs(m, __shfl_xor_sync(kFull, m, o));
-  return m;
 }
 __device__ __forceinline__ float magnitude(const float (&x)[8]) {
   return max_abs(max_abs(max_abs(x[0], x[1]), max_abs(x[2], x[3])),

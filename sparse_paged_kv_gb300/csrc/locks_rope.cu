@@ -274,7 +274,8 @@ extern "C" int locks_rope_frequencies(const locks_rope_spec_t* spec, uint64_t* t
       z = std::fmin(1.0, std::fmax(0.0, z));
       w = w / spec->factor * z + w * (1 - z);
     }
-    turns[i] = uint64_t(std::ldexp(w / (2 * kPi), 64) + 0.5);   // w <= 1: below 2^62
+    // w <= 1: below 2^62.  (The half rounds the slow pairs; the fast ones' doubles end above it.)
+    turns[i] = uint64_t(std::ldexp(w / (2 * kPi), 64) + 0.5);
   }
   return LOCKS_OK;
 }
