@@ -67,6 +67,7 @@ extern "C" {
 #define LOCKS_DEV_NOT_CONVERGED  0x4  /* Jacobi hit max_sweeps before its tolerance       */
 #define LOCKS_DEV_BAD_PAGE_ID    0x8  /* selected page id outside [0, n): entry skipped   */
 #define LOCKS_DEV_BAD_SEQ_LEN    0x10 /* seq_len > max_pages * page_size: clamped         */
+#define LOCKS_DEV_BAD_GROUP      0x20 /* group_starts or prefix_pages out of range: clamped */
 
 /* summary record element type */
 #define LOCKS_SUMMARY_F32  0
@@ -519,6 +520,64 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
                     const void* v_pool, const int32_t* block_table, const int32_t* seq_lens,
                     const int32_t* selected, int32_t k, int32_t window, void* out, float* out_lse,
                     void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ===========================================================================
+ * A batch that shares prefixes and lives within a budget, over the bf16 pools.
+ *
+ * The conventions at the top hold (device pointers, no allocation, no
+ * synchronisation, status bits).  The calls take a locks_cfg_t of which rank
+ * and summary_dtype are not read; supported are head_dim = 128; page_size 64,
+ * 32 or 16; any G from 1 to 16; max_pages < 2^24, max_pages * page_size < 2^31;
+ * num_blocks * n_kv_heads < 2^31; batch * n_q_heads < 2^24.
+ *
+ * The newest tokens of a sequence: the calls take the queries of the last
+ * n_rows tokens of every sequence, q [batch][n_rows][n_q_heads][d]: 1 in a
+ * decode step, more for drafted tokens or the last tokens of a prompt.  Query
+ * row r of a sequence of t tokens is that of slot t - n_rows + r and sees the
+ * slots up to it.  A row whose slot would be negative sees nothing.
+ * n_rows <= 2 * floor(128 / G).
+ * =========================================================================== */
+
+/* Bytes of workspace locks_prefix_decode needs (0: refused arguments). */
+size_t locks_prefix_workspace_bytes(const locks_cfg_t* cfg, int32_t n_groups, int32_t n_rows);
+
+/*
+ * locks_prefix_decode -- attention of the newest tokens of a batch whose
+ * sequences share prefixes: out = sum_t p_t v_t, p = softmax(q^T k_t / sqrt(d))
+ * over every slot the row sees.  Sequences group_starts[g] ..
+ * group_starts[g + 1] - 1 have their first prefix_pages[g] pages in common; the
+ * call reads them once for all of the group's queries (256 rows at a time),
+ * through the block-table row of the group's first sequence, and each sequence's
+ * further pages through its own row.  The entries of the other rows for shared
+ * pages are not read.
+ *
+ *   q             bf16 [batch][n_rows][n_q_heads][d], 16-byte aligned
+ *   k_cache, v_cache  the pools, 16-byte aligned
+ *   seq_lens      int32 [batch], the new tokens included.  A sequence may end
+ *                 inside its group's prefix
+ *   group_starts  int32 [n_groups + 1], ascending, within 0 .. batch; sequences
+ *                 outside every group share nothing
+ *   prefix_pages  int32 [n_groups], each 0 .. max_pages
+ *   n_groups      0 .. batch (0: the two arrays are not read and may be NULL)
+ *   out           bf16 [batch][n_rows][n_q_heads][d], 16-byte aligned; a row
+ *                 that sees nothing gets 0
+ *   out_lse       nullable float [batch][n_rows][n_q_heads]: natural-log
+ *                 log-sum-exp (-inf for a row that sees nothing)
+ *   workspace     >= locks_prefix_workspace_bytes bytes, 16-byte aligned
+ *
+ * Logits, maxima, sums and accumulators are float32.  Weights are rounded to
+ * bf16 before their product with the values (2^-9 of each at most), and the
+ * output divides by their sum.  Slots that no row of a sequence (of a group,
+ * within the prefix) sees may hold anything; a NaN or an infinity in the value of a token that only some
+ * of the rows see (one of the last n_rows tokens, or a token of the prefix behind
+ * a shorter sequence's end) may reach the others.
+ * Pages of a block id outside the pool are left out (LOCKS_DEV_BAD_BLOCK_ID).
+ */
+int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const void* k_cache,
+                        const void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                        const int32_t* group_starts, const int32_t* prefix_pages, int32_t n_groups,
+                        void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream);
 
 /* Static string for a LOCKS_* return code. */
 const char* locks_status_string(int code);

@@ -30,6 +30,7 @@ LOCKS_DEV_WAIT_TIMEOUT = 0x2
 LOCKS_DEV_NOT_CONVERGED = 0x4
 LOCKS_DEV_BAD_PAGE_ID = 0x8
 LOCKS_DEV_BAD_SEQ_LEN = 0x10
+LOCKS_DEV_BAD_GROUP = 0x20
 
 LOCKS_SUMMARY_F32 = 0
 LOCKS_SUMMARY_BF16 = 1
@@ -192,6 +193,9 @@ _SIGS = {
     "locks_kv_read": (ctypes.c_int, [_KV, _P, _P, _P, _I, _P, _P, _P, _P]),
     "locks_kv_decode": (ctypes.c_int, [_KV, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P,
                                        _P]),
+    "locks_prefix_workspace_bytes": (_Z, [ctypes.POINTER(locks_cfg_t), _I, _I]),
+    "locks_prefix_decode": (ctypes.c_int, [ctypes.POINTER(locks_cfg_t), _P, _I, _P, _P, _P, _P, _P,
+                                           _P, _I, _P, _P, _P, _Z, _P, _P]),
     "locks_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "locks_abi_version": (ctypes.c_int, []),
 }
@@ -504,6 +508,65 @@ def locks_kv_decode(cfg: LocksKvConfig, q, k_pool, v_pool, block_table, seq_lens
         _sized(out_lse, "float32", (cfg.batch, cfg.n_q_heads), "out_lse"), _ptr(workspace),
         int(wsb), _ptr(_typed(status, "int32", "status")), _stream(stream))
     _check("locks_kv_decode", rc)
+
+
+# --------------------------------------------------------------------------
+# a batch that shares prefixes and lives within a budget (C names)
+# --------------------------------------------------------------------------
+def prefix_workspace_bytes(cfg: LocksConfig, n_groups: int, n_rows: int = 1) -> int:
+    return int(load_library().locks_prefix_workspace_bytes(ctypes.byref(cfg.c()), n_groups, n_rows))
+
+
+def _here(x, what: str):
+    """x, if it is a tensor on the current device (where the call's kernels run)."""
+    if type(x) is not int and x.is_cuda:
+        if _current_device is None:
+            _find_raw_stream()
+        if x.get_device() != _current_device():
+            raise ValueError(f"{what}: a tensor of the current device expected, got {x.device}")
+    return x
+
+
+def _query_rows(q, cfg: LocksConfig, what: str = "q") -> int:
+    """Query rows a sequence of q [batch][n_rows][H_q][d] (or [batch][H_q][d]: one)."""
+    if q.dim() == 3:
+        return 1
+    if q.dim() != 4:
+        raise ValueError(f"{what}: [batch][rows][heads][dim] expected, got {tuple(q.shape)}")
+    return q.shape[1]
+
+
+def _pages(x, cfg: LocksConfig, dtype: str, what: str, row: Tuple = ()) -> Optional[int]:
+    """Pointer of a pool [num_blocks][H_kv][page_size]... of that type."""
+    return _sized(x, dtype, (cfg.num_blocks, cfg.n_kv_heads, cfg.page_size) + row, what)
+
+
+def locks_prefix_decode(cfg: LocksConfig, q, k_cache, v_cache, block_table, seq_lens, group_starts,
+                        prefix_pages, out, workspace, out_lse=None, status=None,
+                        workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """Attention of the newest tokens, q bf16 [batch][rows][H_q][d] (or [batch][H_q][d]), of a
+    batch whose sequences group_starts[g] .. group_starts[g + 1] - 1 share their first
+    prefix_pages[g] pages (int32 device tensors; both None: nothing is shared)."""
+    rows = _query_rows(q, cfg)
+    shape = (cfg.batch, cfg.n_q_heads, cfg.head_dim)
+    if q.dim() == 4:
+        shape = (cfg.batch, rows, cfg.n_q_heads, cfg.head_dim)
+    if (group_starts is None) != (prefix_pages is None):
+        raise ValueError("group_starts, prefix_pages: both or neither expected")
+    n_groups = 0 if prefix_pages is None else prefix_pages.shape[0]
+    wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
+    row = (cfg.head_dim,)
+    rc = load_library().locks_prefix_decode(
+        ctypes.byref(cfg.c()), _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
+        _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", row),
+        _pages(v_cache, cfg, "bfloat16", "v_cache", row),
+        _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
+        _sized(seq_lens, "int32", (cfg.batch,), "seq_lens"),
+        _sized(group_starts, "int32", (n_groups + 1,), "group_starts"),
+        _sized(prefix_pages, "int32", (n_groups,), "prefix_pages"), n_groups,
+        _sized(out, "bfloat16", shape, "out"), _sized(out_lse, "float32", shape[:-1], "out_lse"),
+        _ptr(workspace), int(wsb), _ptr(_typed(status, "int32", "status")), _stream(stream))
+    _check("locks_prefix_decode", rc)
 
 
 # --------------------------------------------------------------------------

@@ -1,0 +1,47 @@
+// Parameter blocks and launchers of the operators of a batch that shares
+// prefixes and lives within a budget.  Internal to the library.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "../../include/locks.h"
+
+namespace locks {
+
+constexpr int kBatchSms = 152;         // blocks of a persistent launch: one per SM
+constexpr size_t kMaxSmemBlock = 227 * 1024;
+constexpr int kBatchMaxGroup = 16;     // query heads a KV head
+constexpr int kTileRows = 128;         // query rows of a matrix instruction
+constexpr int kStageTok = 128;         // tokens of a stage of the attention
+
+struct PrefixParams {
+  const int32_t* block_table;    // [batch][max_pages]
+  const int32_t* seq_lens;       // [batch]
+  const int32_t* group_starts;   // [n_groups + 1]
+  const int32_t* prefix_pages;   // [n_groups]
+  __nv_bfloat16* out;            // [batch][n_rows][H_q][d]
+  float* out_lse;                // nullable [batch][n_rows][H_q]
+  int32_t* status;               // nullable
+  // workspace (see prefix_layout)
+  float* acc;                    // [2 kinds][2 halves][rows][d] first pieces
+  float4* sums;                  // [2][2][rows] (m, l, l of the rounded weights, -)
+  float* carry_acc;              // [blocks][256][d] pieces continued from the block before
+  float4* carry_sums;            // [blocks][256]
+  int32_t* entry_start;          // [n_groups + batch + 1] first stage of each entry; their total
+  int batch, n_groups, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift;
+  int tile_tokens;               // query tokens of a tile: floor(128 / group)
+  int64_t rows;                  // batch * n_rows * n_q_heads
+  float scale_log2;
+};
+
+struct PrefixLayout {
+  size_t acc, sums, carry_acc, carry_sums, entry_start, total;
+};
+PrefixLayout prefix_layout(int64_t rows, int64_t entries);
+int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUtensorMap& q_own,
+                  const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
+
+}  // namespace locks

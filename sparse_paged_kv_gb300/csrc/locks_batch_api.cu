@@ -1,0 +1,162 @@
+// C-ABI entry points of the operators of a batch that shares prefixes and lives
+// within a budget (declared in include/locks.h): argument validation, tensor
+// maps and dispatch.  Nothing here allocates, frees or synchronises.
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "locks_batch.h"
+#include "locks_common.cuh"
+
+namespace {
+
+using locks::kHeadDim;
+
+bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15; }
+
+int check_batch_cfg(const locks_cfg_t* c) {
+  if (!c) return LOCKS_ERR_INVALID_ARG;
+  if (c->batch < 0 || c->n_q_heads <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 ||
+      c->page_size <= 0 || c->max_pages <= 0 || c->num_blocks <= 0)
+    return LOCKS_ERR_INVALID_ARG;
+  if (c->n_q_heads % c->n_kv_heads != 0) return LOCKS_ERR_INVALID_ARG;
+  if (c->head_dim != kHeadDim ||
+      (c->page_size != 64 && c->page_size != 32 && c->page_size != 16))
+    return LOCKS_ERR_UNSUPPORTED;
+  if (c->n_q_heads / c->n_kv_heads > locks::kBatchMaxGroup) return LOCKS_ERR_UNSUPPORTED;
+  // slots and (block, head) indices are ints
+  if (c->max_pages >= (1 << 24) || int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 31) ||
+      int64_t(c->num_blocks) * c->n_kv_heads >= (int64_t(1) << 31) ||
+      int64_t(c->batch) * c->n_q_heads >= (1 << 24))
+    return LOCKS_ERR_UNSUPPORTED;
+  return LOCKS_OK;
+}
+
+int page_shift(const locks_cfg_t* c) { return c->page_size == 64 ? 6 : c->page_size == 32 ? 5 : 4; }
+int group_size(const locks_cfg_t* c) { return c->n_q_heads / c->n_kv_heads; }
+int tile_tokens(const locks_cfg_t* c) { return locks::kTileRows / group_size(c); }
+
+int check_rows(const locks_cfg_t* c, int32_t n_rows) {
+  if (n_rows <= 0) return LOCKS_ERR_INVALID_ARG;
+  return n_rows > 2 * tile_tokens(c) ? LOCKS_ERR_UNSUPPORTED : LOCKS_OK;
+}
+
+int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
+  int rc = check_batch_cfg(c);
+  if (rc != LOCKS_OK || (rc = check_rows(c, n_rows)) != LOCKS_OK) return rc;
+  if (n_groups < 0 || n_groups > c->batch) return LOCKS_ERR_INVALID_ARG;
+  // stages of the whole list, and rows, are ints: every sequence's own pages and every group's
+  // (at most one unit of two tiles more than the sequences fill) over all of the table's pages
+  const int64_t stages = (int64_t(c->max_pages) * c->page_size + locks::kStageTok - 1) / locks::kStageTok;
+  const int64_t units = int64_t(c->batch) + n_groups +
+                        int64_t(c->batch) * n_rows / (2 * tile_tokens(c)) + 1;
+  if (stages * units * c->n_kv_heads >= (int64_t(1) << 31) ||
+      int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 31))
+    return LOCKS_ERR_UNSUPPORTED;
+  return LOCKS_OK;
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
+// against the driver library)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A contiguous bf16 tensor [n2][n1][128], read in boxes [b2][b1][64] with 128-byte swizzle.
+bool encode_map(CUtensorMap* m, const void* base, uint64_t n1, uint64_t n2, uint32_t b1, uint32_t b2) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(kHeadDim), n1, n2};
+  const cuuint64_t strides[2] = {cuuint64_t(kHeadDim) * 2, n1 * kHeadDim * 2};
+  const cuuint32_t box[3] = {64, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// pages [num_blocks * n_kv_heads][page_size][128], a page a box
+bool encode_pool(CUtensorMap* m, const void* pool, const locks_cfg_t* c) {
+  return encode_map(m, pool, c->page_size, uint64_t(c->num_blocks) * c->n_kv_heads, c->page_size, 1);
+}
+
+// queries [batch * n_rows][n_q_heads][128], `tokens` of one KV head's group a box
+bool encode_queries(CUtensorMap* m, const void* q, const locks_cfg_t* c, int n_rows, int tokens) {
+  return encode_map(m, q, c->n_q_heads, uint64_t(c->batch) * n_rows, group_size(c), tokens);
+}
+
+float logit_scale_log2() { return float(1.4426950408889634 / std::sqrt(double(kHeadDim))); }
+
+}  // namespace
+
+extern "C" {
+
+size_t locks_prefix_workspace_bytes(const locks_cfg_t* cfg, int32_t n_groups, int32_t n_rows) {
+  if (check_prefix(cfg, n_groups, n_rows) != LOCKS_OK) return 0;
+  return locks::prefix_layout(int64_t(cfg->batch) * n_rows * cfg->n_q_heads,
+                              int64_t(n_groups) + cfg->batch).total;
+}
+
+int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const void* k_cache,
+                        const void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                        const int32_t* group_starts, const int32_t* prefix_pages, int32_t n_groups,
+                        void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream) {
+  const int rc = check_prefix(cfg, n_groups, n_rows);
+  if (rc != LOCKS_OK) return rc;
+  if (cfg->batch == 0) return LOCKS_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace ||
+      (n_groups > 0 && (!group_starts || !prefix_pages)))
+    return LOCKS_ERR_INVALID_ARG;
+  if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) ||
+      misaligned(workspace))
+    return LOCKS_ERR_INVALID_ARG;
+  locks::PrefixParams p;
+  p.rows = int64_t(cfg->batch) * n_rows * cfg->n_q_heads;
+  const locks::PrefixLayout L = locks::prefix_layout(p.rows, int64_t(n_groups) + cfg->batch);
+  if (workspace_bytes < L.total) return LOCKS_ERR_WORKSPACE;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.group_starts = group_starts;
+  p.prefix_pages = prefix_pages;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_lse = out_lse;
+  p.status = status;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.acc = reinterpret_cast<float*>(ws + L.acc);
+  p.sums = reinterpret_cast<float4*>(ws + L.sums);
+  p.carry_acc = reinterpret_cast<float*>(ws + L.carry_acc);
+  p.carry_sums = reinterpret_cast<float4*>(ws + L.carry_sums);
+  p.entry_start = reinterpret_cast<int32_t*>(ws + L.entry_start);
+  p.batch = cfg->batch;
+  p.n_groups = n_groups;
+  p.n_rows = n_rows;
+  p.n_kv_heads = cfg->n_kv_heads;
+  p.group = group_size(cfg);
+  p.max_pages = cfg->max_pages;
+  p.num_blocks = cfg->num_blocks;
+  p.page_size = cfg->page_size;
+  p.page_shift = page_shift(cfg);
+  p.tile_tokens = tile_tokens(cfg);
+  p.scale_log2 = logit_scale_log2();
+  CUtensorMap qg, qo, mk, mv;
+  const int own = n_rows < p.tile_tokens ? n_rows : p.tile_tokens;
+  if (!encode_queries(&qg, q, cfg, n_rows, p.tile_tokens) || !encode_queries(&qo, q, cfg, n_rows, own) ||
+      !encode_pool(&mk, k_cache, cfg) || !encode_pool(&mv, v_cache, cfg))
+    return LOCKS_ERR_CUDA;
+  return locks::launch_prefix(p, qg, qo, mk, mv, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
