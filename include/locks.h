@@ -579,6 +579,74 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
                         void* out, float* out_lse, void* workspace, size_t workspace_bytes,
                         int32_t* status, void* stream);
 
+/*
+ * locks_weigh -- the attention weight that each cached token has received:
+ *
+ *   out[slot] = decay * weights[slot] + sum over the query rows of the KV head
+ *               that see the slot of exp(q^T k_slot / sqrt(d) - lse_row)
+ *
+ * for every slot from fixed[b] up to the sequence's length, with lse the rows'
+ * log-sum-exp from the attention call before.  Weights (and positions) lie in
+ * pools [num_blocks][n_kv_heads][page_size] beside the K/V pools, through the
+ * same block table; a weighed page belongs to one sequence (fixed keeps a
+ * shared prefix out).  The last n_new slots have no weight yet: their old one
+ * counts as 0, and their entry of `positions` becomes slot + evicted[b].
+ *
+ *   q             bf16 [batch][n_rows][n_q_heads][d], 16-byte aligned
+ *   lse           float [batch][n_rows][n_q_heads]; -inf: the row adds nothing
+ *   k_cache       the K pool, 16-byte aligned
+ *   fixed         nullable int32 [batch], >= 0 (NULL: 0)
+ *   weights       nullable float pool (NULL: every slot is new)
+ *   out           float pool; may be weights.  Slots before fixed and behind the
+ *                 sequence stay as they are
+ *   n_new         >= 0
+ *   decay         >= 0, 1 to accumulate
+ *   positions     nullable int32 pool
+ *   evicted       nullable int32 [batch]: tokens that locks_evict took so far
+ * All of it in float32.  Slots of a block id outside the pool are left out
+ * (LOCKS_DEV_BAD_BLOCK_ID).
+ */
+int locks_weigh(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const float* lse,
+                const void* k_cache, const int32_t* block_table, const int32_t* seq_lens,
+                const int32_t* fixed, const float* weights, float* out, int32_t n_new, float decay,
+                int32_t* positions, const int32_t* evicted, int32_t* status, void* stream);
+
+/* Bytes of workspace locks_evict needs (0: refused arguments). */
+size_t locks_evict_workspace_bytes(const locks_cfg_t* cfg, int32_t budget);
+
+/*
+ * locks_evict -- every sequence with more than `budget` slots behind its fixed
+ * ones is cut to fixed[b] + budget slots, each KV head for itself: the slots
+ * whose position is among the `recent` newest (position >= seq_lens[b] +
+ * evicted[b] - recent) stay, then those of the largest weights; of equal ones the
+ * lower slot stays.  A NaN weighs more than any number.
+ *
+ * Kept slots from fixed + budget on move into the holes before it, the lowest
+ * into the lowest: rows of K and V, weights and positions.  So the order of slots
+ * is lost, which attention does not depend on (keys are rotated before they are
+ * cached); positions says where a slot's token stood.  Page summaries of pages
+ * behind the fixed ones no longer describe them.  Everything behind the new
+ * length stays as it is.  Then seq_lens[b] becomes fixed + budget, and
+ * evicted[b] grows by what was dropped: the next token's position is
+ * seq_lens[b] + evicted[b].
+ *
+ *   budget        >= 1
+ *   recent        0 .. budget
+ *   k_cache, v_cache  the pools, 16-byte aligned; written
+ *   seq_lens      int32 [batch]; written
+ *   fixed         nullable int32 [batch], >= 0 (NULL: 0): slots that are kept
+ *                 where they are (a shared prefix, the first tokens)
+ *   weights, positions  pools as for locks_weigh; written
+ *   evicted       int32 [batch]; written
+ *   workspace     >= locks_evict_workspace_bytes bytes, 16-byte aligned
+ * A slot of a block id outside the pool weighs less than any other; moves from
+ * or to one are left out (LOCKS_DEV_BAD_BLOCK_ID).
+ */
+int locks_evict(const locks_cfg_t* cfg, int32_t budget, int32_t recent, void* k_cache, void* v_cache,
+                const int32_t* block_table, int32_t* seq_lens, const int32_t* fixed, float* weights,
+                int32_t* positions, int32_t* evicted, void* workspace, size_t workspace_bytes,
+                int32_t* status, void* stream);
+
 /* Static string for a LOCKS_* return code. */
 const char* locks_status_string(int code);
 

@@ -196,6 +196,11 @@ _SIGS = {
     "locks_prefix_workspace_bytes": (_Z, [ctypes.POINTER(locks_cfg_t), _I, _I]),
     "locks_prefix_decode": (ctypes.c_int, [ctypes.POINTER(locks_cfg_t), _P, _I, _P, _P, _P, _P, _P,
                                            _P, _I, _P, _P, _P, _Z, _P, _P]),
+    "locks_weigh": (ctypes.c_int, [ctypes.POINTER(locks_cfg_t), _P, _I, _P, _P, _P, _P, _P, _P, _P,
+                                   _I, ctypes.c_float, _P, _P, _P, _P]),
+    "locks_evict_workspace_bytes": (_Z, [ctypes.POINTER(locks_cfg_t), _I]),
+    "locks_evict": (ctypes.c_int, [ctypes.POINTER(locks_cfg_t), _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                                   _P, _P, _Z, _P, _P]),
     "locks_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "locks_abi_version": (ctypes.c_int, []),
 }
@@ -567,6 +572,55 @@ def locks_prefix_decode(cfg: LocksConfig, q, k_cache, v_cache, block_table, seq_
         _sized(out, "bfloat16", shape, "out"), _sized(out_lse, "float32", shape[:-1], "out_lse"),
         _ptr(workspace), int(wsb), _ptr(_typed(status, "int32", "status")), _stream(stream))
     _check("locks_prefix_decode", rc)
+
+
+def locks_weigh(cfg: LocksConfig, q, lse, k_cache, block_table, seq_lens, weights, out,
+                n_new: int = 1, decay: float = 1.0, fixed=None, positions=None, evicted=None,
+                status=None, stream=None) -> None:
+    """Attention weight of every cached token from slot fixed[b] on: out = decay * weights + what
+    the rows of q (bf16 [batch][rows][H_q][d], or [batch][H_q][d]) give it, lse their log-sum-exps.
+    weights (None: no weights yet) and out are float, positions int32 pools [blocks][H_kv][page]."""
+    rows = _query_rows(q, cfg)
+    shape = (cfg.batch, cfg.n_q_heads, cfg.head_dim)
+    if q.dim() == 4:
+        shape = (cfg.batch, rows, cfg.n_q_heads, cfg.head_dim)
+    rc = load_library().locks_weigh(
+        ctypes.byref(cfg.c()), _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
+        _sized(lse, "float32", shape[:-1], "lse"),
+        _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", (cfg.head_dim,)),
+        _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
+        _sized(seq_lens, "int32", (cfg.batch,), "seq_lens"),
+        _sized(fixed, "int32", (cfg.batch,), "fixed"), _pages(weights, cfg, "float32", "weights"),
+        _pages(out, cfg, "float32", "out"), int(n_new), float(decay),
+        _pages(positions, cfg, "int32", "positions"),
+        _sized(evicted, "int32", (cfg.batch,), "evicted"), _ptr(_typed(status, "int32", "status")),
+        _stream(stream))
+    _check("locks_weigh", rc)
+
+
+def evict_workspace_bytes(cfg: LocksConfig, budget: int) -> int:
+    return int(load_library().locks_evict_workspace_bytes(ctypes.byref(cfg.c()), budget))
+
+
+def locks_evict(cfg: LocksConfig, budget: int, recent: int, k_cache, v_cache, block_table, seq_lens,
+                weights, positions, evicted, workspace, fixed=None, status=None,
+                workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """Cut every sequence to `budget` slots a KV head behind its fixed ones: the `recent` newest
+    positions stay, then the largest weights; kept rows move into the holes.  seq_lens, evicted,
+    the pools, weights and positions are updated in place."""
+    wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
+    row = (cfg.head_dim,)
+    rc = load_library().locks_evict(
+        ctypes.byref(cfg.c()), int(budget), int(recent),
+        _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", row),
+        _pages(v_cache, cfg, "bfloat16", "v_cache", row),
+        _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
+        _sized(seq_lens, "int32", (cfg.batch,), "seq_lens"),
+        _sized(fixed, "int32", (cfg.batch,), "fixed"), _pages(weights, cfg, "float32", "weights"),
+        _pages(positions, cfg, "int32", "positions"),
+        _sized(evicted, "int32", (cfg.batch,), "evicted"), _ptr(workspace), int(wsb),
+        _ptr(_typed(status, "int32", "status")), _stream(stream))
+    _check("locks_evict", rc)
 
 
 # --------------------------------------------------------------------------

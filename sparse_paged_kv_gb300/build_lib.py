@@ -23,9 +23,10 @@ LIB = os.path.join(LIB_DIR, "libsparse_paged_kv.so")
 SOURCES = ["locks_api.cu", "locks_build.cu", "locks_select.cu", "locks_score_b16.cu",
            "locks_decode.cu", "locks_select_noalloc.cu", "locks_append.cu", "locks_rope.cu",
            "locks_kv_write.cu", "locks_kv_decode.cu", "locks_kv_api.cu", "locks_prefix.cu",
-           "locks_batch_api.cu"]
+           "locks_weigh.cu", "locks_evict.cu", "locks_batch_api.cu"]
 HEADERS = ["locks_common.cuh", "locks_internal.h", "locks_score.cuh", "locks_topk.cuh",
-           "locks_mma.cuh", "locks_kv.cuh", "locks_tc.cuh", "locks_batch.h"]
+           "locks_mma.cuh", "locks_kv.cuh", "locks_tc.cuh", "locks_batch.h",
+           "locks_batch.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE]

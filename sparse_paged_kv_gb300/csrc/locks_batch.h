@@ -44,4 +44,38 @@ PrefixLayout prefix_layout(int64_t rows, int64_t entries);
 int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUtensorMap& q_own,
                   const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
 
+struct WeighParams {
+  const float* lse;              // [batch][n_rows][H_q]
+  const int32_t* block_table;    // [batch][max_pages]
+  const int32_t* seq_lens;       // [batch]
+  const int32_t* fixed;          // nullable [batch]
+  const float* weights;          // nullable [num_blocks][H_kv][B]
+  float* out;                    // [num_blocks][H_kv][B]
+  int32_t* positions;            // nullable [num_blocks][H_kv][B]
+  const int32_t* evicted;        // nullable [batch]
+  int32_t* status;               // nullable
+  int batch, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift, n_new;
+  float decay, scale_log2;
+  int q_half, n_cols, tmem_cols, ring;   // set by the launch: see launch_weigh
+};
+int launch_weigh(WeighParams p, const CUtensorMap& q, const CUtensorMap& k, cudaStream_t stream);
+
+struct EvictParams {
+  __nv_bfloat16* k_cache;        // [num_blocks][H_kv][B][d]
+  __nv_bfloat16* v_cache;
+  const int32_t* block_table;    // [batch][max_pages]
+  int32_t* seq_lens;             // [batch], lowered
+  const int32_t* fixed;          // nullable [batch]
+  float* weights;                // [num_blocks][H_kv][B]
+  int32_t* positions;            // [num_blocks][H_kv][B]
+  int32_t* evicted;              // [batch], raised
+  int32_t* tickets;              // [batch] zeros, left as zeros
+  int32_t* lists;                // [batch * H_kv][2][list_len]
+  int32_t* status;               // nullable
+  int batch, n_kv_heads, max_pages, num_blocks, page_size, page_shift, budget, recent, list_len;
+  int keys;                      // set by the launch: keys a block holds
+};
+int evict_list_len(int budget, int64_t slots);
+int launch_evict(EvictParams p, cudaStream_t stream);
+
 }  // namespace locks

@@ -58,6 +58,23 @@ int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
   return LOCKS_OK;
 }
 
+// the stages of every sequence's pages are counted in an int
+int check_stages(const locks_cfg_t* c) {
+  const int64_t stages = (int64_t(c->max_pages) * c->page_size + locks::kStageTok - 1) / locks::kStageTok;
+  return (stages + 1) * c->batch * c->n_kv_heads >= (int64_t(1) << 31) ? LOCKS_ERR_UNSUPPORTED : LOCKS_OK;
+}
+
+int check_evict(const locks_cfg_t* c, int32_t budget) {
+  const int rc = check_batch_cfg(c);
+  if (rc != LOCKS_OK) return rc;
+  if (budget < 1) return LOCKS_ERR_INVALID_ARG;
+  return LOCKS_OK;
+}
+int evict_list(const locks_cfg_t* c, int32_t budget) {
+  return locks::evict_list_len(budget, int64_t(c->max_pages) * c->page_size);
+}
+size_t evict_list_offset(const locks_cfg_t* c) { return (size_t(c->batch) * 4 + 255) / 256 * 256; }
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link
 // against the driver library)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -157,6 +174,85 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
       !encode_pool(&mk, k_cache, cfg) || !encode_pool(&mv, v_cache, cfg))
     return LOCKS_ERR_CUDA;
   return locks::launch_prefix(p, qg, qo, mk, mv, static_cast<cudaStream_t>(stream));
+}
+
+int locks_weigh(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const float* lse,
+                const void* k_cache, const int32_t* block_table, const int32_t* seq_lens,
+                const int32_t* fixed, const float* weights, float* out, int32_t n_new, float decay,
+                int32_t* positions, const int32_t* evicted, int32_t* status, void* stream) {
+  int rc = check_batch_cfg(cfg);
+  if (rc != LOCKS_OK || (rc = check_rows(cfg, n_rows)) != LOCKS_OK) return rc;
+  if (n_new < 0 || !(decay >= 0.f) || !std::isfinite(decay)) return LOCKS_ERR_INVALID_ARG;
+  if ((rc = check_stages(cfg)) != LOCKS_OK) return rc;
+  if (cfg->batch == 0) return LOCKS_OK;
+  if (!q || !lse || !k_cache || !block_table || !seq_lens || !out) return LOCKS_ERR_INVALID_ARG;
+  if (misaligned(q) || misaligned(k_cache)) return LOCKS_ERR_INVALID_ARG;
+  locks::WeighParams p = {};
+  p.lse = lse;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.fixed = fixed;
+  p.weights = weights;
+  p.out = out;
+  p.positions = positions;
+  p.evicted = evicted;
+  p.status = status;
+  p.batch = cfg->batch;
+  p.n_rows = n_rows;
+  p.n_kv_heads = cfg->n_kv_heads;
+  p.group = group_size(cfg);
+  p.max_pages = cfg->max_pages;
+  p.num_blocks = cfg->num_blocks;
+  p.page_size = cfg->page_size;
+  p.page_shift = page_shift(cfg);
+  p.n_new = n_new;
+  p.decay = decay;
+  p.scale_log2 = logit_scale_log2();
+  CUtensorMap mq, mk;
+  if (!encode_queries(&mq, q, cfg, n_rows, n_rows) || !encode_pool(&mk, k_cache, cfg))
+    return LOCKS_ERR_CUDA;
+  return locks::launch_weigh(p, mq, mk, static_cast<cudaStream_t>(stream));
+}
+
+size_t locks_evict_workspace_bytes(const locks_cfg_t* cfg, int32_t budget) {
+  if (check_evict(cfg, budget) != LOCKS_OK) return 0;
+  return evict_list_offset(cfg) + size_t(cfg->batch) * cfg->n_kv_heads * 2 * evict_list(cfg, budget) * 4;
+}
+
+int locks_evict(const locks_cfg_t* cfg, int32_t budget, int32_t recent, void* k_cache, void* v_cache,
+                const int32_t* block_table, int32_t* seq_lens, const int32_t* fixed, float* weights,
+                int32_t* positions, int32_t* evicted, void* workspace, size_t workspace_bytes,
+                int32_t* status, void* stream) {
+  const int rc = check_evict(cfg, budget);
+  if (rc != LOCKS_OK) return rc;
+  if (recent < 0 || recent > budget) return LOCKS_ERR_INVALID_ARG;
+  if (cfg->batch == 0) return LOCKS_OK;
+  if (!k_cache || !v_cache || !block_table || !seq_lens || !weights || !positions || !evicted || !workspace)
+    return LOCKS_ERR_INVALID_ARG;
+  if (misaligned(k_cache) || misaligned(v_cache) || misaligned(workspace)) return LOCKS_ERR_INVALID_ARG;
+  if (workspace_bytes < locks_evict_workspace_bytes(cfg, budget)) return LOCKS_ERR_WORKSPACE;
+  locks::EvictParams p = {};
+  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.fixed = fixed;
+  p.weights = weights;
+  p.positions = positions;
+  p.evicted = evicted;
+  p.tickets = static_cast<int32_t*>(workspace);
+  p.lists = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + evict_list_offset(cfg));
+  p.status = status;
+  p.batch = cfg->batch;
+  p.n_kv_heads = cfg->n_kv_heads;
+  p.max_pages = cfg->max_pages;
+  p.num_blocks = cfg->num_blocks;
+  p.page_size = cfg->page_size;
+  p.page_shift = page_shift(cfg);
+  p.budget = budget;
+  p.recent = recent;
+  p.list_len = evict_list(cfg, budget);
+  return locks::launch_evict(p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

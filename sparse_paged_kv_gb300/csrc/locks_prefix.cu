@@ -32,6 +32,7 @@
 // rounded weights, so that a row with one dominant token keeps that token's
 // value exactly; the log-sum-exp comes from the unrounded sum.
 #include "locks_batch.h"
+#include "locks_batch.cuh"
 #include "locks_kv.cuh"
 #include "locks_tc.cuh"
 
@@ -55,8 +56,7 @@ struct Shared {
   uint32_t tmem;
   int dead;                                           // a wait ran out: every role leaves
   int bad[8];                                         // pages of a stage whose block is invalid, by stage & 7
-  int scan[kThreads / 32];
-  int total, entry, offset;
+  ListPlace place;
 };
 constexpr size_t kSmemBytes = size_t(kRing + 2) * kTileBytes + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= kMaxSmemBlock, "shared memory of a block");
@@ -129,7 +129,7 @@ struct Walk {
   int e, offset, left;
   Entry n;
   __device__ Walk(const PrefixParams& p, const Shared& sh, int share)
-      : e(sh.entry), offset(sh.offset), left(share) {
+      : e(sh.place.entry), offset(sh.place.offset), left(share) {
     if (left > 0) n = load_entry(p, e);
   }
   __device__ bool next(const PrefixParams& p, Piece& u) {
@@ -155,10 +155,6 @@ struct Walk {
     return true;
   }
 };
-
-__device__ __forceinline__ int share_begin(int total, int block) {
-  return int(int64_t(total) * block / kBatchSms);
-}
 
 // ---- the softmax groups ---------------------------------------------------------
 __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* ring, int w,
@@ -209,7 +205,8 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
             for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[c + k]);
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          if (__any_sync(kFull, top > m + kLazy)) {
+          // (rows past the unit's last hold whatever the tile held, and decide nothing)
+          if (__any_sync(kFull, valid && top > m + kLazy)) {
             const float mn = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
             m = mn;
@@ -502,63 +499,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   // what follows reads memory that the kernel before this one may write
   griddep_wait();
 
-  // every block adds up the list; a thread has `each` neighbouring entries
-  const int entries = p.n_groups + p.batch, each = (entries + kThreads - 1) / kThreads;
-  const int e_lo = min(entries, tid * each), e_hi = min(entries, e_lo + each);
-  int sum = 0;
-  for (int e = e_lo; e < e_hi; ++e) {
-    const Entry n = load_entry(p, e);
-    sum += n.units * n.stages;
-  }
-  int before = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, before, o);
-    if (lane >= o) before += x;
-  }
-  if (lane == 31) sh.scan[warp] = before;
-  before -= sum;
   tc_fence_before();
-  __syncthreads();
+  const int entries = p.n_groups + p.batch;
+  int total;
+  const int share = locate<kThreads>(
+      [&](int e) {
+        const Entry n = load_entry(p, e);
+        return n.units * n.stages;
+      },
+      entries, blockIdx.x, kBatchSms, sh.place, total,
+      [&](int e, int first) {
+        if (blockIdx.x) return;
+        // for the kernel that joins the pieces; and the arguments' check
+        p.entry_start[e] = first;
+        if (e >= p.n_groups) {
+          const int t = p.seq_lens[e - p.n_groups];
+          if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
+        } else {
+          const int a = p.group_starts[e], z = p.group_starts[e + 1], n_pages = p.prefix_pages[e];
+          if (a < 0 || z < a || z > p.batch || n_pages < 0 || n_pages > p.max_pages)
+            flag_status(p.status, LOCKS_DEV_BAD_GROUP);
+        }
+      });
+  if (blockIdx.x == 0 && tid == 0) p.entry_start[entries] = total;
   tc_fence_after();
   griddep_launch();
-  int total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += sh.scan[i];
-    total += sh.scan[i];
-  }
-  const int lo = share_begin(total, blockIdx.x), share = share_begin(total, blockIdx.x + 1) - lo;
-  if (share > 0 && lo >= before && lo < before + sum) {
-    int at = before;
-    for (int e = e_lo; e < e_hi; ++e) {
-      const Entry n = load_entry(p, e);
-      if (lo < at + n.units * n.stages) {
-        sh.entry = e;
-        sh.offset = lo - at;
-        break;
-      }
-      at += n.units * n.stages;
-    }
-  }
-  if (blockIdx.x == 0) {
-    // for the kernel that joins the pieces; and the arguments' check
-    int at = before;
-    for (int e = e_lo; e < e_hi; ++e) {
-      const Entry n = load_entry(p, e);
-      p.entry_start[e] = at;
-      at += n.units * n.stages;
-      if (e >= p.n_groups) {
-        const int t = p.seq_lens[e - p.n_groups];
-        if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
-      } else {
-        const int s = p.group_starts[e], t = p.group_starts[e + 1], n_pages = p.prefix_pages[e];
-        if (s < 0 || t < s || t > p.batch || n_pages < 0 || n_pages > p.max_pages)
-          flag_status(p.status, LOCKS_DEV_BAD_GROUP);
-      }
-    }
-    if (tid == 0) p.entry_start[entries] = total;
-  }
-  __syncthreads();
 
   if (share > 0) {
     if (warp < kProducerWarp) softmax_role(p, sh, ring, warp >> 2, share);
@@ -614,7 +579,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
     int at = first;
     while (at < first + n.stages) {
       const int c = int(((int64_t(at) + 1) * kBatchSms - 1) / total);
-      const int end = min(first + n.stages, share_begin(total, c + 1));
+      const int end = min(first + n.stages, share_begin(total, c + 1, kBatchSms));
       for (int half = 0; half < (pair ? 1 : min(2, end - at)); ++half) {
         if (at == first) {
           const int64_t i = (2 * kind + half) * p.rows + row;

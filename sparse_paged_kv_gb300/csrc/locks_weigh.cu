@@ -1,0 +1,319 @@
+// The attention weight that each cached token receives (locks_weigh):
+//
+//   w'[slot] = decay w[slot] + sum over the KV head's query rows that see the slot of
+//              exp(q^T k_slot / sqrt(d) - lse_row).
+//
+// Every key is read once (256 bytes against 8 of weights), so memory bounds it
+// while a sequence's rows are few.  The product is taken with the tokens as the
+// rows of the matrix instruction: S^T (128 tokens x rows) = K Q^T, so that a
+// thread holds one token, sums over its own registers and writes one float; no
+// reduction across threads, no atomics, any number of rows up to 256 in one
+// pass over the keys.  A list of stages of 128 tokens is shared out equally
+// over 152 blocks (a stage's result is complete, so pieces need no joining).  A
+// block's 10 warps: one loads keys (tensor maps, a ring of 32 KB tiles) and the
+// unit's queries (two buffers), one's first lane issues the products, and two
+// groups of four take stages in turn, thread = token, each with an accumulator
+// of its own in tensor memory.  Weights and block ids of a stage are loaded
+// before the wait for its product.
+#include "locks_batch.h"
+#include "locks_batch.cuh"
+#include "locks_kv.cuh"
+#include "locks_tc.cuh"
+
+namespace locks {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kTileBytes = 128 * 256;
+constexpr int kHalfBytes = kTileBytes / 2;
+constexpr int kMaxRing = 6;
+
+struct Shared {
+  uint64_t full[kMaxRing], empty[kMaxRing];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t d_full[2], d_empty[2];
+  uint64_t lse_full;
+  uint64_t done;
+  uint32_t tmem;
+  int dead;
+  ListPlace place;
+  float lse[2][256];                                  // of the unit, times log2 e; units in turn
+};
+
+struct Unit {
+  int b, head, first, page0, len;                     // slots [first, len), from page page0 on
+  int s0, s1;                                         // stages of this block
+};
+
+__device__ __forceinline__ int length_of(const WeighParams& p, int b) {
+  return min(max(p.seq_lens[b], 0), p.max_pages * p.page_size);
+}
+__device__ __forceinline__ int first_of(const WeighParams& p, int b) {
+  return p.fixed ? max(p.fixed[b], 0) : 0;
+}
+__device__ __forceinline__ int stages_of(const WeighParams& p, int b) {
+  const int t = length_of(p, b), f = first_of(p, b);
+  return f >= t ? 0 : (t - (f >> p.page_shift << p.page_shift) + kStageTok - 1) / kStageTok;
+}
+
+struct Walk {
+  int b, offset, left, n;
+  __device__ Walk(const WeighParams& p, const Shared& sh, int share)
+      : b(sh.place.entry), offset(sh.place.offset), left(share), n(stages_of(p, b)) {}
+  __device__ bool next(const WeighParams& p, Unit& u) {
+    if (left <= 0) return false;
+    while (offset >= n * p.n_kv_heads) {
+      offset = 0;
+      if (++b >= p.batch) return false;
+      n = stages_of(p, b);
+    }
+    u.b = b;
+    u.head = offset / n;
+    u.len = length_of(p, b);
+    u.first = first_of(p, b);
+    u.page0 = u.first >> p.page_shift;
+    u.s0 = offset - u.head * n;
+    u.s1 = min(n, u.s0 + left);
+    offset += u.s1 - u.s0;
+    left -= u.s1 - u.s0;
+    return true;
+  }
+};
+
+__device__ void load_role(const WeighParams& p, Shared& sh, unsigned char* qbuf, unsigned char* ring,
+                          const CUtensorMap* map_q, const CUtensorMap* map_k, int share) {
+  const int lane = threadIdx.x & 31;
+  const int per_stage = kStageTok >> p.page_shift;
+  Walk walk(p, sh, share);
+  Unit u;
+  int qn = 0, stage = 0;
+  bool ok = true;
+  while (ok && walk.next(p, u)) {
+    const int qs = qn & 1;
+    ok = warp_wait_or_dead(&sh.q_empty[qs], ((qn >> 1) & 1) ^ 1, &sh.dead);
+    if (!ok) break;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&sh.q_full[qs], p.n_rows * p.group * 256);
+      unsigned char* dst = qbuf + qs * 2 * p.q_half;
+      tma_load3(dst, map_q, 0, u.head * p.group, u.b * p.n_rows, &sh.q_full[qs]);
+      tma_load3(dst + p.q_half, map_q, 64, u.head * p.group, u.b * p.n_rows, &sh.q_full[qs]);
+    }
+    ++qn;
+    const int32_t* table = p.block_table + int64_t(u.b) * p.max_pages + u.page0;
+    const int tokens = u.len - (u.page0 << p.page_shift);
+    for (int s = u.s0; s < u.s1; ++s) {
+      const int page = s * per_stage + lane;
+      bool want = lane < per_stage && page << p.page_shift < tokens;
+      int block = 0;
+      if (want) {
+        block = table[page];
+        if (block < 0 || block >= p.num_blocks) {
+          flag_status(p.status, LOCKS_DEV_BAD_BLOCK_ID);
+          want = false;
+        }
+      }
+      const int n = __popc(__ballot_sync(kFull, want));
+      const int slot = stage % p.ring;
+      ok = warp_wait_or_dead(&sh.empty[slot], ((stage / p.ring) & 1) ^ 1, &sh.dead);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (n << p.page_shift) * 256);
+      __syncwarp();
+      if (want) {
+        unsigned char* dst = ring + slot * kTileBytes + (lane << p.page_shift) * 128;
+        const int z = block * p.n_kv_heads + u.head;
+        tma_load3(dst, map_k, 0, 0, z, &sh.full[slot]);
+        tma_load3(dst + kHalfBytes, map_k, 64, 0, z, &sh.full[slot]);
+      }
+      ++stage;
+    }
+  }
+  // no block leaves while copies into its memory are in flight
+  if (!ok) {
+    for (int c = max(0, stage - p.ring); c < stage; ++c)
+      mbar_wait_bounded(&sh.full[c % p.ring], (c / p.ring) & 1);
+    for (int t = max(0, qn - 2); t < qn; ++t)
+      mbar_wait_bounded(&sh.q_full[t & 1], (t >> 1) & 1);
+  }
+}
+
+__device__ void issue_role(const WeighParams& p, Shared& sh, unsigned char* qbuf, unsigned char* ring,
+                           int share) {
+  const uint32_t idesc = mma_idesc(128, p.n_cols, false);
+  const uint32_t q_addr = smem_u32(qbuf), ring_addr = smem_u32(ring), tmem = sh.tmem;
+  Walk walk(p, sh, share);
+  Unit u;
+  int qn = 0, stage = 0;
+  bool ok = true;
+  while (ok && walk.next(p, u)) {
+    const int qs = qn & 1;
+    ok = mbar_wait_or_dead(&sh.q_full[qs], (qn >> 1) & 1, &sh.dead);
+    ++qn;
+    for (int s = u.s0; ok && s < u.s1; ++s, ++stage) {
+      const int slot = stage % p.ring, w = stage & 1;
+      ok = mbar_wait_or_dead(&sh.full[slot], (stage / p.ring) & 1, &sh.dead) &&
+           mbar_wait_or_dead(&sh.d_empty[w], ((stage >> 1) & 1) ^ 1, &sh.dead);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t da = smem_desc(ring_addr + slot * kTileBytes, 16, 1024);
+      const uint64_t db = smem_desc(q_addr + qs * 2 * p.q_half, 16, 1024);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mma_ss(tmem + w * p.n_cols, da + (uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+               db + (uint64_t((k >> 2) * p.q_half + (k & 3) * 32) >> 4), idesc, k > 0);
+      mma_commit(&sh.d_full[w]);
+      mma_commit(&sh.empty[slot]);
+      if (s == u.s1 - 1) mma_commit(&sh.q_empty[qs]);
+    }
+  }
+  mma_commit(&sh.done);
+  mbar_wait_bounded(&sh.done, 0);
+}
+
+__device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const uint32_t d = sh.tmem + (uint32_t(tid >> 5 << 5) << 16) + w * p.n_cols;
+  const int rows = p.n_rows * p.group;
+  Walk walk(p, sh, share);
+  Unit u;
+  int stage = 0, units = 0;
+  while (walk.next(p, u)) {
+    // this unit's log-sum-exps (a row that sees nothing has -inf, and its weights none), a part a
+    // warp.  A warp that gets here has finished the unit before, so once all have arrived for
+    // unit n, nobody reads the buffer of unit n - 1, which unit n + 1 takes.
+    float* lse = sh.lse[units & 1];
+    for (int c = threadIdx.x; c < rows; c += 256) {
+      const int r = c / p.group;
+      const float x = p.lse[(int64_t(u.b) * p.n_rows + r) * (p.n_kv_heads * p.group) +
+                            u.head * p.group + c - r * p.group];
+      lse[c] = x == -INFINITY ? INFINITY : x * kLog2e;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.lse_full);
+    if (!warp_wait_or_dead(&sh.lse_full, units & 1, &sh.dead)) return;
+    ++units;
+    const int32_t* table = p.block_table + int64_t(u.b) * p.max_pages;
+    for (int s = u.s0; s < u.s1; ++s, ++stage) {
+      if ((stage & 1) != w) continue;
+      const int slot = (u.page0 << p.page_shift) + s * kStageTok + tid;
+      const bool there = slot >= u.first && slot < u.len;
+      const bool fresh = !p.weights || slot >= u.len - p.n_new;
+      int64_t at = -1;
+      float old = 0.f;
+      if (there) {
+        const int block = table[slot >> p.page_shift];
+        if (block >= 0 && block < p.num_blocks) {
+          at = (int64_t(block) * p.n_kv_heads + u.head) * p.page_size + (slot & (p.page_size - 1));
+          if (!fresh) old = p.weights[at];
+        }
+      }
+      if (!warp_wait_or_dead(&sh.d_full[w], (stage >> 1) & 1, &sh.dead)) return;
+      tc_fence_after();
+      // rows from c0 on see this slot
+      const int c0 = max(0, slot - (u.len - p.n_rows)) * p.group;
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < rows; c += 16) {
+        float x[16];
+        tmem_ld16(d + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float y = ex2_approx(fmaf(x[k], p.scale_log2, -lse[c + k]));
+          if (c + k >= c0 && c + k < rows) a[k & 3] += y;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.d_empty[w]);
+      if (at >= 0) {
+        p.out[at] = fmaf(p.decay, old, (a[0] + a[1]) + (a[2] + a[3]));
+        if (fresh && p.positions) p.positions[at] = slot + (p.evicted ? p.evicted[u.b] : 0);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    weigh_kernel(const WeighParams p, const __grid_constant__ CUtensorMap map_q,
+                 const __grid_constant__ CUtensorMap map_k) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* ring = smem;
+  unsigned char* qbuf = ring + p.ring * kTileBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(qbuf + 4 * p.q_half);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, p.tmem_cols);
+  if (tid == 0) {
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.d_full[i], 1);
+      mbar_init(&sh.d_empty[i], 4);
+    }
+    mbar_init(&sh.lse_full, 8);
+    mbar_init(&sh.done, 1);
+    mbar_fence_init();
+    sh.dead = 0;
+    prefetch_map(&map_q);
+    prefetch_map(&map_k);
+  }
+  // columns behind the rows are loaded with the last of them: whatever they hold goes unused
+  for (int i = tid; i < 512; i += kThreads) sh.lse[i >> 8][i & 255] = 0.f;
+  griddep_wait();
+  tc_fence_before();
+  const int share = locate<kThreads>(
+      [&](int b) { return stages_of(p, b) * p.n_kv_heads; }, p.batch, blockIdx.x, kBatchSms, sh.place);
+  tc_fence_after();
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.batch; b += kThreads)
+      if (p.seq_lens[b] < 0 || p.seq_lens[b] > p.max_pages * p.page_size)
+        flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
+  if (share > 0) {
+    if (warp < kProducerWarp) weigh_role(p, sh, warp >> 2, share);
+    else if (warp == kProducerWarp) load_role(p, sh, qbuf, ring, &map_q, &map_k, share);
+    else if (lane == 0) issue_role(p, sh, qbuf, ring, share);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && sh.dead) flag_status(p.status, LOCKS_DEV_WAIT_TIMEOUT);
+  if (warp == kMmaWarp) tmem_free(sh.tmem, p.tmem_cols);
+}
+
+}  // namespace
+
+int launch_weigh(WeighParams p, const CUtensorMap& q, const CUtensorMap& k, cudaStream_t stream) {
+  const int rows = p.n_rows * p.group;
+  p.q_half = (rows + 7) / 8 * 1024;                   // 64 columns of the unit's queries, whole swizzle atoms
+  p.n_cols = (rows + 15) / 16 * 16;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2 * p.n_cols) p.tmem_cols *= 2;
+  // (the product reads n_cols rows of each half: up to 8 behind the second one)
+  const int fixed = 4 * p.q_half + int(sizeof(Shared));
+  p.ring = (int(kMaxSmemBlock) - fixed) / kTileBytes;
+  if (p.ring > kMaxRing) p.ring = kMaxRing;
+  static LaunchOnce once;
+  if (!once.run([] {
+        return cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(kMaxSmemBlock)) == cudaSuccess;
+      }))
+    return LOCKS_ERR_CUDA;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(kBatchSms);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = size_t(p.ring) * kTileBytes + fixed;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, weigh_kernel, p, q, k) == cudaSuccess ? LOCKS_OK : LOCKS_ERR_CUDA;
+}
+
+}  // namespace locks
