@@ -13,7 +13,7 @@
 // over the group's pages, then every (sequence, KV head) over its own.  152
 // blocks, one per SM, take equal shares of the list, so that any mix of lengths
 // fills the chip; a unit cut by a share's border leaves a piece in either block.
-// A block's 10 warps are: one that loads (tensor maps, a ring of five 32 KB
+// A block's warps are: one that loads (tensor maps, a ring of five 32 KB
 // tiles, K and V of a stage in turn), one whose first lane issues the matrix
 // instructions, and two groups of four for the softmax, thread = query row:
 //   S (128 x 128, tensor memory) = Q K^T    both operands in shared memory
@@ -40,15 +40,33 @@ namespace locks {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;                         // three warpgroups: two of softmax, one of the others
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
+// registers a thread after the split: 256 * 208 + 128 * 88 = 384 * 168, the launch's
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileBytes = 128 * 256;                 // 128 rows of 128 bf16
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kRing = 5;
+// Pieces handed on: when piece n is written the queries of piece n - 2 have had their last use, so
+// (two products ahead, at least one stage a piece) the softmax groups are past piece n - 8.
+constexpr int kPieces = 16;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
+// A unit's stages [s0, s0 + stages) that this block has, as the loading warp hands them to the others.
+struct Piece {
+  int stages;
+  int pair;               // two tiles: both on every stage; else stages in turn
+  int group_pages;        // the unit is a group's (else a sequence's own pages)
+  int head, tokens, row, page0;
+  int q0, nq;             // query tokens of the unit (at most two tiles)
+  int s0;
+  __device__ __forceinline__ int jobs() const { return pair ? 2 * stages : stages; }
+};
+
 struct Shared {
+  Piece piece[kPieces];
+  uint64_t piece_full[kPieces];
   uint64_t full[kRing], empty[kRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
@@ -115,23 +133,12 @@ __device__ Entry load_entry(const PrefixParams& p, int e) {
   return n;
 }
 
-// a unit's stages [s0, s1) that this block has
-struct Piece {
-  int group_pages;        // the unit is a group's (else a sequence's own pages)
-  int head, tokens, row, page0;
-  int q0, nq;             // query tokens of the unit (at most two tiles)
-  int s0, s1;
-  bool pair;              // two tiles: both on every stage; else stages in turn
-  __device__ __forceinline__ int jobs() const { return pair ? 2 * (s1 - s0) : s1 - s0; }
-};
-
+// The pieces of this block's share, in the list's order.
 struct Walk {
   int e, offset, left;
   Entry n;
   __device__ Walk(const PrefixParams& p, const Shared& sh, int share)
-      : e(sh.place.entry), offset(sh.place.offset), left(share) {
-    if (left > 0) n = load_entry(p, e);
-  }
+      : e(sh.place.entry), offset(sh.place.offset), left(share), n(load_entry(p, e)) {}
   __device__ bool next(const PrefixParams& p, Piece& u) {
     if (left <= 0) return false;
     while (offset >= n.units * n.stages) {
@@ -149,9 +156,9 @@ struct Walk {
     u.nq = min(n.nq - tile * 2 * p.tile_tokens, 2 * p.tile_tokens);
     u.pair = u.nq > p.tile_tokens;
     u.s0 = offset - unit * n.stages;
-    u.s1 = min(n.stages, u.s0 + left);
-    offset += u.s1 - u.s0;
-    left -= u.s1 - u.s0;
+    u.stages = min(n.stages - u.s0, left);
+    offset += u.stages;
+    left -= u.stages;
     return true;
   }
 };
@@ -164,11 +171,11 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
   const uint32_t t_s = lanes + w * 128, t_o = lanes + 256 + w * 128;
   const int rt = tid / p.group, head_in_group = tid % p.group;
   const int npg_shift = p.page_shift;
-  Walk walk(p, sh, share);
-  Piece u;
   int job0 = 0, stage0 = 0, units = 0;
-  while (walk.next(p, u)) {
-    const int njobs = u.jobs(), nst = u.s1 - u.s0;
+  for (int n = 0; stage0 < share; ++n) {
+    if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return;
+    const Piece u = sh.piece[n % kPieces];
+    const int njobs = u.jobs();
     const int first = (job0 & 1) == w ? 0 : 1;
     if (first < njobs) {
       const int tq = (u.pair ? w * p.tile_tokens : 0) + rt;
@@ -213,14 +220,14 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
             l *= f;
             lr *= f;
             if (job >= 2) {                           // (the first product overwrites O)
-#pragma unroll
-              for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                tmem_ld32(t_o + c, o);
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 16) {
+                float o[16];
+                tmem_ld16(t_o + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= f;
-                tmem_st32(t_o + c, reinterpret_cast<uint32_t*>(o));
+                for (int k = 0; k < 16; ++k) o[k] *= f;
+                tmem_st16(t_o + c, reinterpret_cast<uint32_t*>(o));
               }
             }
           }
@@ -228,10 +235,10 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mu, -mu);
           float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-          for (int c = 0; c < 128; c += 64) {
-            uint32_t pk[32];
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 16; ++k) {
               float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
               x.x = ex2_approx(x.x);
               x.y = ex2_approx(x.y);
@@ -240,7 +247,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
               a0 = fadd2(a0, x);
               a1 = fadd2(a1, make_float2(bf16_lo(pk[k]), bf16_hi(pk[k])));
             }
-            tmem_st32(t_s + c / 2, pk);
+            tmem_st16(t_s + c / 2, pk);
           }
           l += a0.x + a0.y;
           lr += a1.x + a1.y;
@@ -301,7 +308,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
       if (lane == 0) mbar_arrive(&sh.o_empty[w]);
     }
     job0 += njobs;
-    stage0 += nst;
+    stage0 += u.stages;
   }
 }
 
@@ -315,13 +322,17 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
   Piece u;
   int qn = 0, stage = 0;
   bool ok = true;
-  while (ok && walk.next(p, u)) {
+  for (int piece = 0; ok && walk.next(p, u); ++piece) {
     const int box_tokens = u.group_pages ? p.tile_tokens : min(p.n_rows, p.tile_tokens);
     const CUtensorMap* map_q = u.group_pages ? map_qg : map_qo;
     for (int t = 0; ok && t < (u.pair ? 2 : 1); ++t, ++qn) {
       const int slot = qn & 1;
       ok = warp_wait_or_dead(&sh.q_empty[slot], ((qn >> 1) & 1) ^ 1, &sh.dead);
       if (ok && lane == 0) {
+        if (t == 0) {
+          sh.piece[piece % kPieces] = u;
+          mbar_arrive(&sh.piece_full[piece % kPieces]);
+        }
         mbar_arrive_expect_tx(&sh.q_full[slot], box_tokens * p.group * 256);
         unsigned char* dst = qtile + slot * kTileBytes;
         tma_load3(dst, map_q, 0, u.head * p.group, u.q0 + t * p.tile_tokens, &sh.q_full[slot]);
@@ -330,7 +341,7 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
       }
     }
     const int32_t* table = p.block_table + int64_t(u.row) * p.max_pages + u.page0;
-    for (int s = u.s0; ok && s < u.s1; ++s, ++stage) {
+    for (int s = u.s0; ok && s < u.s0 + u.stages; ++s, ++stage) {
       // lane i has the stage's page i
       const int page = s * per_stage + lane;
       bool want = lane < per_stage && page << p.page_shift < u.tokens;
@@ -376,48 +387,53 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
 }
 
 // ---- the issuing thread -------------------------------------------------------------
-// Job J (counted over the block's pieces) is one stage for one softmax group, J & 1.
-struct Jobs {
-  Walk walk;
-  Piece u;
-  int job, njobs, J, stage0, q0;
+// Job J (counted over the block's pieces) is one stage for one softmax group, J & 1.  The products
+// Q K^T run two jobs ahead of the products P V, each with a cursor like this.
+struct Cursor {
+  int J, job, njobs, pair, stage0, stages, q0, n;
   bool more;
-  __device__ Jobs(const PrefixParams& p, const Shared& sh, int share)
-      : walk(p, sh, share), job(0), J(0), stage0(0), q0(0) {
-    more = walk.next(p, u);
-    njobs = more ? u.jobs() : 0;
-  }
-  __device__ void advance(const PrefixParams& p) {
-    ++J;
-    if (++job < njobs) return;
-    stage0 += u.s1 - u.s0;
-    q0 += u.pair ? 2 : 1;
+  __device__ __forceinline__ bool open(Shared& sh, int share) {
+    more = stage0 < share;
+    if (!more) return true;
+    if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
+    const Piece& u = sh.piece[n % kPieces];
+    stages = u.stages;
+    pair = u.pair;
+    njobs = u.jobs();
     job = 0;
-    more = walk.next(p, u);
-    njobs = more ? u.jobs() : 0;
+    return true;
   }
-  __device__ __forceinline__ int stage() const { return stage0 + (u.pair ? job >> 1 : job); }
-  __device__ __forceinline__ bool first_of_stage() const { return !u.pair || !(job & 1); }
-  __device__ __forceinline__ bool last_of_stage() const { return !u.pair || (job & 1); }
+  __device__ __forceinline__ bool advance(Shared& sh, int share) {
+    ++J;
+    if (++job < njobs) return true;
+    stage0 += stages;
+    q0 += 1 + pair;
+    ++n;
+    return open(sh, share);
+  }
+  __device__ __forceinline__ int stage() const { return stage0 + (job >> pair); }
+  __device__ __forceinline__ bool first_of_stage() const { return !(job & pair); }
+  __device__ __forceinline__ bool last_of_stage() const { return !pair || (job & 1); }
 };
 
-__device__ void issue_role(const PrefixParams& p, Shared& sh, unsigned char* qtile,
-                           unsigned char* ring, int share) {
+__device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int share) {
   constexpr uint32_t kIdescS = mma_idesc(128, 128, false), kIdescO = mma_idesc(128, 128, true);
-  const uint32_t q_addr = smem_u32(qtile), ring_addr = smem_u32(ring), tmem = sh.tmem;
-  Jobs a(p, sh, share), b(p, sh, share);              // of the products Q K^T and P V
-  int units[2] = {0, 0};
-  bool ok = true;
+  const uint32_t tmem = sh.tmem;
+  const uint64_t q_desc = smem_desc(smem_u32(qtile), 16, 1024);
+  const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024);
+  // 64 columns of V (a half) follow each other at kHalfBytes, 8 tokens at 1024 bytes
+  const uint64_t v_desc = smem_desc(smem_u32(ring), kHalfBytes, 1024);
+  Cursor a = {}, b = {};
+  uint32_t opened = 0;                                // accumulators begun by either group, modulo 2, in bits 0 and 16
+  bool ok = a.open(sh, share) && b.open(sh, share);
 
   auto scores = [&]() {
-    const int w = a.J & 1, t = a.q0 + (a.u.pair ? w : 0), qs = t & 1;
-    const int c = 2 * a.stage(), slot = c % kRing;
-    if (a.job < (a.u.pair ? 2 : 1) && !mbar_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead))
-      return false;
+    const uint32_t w = a.J & 1, t = a.q0 + (a.pair ? w : 0), qs = t & 1;
+    const uint32_t c = 2 * a.stage(), slot = c % kRing;
+    if (a.job <= a.pair && !mbar_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead)) return false;
     if (a.first_of_stage() && !mbar_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
       return false;
-    const uint64_t da = smem_desc(q_addr + qs * kTileBytes, 16, 1024);
-    const uint64_t db = smem_desc(ring_addr + slot * kTileBytes, 16, 1024);
+    const uint64_t da = q_desc + qs * (kTileBytes >> 4), db = k_desc + slot * (kTileBytes >> 4);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {                     // 16 of the 128 dims each, 64 in a half
       const uint64_t o = uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
@@ -425,31 +441,29 @@ __device__ void issue_role(const PrefixParams& p, Shared& sh, unsigned char* qti
     }
     mma_commit(&sh.s_full[w]);
     if (a.last_of_stage()) mma_commit(&sh.empty[slot]);
-    if (a.job >= a.njobs - (a.u.pair ? 2 : 1)) mma_commit(&sh.q_empty[qs]);
-    a.advance(p);
-    return true;
+    if (a.job >= a.njobs - 1 - a.pair) mma_commit(&sh.q_empty[qs]);
+    return a.advance(sh, share);
   };
   auto values = [&]() {
-    const int w = b.J & 1, c = 2 * b.stage() + 1, slot = c % kRing;
+    const uint32_t w = b.J & 1, c = 2 * b.stage() + 1, slot = c % kRing;
     if (!mbar_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead)) return false;
     if (b.first_of_stage() && !mbar_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
       return false;
     const bool fresh = b.job < 2;                     // of this unit for this group
     if (fresh) {
-      if (!mbar_wait_or_dead(&sh.o_empty[w], (units[w] & 1) ^ 1, &sh.dead)) return false;
-      ++units[w];
+      const uint32_t n = opened >> (16 * w);
+      if (!mbar_wait_or_dead(&sh.o_empty[w], (n & 1) ^ 1, &sh.dead)) return false;
+      opened ^= 1u << (16 * w);
     }
     tc_fence_after();
-    // 64 columns of V (a half) follow each other at kHalfBytes, 8 tokens at 1024 bytes
-    const uint64_t db = smem_desc(ring_addr + slot * kTileBytes, kHalfBytes, 1024);
+    const uint64_t db = v_desc + slot * (kTileBytes >> 4);
 #pragma unroll
     for (int k = 0; k < 8; ++k)                       // 16 of the 128 tokens each
       mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, db + (uint64_t(k * 2048) >> 4), kIdescO,
              !fresh || k > 0);
     if (b.last_of_stage()) mma_commit(&sh.empty[slot]);
     if (b.job >= b.njobs - 2) mma_commit(&sh.o_full[w]);
-    b.advance(p);
-    return true;
+    return b.advance(sh, share);
   };
 
   for (int i = 0; ok && i < 2 && a.more; ++i) ok = scores();
@@ -488,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_empty[i], 4);
     }
+    for (int i = 0; i < kPieces; ++i) mbar_init(&sh.piece_full[i], 1);
     mbar_init(&sh.done, 1);
     mbar_fence_init();
     sh.dead = 0;
@@ -526,9 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch();
 
   if (share > 0) {
-    if (warp < kProducerWarp) softmax_role(p, sh, ring, warp >> 2, share);
-    else if (warp == kProducerWarp) load_role(p, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
-    else if (lane == 0) issue_role(p, sh, qtile, ring, share);
+    if (warp < kProducerWarp) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+      softmax_role(p, sh, ring, warp >> 2, share);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == kProducerWarp) load_role(p, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
+      else if (warp == kMmaWarp && lane == 0) issue_role(sh, qtile, ring, share);
+    }
   }
   tc_fence_before();
   __syncthreads();
