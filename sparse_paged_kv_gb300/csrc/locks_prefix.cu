@@ -386,7 +386,7 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
   }
 }
 
-// ---- the issuing thread -------------------------------------------------------------
+// ---- the issuing warp (one lane issues) -------------------------------------------------------------
 // Job J (counted over the block's pieces) is one stage for one softmax group, J & 1.  The products
 // Q K^T run two jobs ahead of the products P V, each with a cursor like this.
 struct Cursor {
@@ -395,7 +395,7 @@ struct Cursor {
   __device__ __forceinline__ bool open(Shared& sh, int share) {
     more = stage0 < share;
     if (!more) return true;
-    if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
+    if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
     const Piece& u = sh.piece[n % kPieces];
     stages = u.stages;
     pair = u.pair;
@@ -430,39 +430,47 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
   auto scores = [&]() {
     const uint32_t w = a.J & 1, t = a.q0 + (a.pair ? w : 0), qs = t & 1;
     const uint32_t c = 2 * a.stage(), slot = c % kRing;
-    if (a.job <= a.pair && !mbar_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead)) return false;
-    if (a.first_of_stage() && !mbar_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
+    if (a.job <= a.pair && !warp_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead)) return false;
+    if (a.first_of_stage() && !warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
       return false;
     const uint64_t da = q_desc + qs * (kTileBytes >> 4), db = k_desc + slot * (kTileBytes >> 4);
+    const bool last_k = a.last_of_stage(), last_q = a.job >= a.njobs - 1 - a.pair;
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {                     // 16 of the 128 dims each, 64 in a half
-      const uint64_t o = uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-      mma_ss(tmem + w * 128, da + o, db + o, kIdescS, k > 0);
+      for (int k = 0; k < 8; ++k) {                   // 16 of the 128 dims each, 64 in a half
+        const uint64_t o = uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+        mma_ss(tmem + w * 128, da + o, db + o, kIdescS, k > 0);
+      }
+      mma_commit(&sh.s_full[w]);
+      if (last_k) mma_commit(&sh.empty[slot]);
+      if (last_q) mma_commit(&sh.q_empty[qs]);
     }
-    mma_commit(&sh.s_full[w]);
-    if (a.last_of_stage()) mma_commit(&sh.empty[slot]);
-    if (a.job >= a.njobs - 1 - a.pair) mma_commit(&sh.q_empty[qs]);
+    __syncwarp();
     return a.advance(sh, share);
   };
   auto values = [&]() {
     const uint32_t w = b.J & 1, c = 2 * b.stage() + 1, slot = c % kRing;
-    if (!mbar_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead)) return false;
-    if (b.first_of_stage() && !mbar_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
+    if (!warp_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead)) return false;
+    if (b.first_of_stage() && !warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
       return false;
     const bool fresh = b.job < 2;                     // of this unit for this group
     if (fresh) {
       const uint32_t n = opened >> (16 * w);
-      if (!mbar_wait_or_dead(&sh.o_empty[w], (n & 1) ^ 1, &sh.dead)) return false;
+      if (!warp_wait_or_dead(&sh.o_empty[w], (n & 1) ^ 1, &sh.dead)) return false;
       opened ^= 1u << (16 * w);
     }
     tc_fence_after();
     const uint64_t db = v_desc + slot * (kTileBytes >> 4);
+    const bool last_v = b.last_of_stage(), last_o = b.job >= b.njobs - 2;
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)                       // 16 of the 128 tokens each
-      mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, db + (uint64_t(k * 2048) >> 4), kIdescO,
-             !fresh || k > 0);
-    if (b.last_of_stage()) mma_commit(&sh.empty[slot]);
-    if (b.job >= b.njobs - 2) mma_commit(&sh.o_full[w]);
+      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
+        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, db + (uint64_t(k * 2048) >> 4), kIdescO,
+               !fresh || k > 0);
+      if (last_v) mma_commit(&sh.empty[slot]);
+      if (last_o) mma_commit(&sh.o_full[w]);
+    }
+    __syncwarp();
     return b.advance(sh, share);
   };
 
@@ -472,7 +480,8 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
     if (ok && a.more) ok = scores();
   }
   // everything issued is done before the block frees its tensor memory
-  mma_commit(&sh.done);
+  if (elect_one()) mma_commit(&sh.done);
+  __syncwarp();
   mbar_wait_bounded(&sh.done, 0);
 }
 
@@ -547,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == kProducerWarp) load_role(p, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
-      else if (warp == kMmaWarp && lane == 0) issue_role(sh, qtile, ring, share);
+      else if (warp == kMmaWarp) issue_role(sh, qtile, ring, share);
     }
   }
   tc_fence_before();
