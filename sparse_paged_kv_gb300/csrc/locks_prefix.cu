@@ -14,7 +14,7 @@
 // blocks, one per SM, take equal shares of the list, so that any mix of lengths
 // fills the chip; a unit cut by a share's border leaves a piece in either block.
 // A block's warps are: one that loads (tensor maps, a ring of five 32 KB
-// tiles, K and V of a stage in turn), one whose first lane issues the matrix
+// tiles, K and V of a stage in turn), one that issues the matrix
 // instructions, and two groups of four for the softmax, thread = query row:
 //   S (128 x 128, tensor memory) = Q K^T    both operands in shared memory
 //   P (bf16, over S's columns)   = 2^(S - m)
@@ -419,10 +419,10 @@ struct Cursor {
 __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int share) {
   constexpr uint32_t kIdescS = mma_idesc(128, 128, false), kIdescO = mma_idesc(128, 128, true);
   const uint32_t tmem = sh.tmem;
-  const uint64_t q_desc = smem_desc(smem_u32(qtile), 16, 1024);
-  const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024);
+  const uint32_t q_desc = smem_desc_lo(smem_u32(qtile), 16);
+  const uint32_t k_desc = smem_desc_lo(smem_u32(ring), 16);
   // 64 columns of V (a half) follow each other at kHalfBytes, 8 tokens at 1024 bytes
-  const uint64_t v_desc = smem_desc(smem_u32(ring), kHalfBytes, 1024);
+  const uint32_t v_desc = smem_desc_lo(smem_u32(ring), kHalfBytes);
   Cursor a = {}, b = {};
   uint32_t opened = 0;                                // accumulators begun by either group, modulo 2, in bits 0 and 16
   bool ok = a.open(sh, share) && b.open(sh, share);
@@ -433,13 +433,15 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
     if (a.job <= a.pair && !warp_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead)) return false;
     if (a.first_of_stage() && !warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
       return false;
-    const uint64_t da = q_desc + qs * (kTileBytes >> 4), db = k_desc + slot * (kTileBytes >> 4);
+    const uint32_t da = warp_uniform(q_desc + qs * (kTileBytes >> 4));
+    const uint32_t db = warp_uniform(k_desc + slot * (kTileBytes >> 4));
+    const uint32_t d = warp_uniform(tmem + w * 128);
     const bool last_k = a.last_of_stage(), last_q = a.job >= a.njobs - 1 - a.pair;
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {                   // 16 of the 128 dims each, 64 in a half
-        const uint64_t o = uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-        mma_ss(tmem + w * 128, da + o, db + o, kIdescS, k > 0);
+        const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+        mma_ss(d, da + o, db + o, kIdescS, k > 0);
       }
       mma_commit(&sh.s_full[w]);
       if (last_k) mma_commit(&sh.empty[slot]);
@@ -460,13 +462,14 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
       opened ^= 1u << (16 * w);
     }
     tc_fence_after();
-    const uint64_t db = v_desc + slot * (kTileBytes >> 4);
+    const uint32_t db = warp_uniform(v_desc + slot * (kTileBytes >> 4));
+    const uint32_t d = warp_uniform(tmem + 256 + w * 128);
+    const uint32_t keep = warp_uniform(!fresh);
     const bool last_v = b.last_of_stage(), last_o = b.job >= b.njobs - 2;
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
-        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, db + (uint64_t(k * 2048) >> 4), kIdescO,
-               !fresh || k > 0);
+        mma_ts(d, d - 256 + k * 8, db + k * (2048 >> 4), kIdescO, k > 0 ? 1u : keep);
       if (last_v) mma_commit(&sh.empty[slot]);
       if (last_o) mma_commit(&sh.o_full[w]);
     }
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* qtile = smem;
   unsigned char* ring = smem + 2 * kTileBytes;
   Shared& sh = *reinterpret_cast<Shared*>(smem + (kRing + 2) * kTileBytes);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
 
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   if (tid == 0) {

@@ -16,12 +16,17 @@
 namespace locks {
 
 // ---- descriptors ------------------------------------------------------------
-// shared-memory matrix descriptor, 128-byte swizzle: start address, leading and
-// stride byte offsets in 16-byte units; version 1 at bit 46, swizzle 2 at bit 61
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((addr >> 4) & 0x3FFF) | uint64_t((lbo >> 4) & 0x3FFF) << 16 |
-         uint64_t((sbo >> 4) & 0x3FFF) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+// Shared-memory matrix descriptor, 128-byte swizzle, 1024 bytes from 8 rows to the next: the low
+// word (start address and leading byte offset in 16-byte units); the high word is the same for all
+// (stride 1024, version 1 at bit 46, swizzle 2 at bit 61).
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFF) | ((lbo >> 4) & 0x3FFF) << 16;
 }
+// A value that all lanes have, in a form that the compiler keeps in a uniform register: a matrix
+// instruction takes its operands from those, and moving five of them there for each one took
+// longer (140 cycles) than the instruction itself (64).
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
 
 // instruction descriptor of kind::f16: bf16 operands, float accumulators, M x N;
 // the second operand MN-major if bit 16 is set
@@ -117,19 +122,23 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ---- matrix instructions (one thread issues) ----------------------------------
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
       : "memory");
 }
 // first operand from tensor memory (two bf16 a column)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %5};\n"
+      " setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
       : "memory");
 }
 // `bar` gets an arrival once everything this thread has issued so far is done

@@ -11,7 +11,7 @@
 // pass over the keys.  A list of stages of 128 tokens is shared out equally
 // over 152 blocks (a stage's result is complete, so pieces need no joining).  A
 // block's 10 warps: one loads keys (tensor maps, a ring of 32 KB tiles) and the
-// unit's queries (two buffers), one's first lane issues the products, and two
+// unit's queries (two buffers), one issues the products, and two
 // groups of four take stages in turn, thread = token, each with an accumulator
 // of its own in tensor memory.  Weights and block ids of a stage are loaded
 // before the wait for its product.
@@ -140,34 +140,40 @@ __device__ void load_role(const WeighParams& p, Shared& sh, unsigned char* qbuf,
 
 __device__ void issue_role(const WeighParams& p, Shared& sh, unsigned char* qbuf, unsigned char* ring,
                            int share) {
-  const uint32_t idesc = mma_idesc(128, p.n_cols, false);
-  const uint32_t q_addr = smem_u32(qbuf), ring_addr = smem_u32(ring), tmem = sh.tmem;
+  const uint32_t idesc = mma_idesc(128, p.n_cols, false), half = p.q_half >> 4;
+  const uint32_t q_desc = smem_desc_lo(smem_u32(qbuf), 16), k_desc = smem_desc_lo(smem_u32(ring), 16);
+  const uint32_t tmem = sh.tmem;
   Walk walk(p, sh, share);
   Unit u;
   int qn = 0, stage = 0;
   bool ok = true;
   while (ok && walk.next(p, u)) {
     const int qs = qn & 1;
-    ok = mbar_wait_or_dead(&sh.q_full[qs], (qn >> 1) & 1, &sh.dead);
+    ok = warp_wait_or_dead(&sh.q_full[qs], (qn >> 1) & 1, &sh.dead);
     ++qn;
+    const uint32_t db = warp_uniform(q_desc + qs * 2 * half);
     for (int s = u.s0; ok && s < u.s1; ++s, ++stage) {
       const int slot = stage % p.ring, w = stage & 1;
-      ok = mbar_wait_or_dead(&sh.full[slot], (stage / p.ring) & 1, &sh.dead) &&
-           mbar_wait_or_dead(&sh.d_empty[w], ((stage >> 1) & 1) ^ 1, &sh.dead);
+      ok = warp_wait_or_dead(&sh.full[slot], (stage / p.ring) & 1, &sh.dead) &&
+           warp_wait_or_dead(&sh.d_empty[w], ((stage >> 1) & 1) ^ 1, &sh.dead);
       if (!ok) break;
       tc_fence_after();
-      const uint64_t da = smem_desc(ring_addr + slot * kTileBytes, 16, 1024);
-      const uint64_t db = smem_desc(q_addr + qs * 2 * p.q_half, 16, 1024);
+      const uint32_t da = warp_uniform(k_desc + slot * (kTileBytes >> 4));
+      const uint32_t d = warp_uniform(tmem + w * p.n_cols);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ss(tmem + w * p.n_cols, da + (uint64_t((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
-               db + (uint64_t((k >> 2) * p.q_half + (k & 3) * 32) >> 4), idesc, k > 0);
-      mma_commit(&sh.d_full[w]);
-      mma_commit(&sh.empty[slot]);
-      if (s == u.s1 - 1) mma_commit(&sh.q_empty[qs]);
+        for (int k = 0; k < 8; ++k)                   // 16 of the 128 dims each, 64 in a half
+          mma_ss(d, da + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                 db + (k >> 2) * half + (k & 3) * 2, idesc, k > 0);
+        mma_commit(&sh.d_full[w]);
+        mma_commit(&sh.empty[slot]);
+        if (s == u.s1 - 1) mma_commit(&sh.q_empty[qs]);
+      }
+      __syncwarp();
     }
   }
-  mma_commit(&sh.done);
+  if (elect_one()) mma_commit(&sh.done);
+  __syncwarp();
   mbar_wait_bounded(&sh.done, 0);
 }
 
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* ring = smem;
   unsigned char* qbuf = ring + p.ring * kTileBytes;
   Shared& sh = *reinterpret_cast<Shared*>(qbuf + 4 * p.q_half);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
 
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, p.tmem_cols);
   if (tid == 0) {
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (share > 0) {
     if (warp < kProducerWarp) weigh_role(p, sh, warp >> 2, share);
     else if (warp == kProducerWarp) load_role(p, sh, qbuf, ring, &map_q, &map_k, share);
-    else if (lane == 0) issue_role(p, sh, qbuf, ring, share);
+    else if (warp == kMmaWarp) issue_role(p, sh, qbuf, ring, share);
   }
   tc_fence_before();
   __syncthreads();
