@@ -388,32 +388,43 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
 
 // ---- the issuing warp (one lane issues) -------------------------------------------------------------
 // Job J (counted over the block's pieces) is one stage for one softmax group, J & 1.  The products
-// Q K^T run two jobs ahead of the products P V, each with a cursor like this.
+// Q K^T run two jobs ahead of the products P V, each with a cursor like this.  The loop is kept
+// short: it shares the instruction cache with the softmax, and the latency of its own instructions,
+// one after another, has to stay below the products' time.
 struct Cursor {
-  int J, job, njobs, pair, stage0, stages, q0, n;
-  bool more;
+  uint32_t J = 0, job = 0, njobs = 0, pair = 0;
+  uint32_t slot, phase = 0;                           // of the ring, for the stage's tile
+  uint32_t tile = 0;                                  // query tiles of the pieces before
+  int stages = 0, n = 0;                              // stages up to and with this piece; the next piece
+  bool more = true;
+  __device__ __forceinline__ explicit Cursor(uint32_t s) : slot(s) {}
   __device__ __forceinline__ bool open(Shared& sh, int share) {
-    more = stage0 < share;
+    more = stages < share;
     if (!more) return true;
-    if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
+    if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
     const Piece& u = sh.piece[n % kPieces];
-    stages = u.stages;
+    ++n;
+    stages += u.stages;
     pair = u.pair;
     njobs = u.jobs();
     job = 0;
     return true;
   }
-  __device__ __forceinline__ bool advance(Shared& sh, int share) {
-    ++J;
-    if (++job < njobs) return true;
-    stage0 += stages;
-    q0 += 1 + pair;
-    ++n;
-    return open(sh, share);
-  }
-  __device__ __forceinline__ int stage() const { return stage0 + (job >> pair); }
   __device__ __forceinline__ bool first_of_stage() const { return !(job & pair); }
   __device__ __forceinline__ bool last_of_stage() const { return !pair || (job & 1); }
+  __device__ __forceinline__ bool advance(Shared& sh, int share) {
+    if (last_of_stage()) {
+      slot += 2;                                      // (keys and values take slots in turn)
+      if (slot >= kRing) {
+        slot -= kRing;
+        phase ^= 1;
+      }
+    }
+    ++J;
+    if (++job < njobs) return true;
+    tile += 1 + pair;
+    return open(sh, share);
+  }
 };
 
 __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int share) {
@@ -423,68 +434,54 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
   const uint32_t k_desc = smem_desc_lo(smem_u32(ring), 16);
   // 64 columns of V (a half) follow each other at kHalfBytes, 8 tokens at 1024 bytes
   const uint32_t v_desc = smem_desc_lo(smem_u32(ring), kHalfBytes);
-  Cursor a = {}, b = {};
-  uint32_t opened = 0;                                // accumulators begun by either group, modulo 2, in bits 0 and 16
+  Cursor a(0), b(1);
+  uint32_t opened = 0;                                // accumulators begun, modulo 2, a bit a group
+  int ahead = 0;
   bool ok = a.open(sh, share) && b.open(sh, share);
-
-  auto scores = [&]() {
-    const uint32_t w = a.J & 1, t = a.q0 + (a.pair ? w : 0), qs = t & 1;
-    const uint32_t c = 2 * a.stage(), slot = c % kRing;
-    if (a.job <= a.pair && !warp_wait_or_dead(&sh.q_full[qs], (t >> 1) & 1, &sh.dead)) return false;
-    if (a.first_of_stage() && !warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
-      return false;
-    const uint32_t da = warp_uniform(q_desc + qs * (kTileBytes >> 4));
-    const uint32_t db = warp_uniform(k_desc + slot * (kTileBytes >> 4));
-    const uint32_t d = warp_uniform(tmem + w * 128);
-    const bool last_k = a.last_of_stage(), last_q = a.job >= a.njobs - 1 - a.pair;
-    if (elect_one()) {
+  while (ok && b.more) {
+    if (ahead == 2) {                                 // P V of job b.J
+      const uint32_t w = b.J & 1;
+      ok = mbar_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead);
+      if (ok && b.first_of_stage()) ok = mbar_wait_or_dead(&sh.full[b.slot], b.phase, &sh.dead);
+      uint32_t add = 1;
+      if (ok && b.job < 2) {                          // the first of this unit for this group
+        add = 0;
+        ok = mbar_wait_or_dead(&sh.o_empty[w], (opened >> w & 1) ^ 1, &sh.dead);
+        opened ^= 1u << w;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t db = v_desc + b.slot * (kTileBytes >> 4), p = tmem + w * 128;
+      const uint32_t d = p + 256;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
+        mma_ts(d, p + 8 * k, db + k * (2048 >> 4), kIdescO, k > 0 ? 1u : add);
+      if (b.last_of_stage()) mma_commit(&sh.empty[b.slot]);
+      if (b.job + 2 >= b.njobs) mma_commit(&sh.o_full[w]);
+      ok = b.advance(sh, share);
+    } else {
+      ++ahead;
+    }
+    if (ok && a.more) {                               // Q K^T of job a.J
+      const uint32_t w = a.J & 1, t = a.tile + (w & a.pair), qs = t & 1;
+      if (a.job <= a.pair) ok = mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead);
+      if (ok && a.first_of_stage()) ok = mbar_wait_or_dead(&sh.full[a.slot], a.phase, &sh.dead);
+      if (!ok) break;
+      const uint32_t da = q_desc + qs * (kTileBytes >> 4), db = k_desc + a.slot * (kTileBytes >> 4);
+      const uint32_t d = tmem + w * 128;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {                   // 16 of the 128 dims each, 64 in a half
         const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
         mma_ss(d, da + o, db + o, kIdescS, k > 0);
       }
       mma_commit(&sh.s_full[w]);
-      if (last_k) mma_commit(&sh.empty[slot]);
-      if (last_q) mma_commit(&sh.q_empty[qs]);
+      if (a.last_of_stage()) mma_commit(&sh.empty[a.slot]);
+      if (a.job + 1 + a.pair >= a.njobs) mma_commit(&sh.q_empty[qs]);
+      ok = a.advance(sh, share);
     }
-    __syncwarp();
-    return a.advance(sh, share);
-  };
-  auto values = [&]() {
-    const uint32_t w = b.J & 1, c = 2 * b.stage() + 1, slot = c % kRing;
-    if (!warp_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead)) return false;
-    if (b.first_of_stage() && !warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead))
-      return false;
-    const bool fresh = b.job < 2;                     // of this unit for this group
-    if (fresh) {
-      const uint32_t n = opened >> (16 * w);
-      if (!warp_wait_or_dead(&sh.o_empty[w], (n & 1) ^ 1, &sh.dead)) return false;
-      opened ^= 1u << (16 * w);
-    }
-    tc_fence_after();
-    const uint32_t db = warp_uniform(v_desc + slot * (kTileBytes >> 4));
-    const uint32_t d = warp_uniform(tmem + 256 + w * 128);
-    const uint32_t keep = warp_uniform(!fresh);
-    const bool last_v = b.last_of_stage(), last_o = b.job >= b.njobs - 2;
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
-        mma_ts(d, d - 256 + k * 8, db + k * (2048 >> 4), kIdescO, k > 0 ? 1u : keep);
-      if (last_v) mma_commit(&sh.empty[slot]);
-      if (last_o) mma_commit(&sh.o_full[w]);
-    }
-    __syncwarp();
-    return b.advance(sh, share);
-  };
-
-  for (int i = 0; ok && i < 2 && a.more; ++i) ok = scores();
-  while (ok && b.more) {
-    ok = values();
-    if (ok && a.more) ok = scores();
   }
   // everything issued is done before the block frees its tensor memory
-  if (elect_one()) mma_commit(&sh.done);
-  __syncwarp();
+  mma_commit(&sh.done);
   mbar_wait_bounded(&sh.done, 0);
 }
 
@@ -559,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == kProducerWarp) load_role(p, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
-      else if (warp == kMmaWarp) issue_role(sh, qtile, ring, share);
+      else if (warp == kMmaWarp && elect_one()) issue_role(sh, qtile, ring, share);
     }
   }
   tc_fence_before();

@@ -175,18 +175,19 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 // Wait for phase `parity` of `bar`.  False, and *dead set, if the limit ran out or another
 // thread of the block gave up: every role then leaves its loop.
 __device__ __forceinline__ bool mbar_wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
+  unsigned long long t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i & 255) continue;
     if (*dead) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
+    const unsigned long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       *dead = 1;
       return false;
     }
   }
+  return true;
 }
 
 // The same for a whole warp: all of its lanes go on, or none.
