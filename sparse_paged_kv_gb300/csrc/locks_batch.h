@@ -26,10 +26,9 @@ struct PrefixParams {
   float* out_lse;                // nullable [batch][n_rows][H_q]
   int32_t* status;               // nullable
   // workspace (see prefix_layout)
-  float* acc;                    // [2 kinds][2 halves][rows][d] first pieces
-  float4* sums;                  // [2][2][rows] (m, l, l of the rounded weights, -)
-  float* carry_acc;              // [blocks][256][d] pieces continued from the block before
-  float4* carry_sums;            // [blocks][256]
+  float* acc;                    // [parts][d]: [2 kinds][2 halves][rows] first pieces, then
+                                 // [blocks][256] pieces continued from the block before
+  float4* sums;                  // [parts] (m, l, l of the rounded weights, -)
   int32_t* entry_start;          // [n_groups + batch + 1] first stage of each entry; their total
   int batch, n_groups, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift;
   int tile_tokens;               // query tokens of a tile: floor(128 / group)
@@ -38,7 +37,7 @@ struct PrefixParams {
 };
 
 struct PrefixLayout {
-  size_t acc, sums, carry_acc, carry_sums, entry_start, total;
+  size_t acc, sums, entry_start, total;
 };
 PrefixLayout prefix_layout(int64_t rows, int64_t entries);
 int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUtensorMap& q_own,

@@ -154,8 +154,6 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.acc = reinterpret_cast<float*>(ws + L.acc);
   p.sums = reinterpret_cast<float4*>(ws + L.sums);
-  p.carry_acc = reinterpret_cast<float*>(ws + L.carry_acc);
-  p.carry_sums = reinterpret_cast<float4*>(ws + L.carry_sums);
   p.entry_start = reinterpret_cast<int32_t*>(ws + L.entry_start);
   p.batch = cfg->batch;
   p.n_groups = n_groups;

@@ -41,27 +41,28 @@ namespace locks {
 namespace {
 
 constexpr int kThreads = 384;                         // three warpgroups: two of softmax, one of the others
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;        // (one issuing warp a softmax group: 9 and 10)
 // registers a thread after the split: 256 * 208 + 128 * 88 = 384 * 168, the launch's
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileBytes = 128 * 256;                 // 128 rows of 128 bf16
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kRing = 5;
-// Pieces handed on: when piece n is written the queries of piece n - 2 have had their last use, so
-// (two products ahead, at least one stage a piece) the softmax groups are past piece n - 8.
+// Pieces handed on.  When piece n is written, the queries of piece n - 2 have had their last use in
+// both groups, so each group's products with the values are issued up to its piece before that
+// (n - 5 at the earliest, if every piece has one stage), and the softmax has read that piece's entry.
 constexpr int kPieces = 16;
+constexpr int kGroupsHeld = 64;                       // groups whose bounds a block holds
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
 // A unit's stages [s0, s0 + stages) that this block has, as the loading warp hands them to the others.
 struct Piece {
   int stages;
-  int pair;               // two tiles: both on every stage; else stages in turn
+  int pair;               // two tiles: a group each, both on every stage; else stages in turn
   int group_pages;        // the unit is a group's (else a sequence's own pages)
   int head, tokens, row, page0;
   int q0, nq;             // query tokens of the unit (at most two tiles)
   int s0;
-  __device__ __forceinline__ int jobs() const { return pair ? 2 * stages : stages; }
 };
 
 struct Shared {
@@ -70,9 +71,10 @@ struct Shared {
   uint64_t full[kRing], empty[kRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t done;
+  uint64_t done[2];
   uint32_t tmem;
   int dead;                                           // a wait ran out: every role leaves
+  int group_start[kGroupsHeld + 1], group_pages[kGroupsHeld];
   int bad[8];                                         // pages of a stage whose block is invalid, by stage & 7
   ListPlace place;
 };
@@ -82,24 +84,28 @@ static_assert(kSmemBytes <= kMaxSmemBlock, "shared memory of a block");
 // ---- the list of work -----------------------------------------------------------
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-__device__ __forceinline__ int start_of(const PrefixParams& p, int g) {
-  return clamp_int(p.group_starts[g], 0, p.batch);
-}
-__device__ __forceinline__ int pages_of(const PrefixParams& p, int g) {
-  return clamp_int(p.prefix_pages[g], 0, p.max_pages);
-}
+// bounds and pages of the groups, held in shared memory or (many of them) as given
+struct Groups {
+  const int32_t *start, *pages;
+  __device__ __forceinline__ int start_of(const PrefixParams& p, int g) const {
+    return clamp_int(start[g], 0, p.batch);
+  }
+  __device__ __forceinline__ int pages_of(const PrefixParams& p, int g) const {
+    return clamp_int(pages[g], 0, p.max_pages);
+  }
+  // the group of sequence b, or -1
+  __device__ int of(const PrefixParams& p, int b) const {
+    int lo = 0, hi = p.n_groups;                      // the groups that start at or before b
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start_of(p, mid) <= b) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo > 0 && b < start_of(p, lo) ? lo - 1 : -1;
+  }
+};
 __device__ __forceinline__ int length_of(const PrefixParams& p, int b) {
   return clamp_int(p.seq_lens[b], 0, p.max_pages * p.page_size);
-}
-// the group of sequence b, or -1
-__device__ int group_of(const PrefixParams& p, int b) {
-  int lo = 0, hi = p.n_groups;                        // the last group that starts at or before b
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (start_of(p, mid) <= b) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo > 0 && b < start_of(p, lo) ? lo - 1 : -1;
 }
 
 // Entry e < n_groups: the shared pages of group e; else the own pages of sequence e - n_groups.
@@ -109,20 +115,20 @@ struct Entry {
   int q0, nq, tiles;      // first query token (of all), how many, in units of two tiles a head
 };
 
-__device__ Entry load_entry(const PrefixParams& p, int e) {
+__device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) {
   Entry n;
   if (e < p.n_groups) {
-    const int a = start_of(p, e), seqs = max(0, start_of(p, e + 1) - a);
-    n.tokens = pages_of(p, e) * p.page_size;
+    const int a = groups.start_of(p, e), seqs = max(0, groups.start_of(p, e + 1) - a);
+    n.tokens = groups.pages_of(p, e) * p.page_size;
     n.row = a;
     n.page0 = 0;
     n.q0 = a * p.n_rows;
     n.nq = seqs * p.n_rows;
     if (n.nq == 0) n.tokens = 0;
   } else {
-    const int b = e - p.n_groups, g = group_of(p, b);
-    n.page0 = g >= 0 ? pages_of(p, g) : 0;
-    n.tokens = max(0, length_of(p, b) - n.page0 * p.page_size);
+    const int b = e - p.n_groups, len = length_of(p, b), g = groups.of(p, b);
+    n.page0 = g >= 0 ? groups.pages_of(p, g) : 0;
+    n.tokens = max(0, len - n.page0 * p.page_size);
     n.row = b;
     n.q0 = b * p.n_rows;
     n.nq = p.n_rows;
@@ -136,15 +142,17 @@ __device__ Entry load_entry(const PrefixParams& p, int e) {
 // The pieces of this block's share, in the list's order.
 struct Walk {
   int e, offset, left;
+  Groups groups;
   Entry n;
-  __device__ Walk(const PrefixParams& p, const Shared& sh, int share)
-      : e(sh.place.entry), offset(sh.place.offset), left(share), n(load_entry(p, e)) {}
+  __device__ Walk(const PrefixParams& p, const Groups& groups, const Shared& sh, int share)
+      : e(sh.place.entry), offset(sh.place.offset), left(share), groups(groups),
+        n(load_entry(p, groups, e)) {}
   __device__ bool next(const PrefixParams& p, Piece& u) {
     if (left <= 0) return false;
     while (offset >= n.units * n.stages) {
       offset = 0;
       if (++e >= p.n_groups + p.batch) return false;
-      n = load_entry(p, e);
+      n = load_entry(p, groups, e);
     }
     const int unit = offset / n.stages, tile = unit % n.tiles;
     u.group_pages = e < p.n_groups;
@@ -171,27 +179,32 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
   const uint32_t t_s = lanes + w * 128, t_o = lanes + 256 + w * 128;
   const int rt = tid / p.group, head_in_group = tid % p.group;
   const int npg_shift = p.page_shift;
-  int job0 = 0, stage0 = 0, units = 0;
+  uint32_t jobs = 0, units = 0;                       // of this group
+  int stage0 = 0;
   for (int n = 0; stage0 < share; ++n) {
     if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return;
     const Piece u = sh.piece[n % kPieces];
-    const int njobs = u.jobs();
-    const int first = (job0 & 1) == w ? 0 : 1;
-    if (first < njobs) {
+    const int first = u.pair ? 0 : (stage0 ^ w) & 1, step = u.pair ? 1 : 2;
+    if (first < u.stages) {
       const int tq = (u.pair ? w * p.tile_tokens : 0) + rt;
       const bool valid = rt < p.tile_tokens && tq < u.nq;
       int lim = 1 << 30;                              // tokens of the unit that this row sees
       const int qt = u.q0 + tq;                       // query token among the batch's
       if (valid) {
-        const int b = qt / p.n_rows, r = qt - b * p.n_rows;
-        lim = clamp_int(length_of(p, b) - p.n_rows + r + 1 - u.page0 * p.page_size, 0, u.tokens);
+        if (u.group_pages) {
+          const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
+          lim = length_of(p, b) - p.n_rows + (qt - b * p.n_rows) + 1;
+        } else {
+          lim = u.tokens - p.n_rows + tq + 1;
+        }
+        lim = clamp_int(lim, 0, u.tokens);
       }
       const bool any = __any_sync(kFull, valid);
       float m = -INFINITY, l = 0.f, lr = 0.f;
-      for (int job = first; job < njobs; job += 2) {
-        const int i = u.pair ? job >> 1 : job;
+      for (int i = first; i < u.stages; i += step) {
         const int tok = (u.s0 + i) * kStageTok, nv = min(kStageTok, u.tokens - tok);
-        if (!warp_wait_or_dead(&sh.s_full[w], ((job0 + job) >> 1) & 1, &sh.dead)) return;
+        if (!warp_wait_or_dead(&sh.s_full[w], jobs & 1, &sh.dead)) return;
+        ++jobs;
         tc_fence_after();
         const int bad = *static_cast<volatile int*>(&sh.bad[(stage0 + i) & 7]);
         if (any) {
@@ -219,7 +232,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
             m = mn;
             l *= f;
             lr *= f;
-            if (job >= 2) {                           // (the first product overwrites O)
+            if (i != first) {                         // (the first product overwrites O)
 #pragma unroll 1
               for (int c = 0; c < 128; c += 16) {
                 float o[16];
@@ -277,20 +290,13 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
       ++units;
       tc_fence_after();
       if (any) {
-        const int half = u.pair ? 0 : first;
+        const int half = u.pair ? 0 : first;              // (of the piece's stages, in turn)
         const int64_t row = int64_t(qt) * (p.n_kv_heads * p.group) + u.head * p.group + head_in_group;
-        float* acc;
-        float4* sums;
-        if (u.s0 == 0) {
-          const int64_t at = (u.group_pages ? 0 : 2 * p.rows) + half * p.rows + row;
-          acc = p.acc + at * kHeadDim;
-          sums = p.sums + at;
-        } else {
-          const int64_t at = int64_t(blockIdx.x) * 256 + (u.pair ? w : half) * 128 + tid;
-          acc = p.carry_acc + at * kHeadDim;
-          sums = p.carry_sums + at;
-        }
-        if (valid) *sums = make_float4(m, l, lr, 0.f);
+        // the first piece of a unit by the row, one continued from the block before by the block
+        const int64_t at = u.s0 == 0 ? ((u.group_pages ? 0 : 2) + half) * p.rows + row
+                                     : 4 * p.rows + int64_t(blockIdx.x) * 256 + (u.pair ? w : half) * 128 + tid;
+        float* acc = p.acc + at * kHeadDim;
+        if (valid) p.sums[at] = make_float4(m, l, lr, 0.f);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           float o[32];
@@ -307,18 +313,17 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty[w]);
     }
-    job0 += njobs;
     stage0 += u.stages;
   }
 }
 
 // ---- the loading warp -------------------------------------------------------------
-__device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtile,
+__device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& sh, unsigned char* qtile,
                           unsigned char* ring, const CUtensorMap* map_qg, const CUtensorMap* map_qo,
                           const CUtensorMap* map_k, const CUtensorMap* map_v, int share) {
   const int lane = threadIdx.x & 31;
   const int per_stage = kStageTok >> p.page_shift;
-  Walk walk(p, sh, share);
+  Walk walk(p, groups, sh, share);
   Piece u;
   int qn = 0, stage = 0;
   bool ok = true;
@@ -386,103 +391,83 @@ __device__ void load_role(const PrefixParams& p, Shared& sh, unsigned char* qtil
   }
 }
 
-// ---- the issuing warp (one lane issues) -------------------------------------------------------------
-// Job J (counted over the block's pieces) is one stage for one softmax group, J & 1.  The products
-// Q K^T run two jobs ahead of the products P V, each with a cursor like this.  The loop is kept
-// short: it shares the instruction cache with the softmax, and the latency of its own instructions,
-// one after another, has to stay below the products' time.
-struct Cursor {
-  uint32_t J = 0, job = 0, njobs = 0, pair = 0;
-  uint32_t slot, phase = 0;                           // of the ring, for the stage's tile
-  uint32_t tile = 0;                                  // query tiles of the pieces before
-  int stages = 0, n = 0;                              // stages up to and with this piece; the next piece
-  bool more = true;
-  __device__ __forceinline__ explicit Cursor(uint32_t s) : slot(s) {}
-  __device__ __forceinline__ bool open(Shared& sh, int share) {
-    more = stages < share;
-    if (!more) return true;
-    if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return false;
-    const Piece& u = sh.piece[n % kPieces];
-    ++n;
-    stages += u.stages;
-    pair = u.pair;
-    njobs = u.jobs();
-    job = 0;
-    return true;
-  }
-  __device__ __forceinline__ bool first_of_stage() const { return !(job & pair); }
-  __device__ __forceinline__ bool last_of_stage() const { return !pair || (job & 1); }
-  __device__ __forceinline__ bool advance(Shared& sh, int share) {
-    if (last_of_stage()) {
-      slot += 2;                                      // (keys and values take slots in turn)
-      if (slot >= kRing) {
-        slot -= kRing;
-        phase ^= 1;
-      }
-    }
-    ++J;
-    if (++job < njobs) return true;
-    tile += 1 + pair;
-    return open(sh, share);
-  }
-};
-
-__device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int share) {
+// ---- the issuing threads ------------------------------------------------------------
+// One a softmax group w: its latency, one instruction after another, is as long as the products, so a
+// single one for both groups would bound the kernel.  Each goes S, (softmax), O += P V, next S; the
+// products of the two meet in the tensor cores' queue.  A wait tells phases apart by one bit, so
+// whoever waits for a phase has to know that the one before is over: each thread waits for every
+// tile and every piece's queries, also for those that only the other group uses, and each tile is
+// free when both have been there.
+__device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int w, int share) {
   constexpr uint32_t kIdescS = mma_idesc(128, 128, false), kIdescO = mma_idesc(128, 128, true);
-  const uint32_t tmem = sh.tmem;
+  const uint32_t t_s = sh.tmem + w * 128, t_o = t_s + 256;
   const uint32_t q_desc = smem_desc_lo(smem_u32(qtile), 16);
   const uint32_t k_desc = smem_desc_lo(smem_u32(ring), 16);
   // 64 columns of V (a half) follow each other at kHalfBytes, 8 tokens at 1024 bytes
   const uint32_t v_desc = smem_desc_lo(smem_u32(ring), kHalfBytes);
-  Cursor a(0), b(1);
-  uint32_t opened = 0;                                // accumulators begun, modulo 2, a bit a group
-  int ahead = 0;
-  bool ok = a.open(sh, share) && b.open(sh, share);
-  while (ok && b.more) {
-    if (ahead == 2) {                                 // P V of job b.J
-      const uint32_t w = b.J & 1;
-      ok = mbar_wait_or_dead(&sh.p_full[w], (b.J >> 1) & 1, &sh.dead);
-      if (ok && b.first_of_stage()) ok = mbar_wait_or_dead(&sh.full[b.slot], b.phase, &sh.dead);
-      uint32_t add = 1;
-      if (ok && b.job < 2) {                          // the first of this unit for this group
-        add = 0;
-        ok = mbar_wait_or_dead(&sh.o_empty[w], (opened >> w & 1) ^ 1, &sh.dead);
-        opened ^= 1u << w;
-      }
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t db = v_desc + b.slot * (kTileBytes >> 4), p = tmem + w * 128;
-      const uint32_t d = p + 256;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
-        mma_ts(d, p + 8 * k, db + k * (2048 >> 4), kIdescO, k > 0 ? 1u : add);
-      if (b.last_of_stage()) mma_commit(&sh.empty[b.slot]);
-      if (b.job + 2 >= b.njobs) mma_commit(&sh.o_full[w]);
-      ok = b.advance(sh, share);
-    } else {
-      ++ahead;
+  uint32_t jobs = 0, units = 0;                       // of this group
+  int stage0 = 0, tile0 = 0;
+  bool ok = true;
+  for (int n = 0; ok && stage0 < share; ++n) {
+    if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) break;
+    const int stages = sh.piece[n % kPieces].stages, pair = sh.piece[n % kPieces].pair;
+    const int first = pair ? 0 : (stage0 ^ w) & 1, step = 2 - pair;
+    const uint32_t t = tile0 + (w & pair), qs = t & 1;
+    if (first >= stages) {
+      ok = mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead);
+      if (ok) mbar_arrive(&sh.q_empty[qs]);
     }
-    if (ok && a.more) {                               // Q K^T of job a.J
-      const uint32_t w = a.J & 1, t = a.tile + (w & a.pair), qs = t & 1;
-      if (a.job <= a.pair) ok = mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead);
-      if (ok && a.first_of_stage()) ok = mbar_wait_or_dead(&sh.full[a.slot], a.phase, &sh.dead);
+    for (int i = 0; ok && i < stages; ++i) {
+      const uint32_t c = 2 * (stage0 + i), ks = c % kRing, kp = c / kRing & 1;
+      const uint32_t vs = (c + 1) % kRing, vp = (c + 1) / kRing & 1;
+      if (!pair && ((stage0 + i) ^ w) & 1) {          // the other group's stage
+        ok = mbar_wait_or_dead(&sh.full[ks], kp, &sh.dead);
+        if (!ok) break;
+        mbar_arrive(&sh.empty[ks]);
+        ok = mbar_wait_or_dead(&sh.full[vs], vp, &sh.dead);
+        if (!ok) break;
+        mbar_arrive(&sh.empty[vs]);
+        continue;
+      }
+      const bool last = i + step >= stages;
+      ok = (i != first || mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead)) &&
+           mbar_wait_or_dead(&sh.full[ks], kp, &sh.dead);
       if (!ok) break;
-      const uint32_t da = q_desc + qs * (kTileBytes >> 4), db = k_desc + a.slot * (kTileBytes >> 4);
-      const uint32_t d = tmem + w * 128;
+      const uint32_t da = q_desc + qs * (kTileBytes >> 4), dk = k_desc + ks * (kTileBytes >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {                   // 16 of the 128 dims each, 64 in a half
         const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-        mma_ss(d, da + o, db + o, kIdescS, k > 0);
+        mma_ss(t_s, da + o, dk + o, kIdescS, k > 0);
       }
+      // (a pair's query tiles are used by one group each, which gives both arrivals)
       mma_commit(&sh.s_full[w]);
-      if (a.last_of_stage()) mma_commit(&sh.empty[a.slot]);
-      if (a.job + 1 + a.pair >= a.njobs) mma_commit(&sh.q_empty[qs]);
-      ok = a.advance(sh, share);
+      mma_commit(&sh.empty[ks]);
+      if (last) {
+        mma_commit(&sh.q_empty[qs]);
+        if (pair) mma_commit(&sh.q_empty[qs]);
+      }
+      ok = mbar_wait_or_dead(&sh.full[vs], vp, &sh.dead) &&
+           (i != first || mbar_wait_or_dead(&sh.o_empty[w], (units & 1) ^ 1, &sh.dead)) &&
+           mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
+      if (!ok) break;
+      ++jobs;
+      tc_fence_after();
+      const uint32_t dv = v_desc + vs * (kTileBytes >> 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
+        mma_ts(t_o, t_s + 8 * k, dv + k * (2048 >> 4), kIdescO, i != first || k > 0);
+      mma_commit(&sh.empty[vs]);
+      if (last) {
+        mma_commit(&sh.o_full[w]);
+        ++units;
+      }
     }
+    stage0 += stages;
+    tile0 += 1 + pair;
   }
   // everything issued is done before the block frees its tensor memory
-  mma_commit(&sh.done);
-  mbar_wait_bounded(&sh.done, 0);
+  mma_commit(&sh.done[w]);
+  mbar_wait_bounded(&sh.done[w], 0);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -501,18 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], 2);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_empty[i], 4);
+      mbar_init(&sh.done[i], 1);
     }
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.piece_full[i], 1);
-    mbar_init(&sh.done, 1);
     mbar_fence_init();
     sh.dead = 0;
     prefetch_map(&map_qg);
@@ -522,13 +507,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // what follows reads memory that the kernel before this one may write
   griddep_wait();
+  Groups groups = {p.group_starts, p.prefix_pages};
+  if (p.n_groups <= kGroupsHeld) {
+    for (int i = tid; i <= p.n_groups && p.n_groups; i += kThreads) {
+      sh.group_start[i] = p.group_starts[i];
+      if (i < p.n_groups) sh.group_pages[i] = p.prefix_pages[i];
+    }
+    if (tid < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + tid));
+    groups.start = sh.group_start;
+    groups.pages = sh.group_pages;
+    __syncthreads();
+  }
 
   tc_fence_before();
   const int entries = p.n_groups + p.batch;
   int total;
   const int share = locate<kThreads>(
       [&](int e) {
-        const Entry n = load_entry(p, e);
+        const Entry n = load_entry(p, groups, e);
         return n.units * n.stages;
       },
       entries, blockIdx.x, kBatchSms, sh.place, total,
@@ -540,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = p.seq_lens[e - p.n_groups];
           if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
         } else {
-          const int a = p.group_starts[e], z = p.group_starts[e + 1], n_pages = p.prefix_pages[e];
+          const int a = groups.start[e], z = groups.start[e + 1], n_pages = groups.pages[e];
           if (a < 0 || z < a || z > p.batch || n_pages < 0 || n_pages > p.max_pages)
             flag_status(p.status, LOCKS_DEV_BAD_GROUP);
         }
@@ -555,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       softmax_role(p, sh, ring, warp >> 2, share);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-      if (warp == kProducerWarp) load_role(p, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
-      else if (warp == kMmaWarp && elect_one()) issue_role(sh, qtile, ring, share);
+      if (warp == kProducerWarp) load_role(p, groups, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
+      else if (warp < kMmaWarp + 2 && elect_one()) issue_role(sh, qtile, ring, warp - kMmaWarp, share);
     }
   }
   tc_fence_before();
@@ -566,73 +562,119 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_free(sh.tmem, kTmemCols);
 }
 
-// ---- joining the pieces: a warp per (query token, head) row -------------------------
+// ---- joining the pieces ---------------------------------------------------------------
+// A block of 8 warps has one (query token, KV head).  Where the parts of its rows lie (a piece of the
+// group's pages or of the sequence's own, for either softmax group) is found once, lane = piece.  With
+// fewer rows than warps several warps share a row's parts and are joined in shared memory.
 constexpr int kJoinWarps = 8;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParams p) {
+  __shared__ int s_n[2];
+  __shared__ int64_t s_part[2][2 * kBatchSms];        // index of the first row's part, or -1
+  __shared__ __align__(16) float s_acc[kJoinWarps][kHeadDim];
+  __shared__ float4 s_sum[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int qt = blockIdx.x / p.n_kv_heads, head = blockIdx.x - qt * p.n_kv_heads;
+  const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
+  const int64_t row0 = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group;
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int hq = p.n_kv_heads * p.group;
-  const int qt = int(row / hq), head_q = int(row - int64_t(qt) * hq);
-  const int b = qt / p.n_rows, head = head_q / p.group;
-  const int entries = p.n_groups + p.batch;
-  const int total = p.entry_start[entries];
-  float M = -INFINITY, L = 0.f, LR = 0.f;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-
-  auto add = [&](const float* acc, const float4* sums) {
-    const float4 s = *sums;
-    // (a part in which the row sees nothing has no sum, and an accumulator of no account)
-    if (s.y == 0.f) return;
-    const float mn = fmaxf(M, s.x);
-    const float f = M == -INFINITY ? 0.f : exp2f(M - mn), g = exp2f(s.x - mn);
-    const float4 a = *reinterpret_cast<const float4*>(acc + 4 * lane);
-    A.x = A.x * f + a.x * g;
-    A.y = A.y * f + a.y * g;
-    A.z = A.z * f + a.z * g;
-    A.w = A.w * f + a.w * g;
-    L = L * f + s.y * g;
-    LR = LR * f + s.z * g;
-    M = mn;
-  };
-  auto unit = [&](int e, int kind) {
-    const Entry n = load_entry(p, e);
-    if (n.units * n.stages == 0) return;
-    const int tq = qt - n.q0, tile = tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
-    const bool pair = n.nq - tile * 2 * p.tile_tokens > p.tile_tokens;
-    const int w = in / p.tile_tokens;
-    const int r = (in - w * p.tile_tokens) * p.group + head_q - head * p.group;
-    const int first = p.entry_start[e] + (head * n.tiles + tile) * n.stages;
-    int at = first;
-    while (at < first + n.stages) {
-      const int c = int(((int64_t(at) + 1) * kBatchSms - 1) / total);
-      const int end = min(first + n.stages, share_begin(total, c + 1, kBatchSms));
-      for (int half = 0; half < (pair ? 1 : min(2, end - at)); ++half) {
-        if (at == first) {
-          const int64_t i = (2 * kind + half) * p.rows + row;
-          add(p.acc + i * kHeadDim, p.sums + i);
-        } else {
-          const int64_t i = int64_t(c) * 256 + (pair ? w : half) * 128 + r;
-          add(p.carry_acc + i * kHeadDim, p.carry_sums + i);
+  if (warp < 2) {                                     // 0: the group's pages, 1: the sequence's own
+    const Groups groups = {p.group_starts, p.prefix_pages};
+    const int total = p.entry_start[p.n_groups + p.batch];
+    const int g = warp == 0 ? groups.of(p, b) : 0, e = warp == 0 ? g : p.n_groups + b;
+    int pieces = 0;
+    if (g >= 0) {
+      const Entry n = load_entry(p, groups, e);
+      const int tq = qt - n.q0, tile = tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
+      const bool pair = n.nq - tile * 2 * p.tile_tokens > p.tile_tokens;
+      const int w = in >= p.tile_tokens, r = (in - w * p.tile_tokens) * p.group;
+      const int first = p.entry_start[e] + (head * n.tiles + tile) * n.stages, end = first + n.stages;
+      if (n.stages > 0) {
+        // the block of a stage: an estimate, put right
+        auto block_of = [&](int stage) {
+          int c = min(kBatchSms - 1, int(float(stage) * kBatchSms / float(total)));
+          while (share_begin(total, c + 1, kBatchSms) <= stage) ++c;
+          while (share_begin(total, c, kBatchSms) > stage) --c;
+          return c;
+        };
+        const int c0 = block_of(first);
+        pieces = block_of(end - 1) - c0 + 1;
+        for (int i = lane; i < pieces; i += 32) {
+          const int at = max(first, share_begin(total, c0 + i, kBatchSms));
+          const int to = min(end, share_begin(total, c0 + i + 1, kBatchSms));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            int64_t x = i == 0 ? (2 * warp + half) * p.rows + row0
+                               : 4 * p.rows + int64_t(c0 + i) * 256 + (pair ? w : half) * 128 + r;
+            if (half == 1 && (pair || to - at < 2)) x = -1;
+            if (to <= at) x = -1;
+            s_part[warp][2 * i + half] = x;
+          }
         }
       }
-      at = end;
     }
-  };
-  const int g = group_of(p, b);
-  if (g >= 0) unit(g, 0);
-  unit(p.n_groups + b, 1);
-
-  const float inv = LR == 0.f ? 0.f : 1.f / LR;
-  const __nv_bfloat162 o01 = __floats2bfloat162_rn(A.x * inv, A.y * inv);
-  const __nv_bfloat162 o23 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
-  uint2 ow;
-  ow.x = *reinterpret_cast<const uint32_t*>(&o01);
-  ow.y = *reinterpret_cast<const uint32_t*>(&o23);
-  *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = ow;
-  if (lane == 0 && p.out_lse) p.out_lse[row] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+    if (lane == 0) s_n[warp] = 2 * pieces;
+  }
+  __syncthreads();
+  const int n0 = s_n[0], n = n0 + s_n[1];
+  // warps a row: 8 / G, G rounded up to a power of two
+  int each = kJoinWarps;
+  while (each > 1 && each * p.group > kJoinWarps) each >>= 1;
+  const int sub = warp & (each - 1);
+  for (int g0 = 0; g0 < p.group; g0 += kJoinWarps / each) {
+    const int g = g0 + warp / each;
+    float M = -INFINITY, L = 0.f, LR = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float4 s, float4 a) {
+      // (a part in which the row sees nothing has no sum, and an accumulator of no account)
+      if (s.y == 0.f) return;
+      const float mn = fmaxf(M, s.x);
+      const float f = M == -INFINITY ? 0.f : exp2f(M - mn), h = exp2f(s.x - mn);
+      A.x = A.x * f + a.x * h;
+      A.y = A.y * f + a.y * h;
+      A.z = A.z * f + a.z * h;
+      A.w = A.w * f + a.w * h;
+      L = L * f + s.y * h;
+      LR = LR * f + s.z * h;
+      M = mn;
+    };
+    if (g < p.group) {
+      constexpr int kAhead = 4;
+      for (int t0 = sub; t0 < n; t0 += each * kAhead) {
+        float4 s[kAhead], a[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int t = t0 + k * each;
+          int64_t x = t >= n ? -1 : t < n0 ? s_part[0][t] : s_part[1][t - n0];
+          s[k].y = 0.f;
+          if (x >= 0) {
+            s[k] = p.sums[x + g];
+            a[k] = *reinterpret_cast<const float4*>(p.acc + (x + g) * kHeadDim + 4 * lane);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) add(s[k], a[k]);
+      }
+    }
+    if (each > 1) {
+      __syncthreads();
+      *reinterpret_cast<float4*>(&s_acc[warp][4 * lane]) = A;
+      if (lane == 0) s_sum[warp] = make_float4(M, L, LR, 0.f);
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < each; ++k)
+          add(s_sum[warp + k], *reinterpret_cast<const float4*>(&s_acc[warp + k][4 * lane]));
+    }
+    if (sub != 0 || g >= p.group) continue;
+    const float inv = LR == 0.f ? 0.f : 1.f / LR;
+    const __nv_bfloat162 o01 = __floats2bfloat162_rn(A.x * inv, A.y * inv);
+    const __nv_bfloat162 o23 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
+    uint2 ow;
+    ow.x = *reinterpret_cast<const uint32_t*>(&o01);
+    ow.y = *reinterpret_cast<const uint32_t*>(&o23);
+    *reinterpret_cast<uint2*>(p.out + (row0 + g) * kHeadDim + 4 * lane) = ow;
+    if (lane == 0 && p.out_lse) p.out_lse[row0 + g] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+  }
 }
 
 }  // namespace
@@ -640,11 +682,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
 PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
   PrefixLayout L;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t parts = size_t(4) * rows + size_t(kBatchSms) * 256;
   L.acc = 0;
-  L.sums = up(L.acc + size_t(4) * rows * kHeadDim * sizeof(float));
-  L.carry_acc = up(L.sums + size_t(4) * rows * sizeof(float4));
-  L.carry_sums = up(L.carry_acc + size_t(kBatchSms) * 256 * kHeadDim * sizeof(float));
-  L.entry_start = up(L.carry_sums + size_t(kBatchSms) * 256 * sizeof(float4));
+  L.sums = up(L.acc + parts * kHeadDim * sizeof(float));
+  L.entry_start = up(L.sums + parts * sizeof(float4));
   L.total = up(L.entry_start + size_t(entries + 1) * sizeof(int32_t));
   return L;
 }
@@ -669,8 +710,7 @@ int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUten
   lc.numAttrs = 1;
   if (cudaLaunchKernelEx(&lc, prefix_kernel, p, q_group, q_own, k, v) != cudaSuccess)
     return LOCKS_ERR_CUDA;
-  const int64_t blocks = (p.rows + kJoinWarps - 1) / kJoinWarps;
-  return launch_dependent(join_kernel, dim3(unsigned(blocks)), kJoinWarps * 32, 0, p, stream);
+  return launch_dependent(join_kernel, dim3(unsigned(p.batch) * p.n_rows * p.n_kv_heads), kJoinWarps * 32, 0, p, stream);
 }
 
 }  // namespace locks
