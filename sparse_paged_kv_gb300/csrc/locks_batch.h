@@ -28,10 +28,11 @@ struct PrefixParams {
   // workspace (see prefix_layout)
   float* acc;                    // [parts][d]: [2 kinds][2 halves][rows] first pieces, then
                                  // [blocks][256] pieces continued from the block before
-  float4* sums;                  // [parts] (m, l, l of the rounded weights, -)
+  float4* sums;                  // [parts][2 halves of the columns] (m, l, l of the rounded weights, -)
   int32_t* entry_start;          // [n_groups + batch + 1] first stage of each entry; their total
   int batch, n_groups, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift;
   int tile_tokens;               // query tokens of a tile: floor(128 / group)
+  uint64_t tile_magic;           // ceil(2^32 / (2 tile_tokens)): n / (2 tile_tokens) = n * magic >> 32 below 2^24
   int64_t rows;                  // batch * n_rows * n_q_heads
   float scale_log2;
 };

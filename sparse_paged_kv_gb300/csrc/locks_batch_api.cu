@@ -53,7 +53,8 @@ int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
   const int64_t units = int64_t(c->batch) + n_groups +
                         int64_t(c->batch) * n_rows / (2 * tile_tokens(c)) + 1;
   if (stages * units * c->n_kv_heads >= (int64_t(1) << 31) ||
-      int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 31))
+      int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 31) ||
+      int64_t(c->batch) * n_rows >= (1 << 24) - 256)
     return LOCKS_ERR_UNSUPPORTED;
   return LOCKS_OK;
 }
@@ -165,6 +166,7 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
   p.page_size = cfg->page_size;
   p.page_shift = page_shift(cfg);
   p.tile_tokens = tile_tokens(cfg);
+  p.tile_magic = ((uint64_t(1) << 32) + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
   p.scale_log2 = logit_scale_log2();
   CUtensorMap qg, qo, mk, mv;
   const int own = n_rows < p.tile_tokens ? n_rows : p.tile_tokens;

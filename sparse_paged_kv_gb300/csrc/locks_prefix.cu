@@ -14,15 +14,15 @@
 // blocks, one per SM, take equal shares of the list, so that any mix of lengths
 // fills the chip; a unit cut by a share's border leaves a piece in either block.
 // A block's warps are: one that loads (tensor maps, a ring of five 32 KB
-// tiles, K and V of a stage in turn), one that issues the matrix
-// instructions, and two groups of four for the softmax, thread = query row:
+// tiles, K and V of a stage in turn), two whose first lanes issue the matrix
+// instructions, and two groups of eight for the softmax, two warps to 32 rows:
 //   S (128 x 128, tensor memory) = Q K^T    both operands in shared memory
 //   P (bf16, over S's columns)   = 2^(S - m)
 //   O (128 x 128, tensor memory) += P V     P from tensor memory
 // A stage's product for one group runs while the other group exponentiates:
 // with more than 128 rows the groups are the two halves of them, both on every
 // stage; with fewer rows they take stages in turn, each with its own m, l and O
-// (two halves of a piece, joined as pieces are).  The accumulator is brought to
+// (two parts of a piece, joined as pieces are).  The accumulator is brought to
 // a new maximum only where a row's maximum grew by more than 2^8, so rarely.
 // A second kernel joins the pieces of each row.
 //
@@ -31,6 +31,8 @@
 // output's own rounding is as large).  The output divides by the sum of the
 // rounded weights, so that a row with one dominant token keeps that token's
 // value exactly; the log-sum-exp comes from the unrounded sum.
+#include <climits>
+
 #include "locks_batch.h"
 #include "locks_batch.cuh"
 #include "locks_kv.cuh"
@@ -40,10 +42,11 @@ namespace locks {
 
 namespace {
 
-constexpr int kThreads = 384;                         // three warpgroups: two of softmax, one of the others
-constexpr int kProducerWarp = 8, kMmaWarp = 9;        // (one issuing warp a softmax group: 9 and 10)
-// registers a thread after the split: 256 * 208 + 128 * 88 = 384 * 168, the launch's
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxWarps = 16;                     // two groups, two halves of the columns, four quarters of the rows
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;   // (two issuing warps)
+// registers a thread after the split: 512 * 104 + 128 * 64 = 640 * 96, the launch's
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kTileBytes = 128 * 256;                 // 128 rows of 128 bf16
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kRing = 5;
@@ -73,12 +76,13 @@ struct Shared {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t done[2];
   uint32_t tmem;
+  int flag[2][2][4][2];                               // what a softmax warp tells its partner
   int dead;                                           // a wait ran out: every role leaves
   int group_start[kGroupsHeld + 1], group_pages[kGroupsHeld];
   int bad[8];                                         // pages of a stage whose block is invalid, by stage & 7
   ListPlace place;
 };
-constexpr size_t kSmemBytes = size_t(kRing + 2) * kTileBytes + 1024 + sizeof(Shared);
+constexpr size_t kSmemBytes = size_t(kRing + 2) * kTileBytes + sizeof(Shared);
 static_assert(kSmemBytes <= kMaxSmemBlock, "shared memory of a block");
 
 // ---- the list of work -----------------------------------------------------------
@@ -134,7 +138,7 @@ __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) 
     n.nq = p.n_rows;
   }
   n.stages = (n.tokens + kStageTok - 1) / kStageTok;
-  n.tiles = (n.nq + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+  n.tiles = int(uint64_t(uint32_t(n.nq + 2 * p.tile_tokens - 1)) * p.tile_magic >> 32);
   n.units = n.tiles * p.n_kv_heads;
   return n;
 }
@@ -154,9 +158,9 @@ struct Walk {
       if (++e >= p.n_groups + p.batch) return false;
       n = load_entry(p, groups, e);
     }
-    const int unit = offset / n.stages, tile = unit % n.tiles;
+    const int unit = offset / n.stages, tile = n.tiles == 1 ? 0 : unit % n.tiles;
     u.group_pages = e < p.n_groups;
-    u.head = unit / n.tiles;
+    u.head = n.tiles == 1 ? unit : unit / n.tiles;
     u.tokens = n.tokens;
     u.row = n.row;
     u.page0 = n.page0;
@@ -171,18 +175,32 @@ struct Walk {
   }
 };
 
-// ---- the softmax groups ---------------------------------------------------------
-__device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* ring, int w,
+// ---- the softmax warps ------------------------------------------------------------
+// Warp (w, h, quarter): 32 rows of group w's tile, columns 64 h .. 64 h + 63 of S and of O, so that a
+// row's exponentials are shared by two warps, and four warps are on a scheduler to hide one
+// another's latency.  The two tell each other once a stage whether the row's maximum has to move.
+__device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* ring, int w, int h,
                              int share) {
-  const int tid = threadIdx.x & 127, lane = tid & 31;
-  const uint32_t lanes = sh.tmem + (uint32_t(tid >> 5 << 5) << 16);
-  const uint32_t t_s = lanes + w * 128, t_o = lanes + 256 + w * 128;
-  const int rt = tid / p.group, head_in_group = tid % p.group;
-  const int npg_shift = p.page_shift;
+  const int tid = threadIdx.x & 127, lane = tid & 31, quarter = tid >> 5;
+  const uint32_t base = sh.tmem + (uint32_t(quarter * 32) << 16) + w * 128;
+  const uint32_t t_s = base + 64 * h, t_o = t_s + 256;
+  const int rt = tid / p.group, head_in_group = tid - rt * p.group;
   uint32_t jobs = 0, units = 0;                       // of this group
   int stage0 = 0;
+
+  // The partners meet: what the other one says.  A warp that leaves says so at the meeting that the
+  // other is at or comes to next; every way out of here has exactly one such last meeting.
+  constexpr int kLeft = 2;
+  volatile int* mine = sh.flag[w][h][quarter];
+  volatile int* theirs = sh.flag[w][h ^ 1][quarter];
+  auto meet = [&](int say) {
+    if (lane == 0) mine[jobs & 1] = say;
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory");
+    return theirs[jobs & 1];
+  };
+
   for (int n = 0; stage0 < share; ++n) {
-    if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) return;
+    if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) break;
     const Piece u = sh.piece[n % kPieces];
     const int first = u.pair ? 0 : (stage0 ^ w) & 1, step = u.pair ? 1 : 2;
     if (first < u.stages) {
@@ -201,40 +219,55 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
       }
       const bool any = __any_sync(kFull, valid);
       float m = -INFINITY, l = 0.f, lr = 0.f;
+      bool ok = true;
       for (int i = first; i < u.stages; i += step) {
         const int tok = (u.s0 + i) * kStageTok, nv = min(kStageTok, u.tokens - tok);
-        if (!warp_wait_or_dead(&sh.s_full[w], jobs & 1, &sh.dead)) return;
-        ++jobs;
+        ok = warp_wait_or_dead(&sh.s_full[w], jobs & 1, &sh.dead);
+        if (!ok) break;
         tc_fence_after();
         const int bad = *static_cast<volatile int*>(&sh.bad[(stage0 + i) & 7]);
         if (any) {
-          float s[128];
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, s + c);
+          float s[64];
+          tmem_ld32(t_s, s);
+          tmem_ld32(t_s + 32, s + 32);
           tmem_wait_ld();
-          const int seen = lim - tok;
-          if (__any_sync(kFull, seen < 128) || bad) {
+          const int seen = lim - tok - 64 * h;
+          if (__any_sync(kFull, seen < 64)) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= seen || (bad >> (c >> npg_shift) & 1)) s[c] = -INFINITY;
+            for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : -INFINITY;
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          if (bad) {
 #pragma unroll
-          for (int c = 4; c < 128; c += 4) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[c + k]);
+            for (int c = 0; c < 64; ++c)
+              if (bad >> ((64 * h + c) >> p.page_shift) & 1) s[c] = -INFINITY;
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          float x0 = s[0], x1 = s[1];
+#pragma unroll
+          for (int c = 2; c < 62; c += 4) {
+            x0 = fmaxf(fmaxf(x0, s[c]), s[c + 1]);
+            x1 = fmaxf(fmaxf(x1, s[c + 2]), s[c + 3]);
+          }
+          const float top = fmaxf(fmaxf(x0, x1), fmaxf(s[62], s[63])) * p.scale_log2;
           // (rows past the unit's last hold whatever the tile held, and decide nothing)
-          if (__any_sync(kFull, valid && top > m + kLazy)) {
-            const float mn = fmaxf(m, top);
+          const int need = __any_sync(kFull, valid && top > m + kLazy);
+          const int other = meet(need);
+          if (other == kLeft) return;                 // (that was the last meeting)
+          if (need | other) {
+            // both halves' maxima, through a column of S that P leaves free
+            tmem_st1(t_s + 63, top);
+            tmem_wait_st();
+            tc_fence_before();
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory");
+            tc_fence_after();
+            const float theirs_top = tmem_ld1(base + 64 * (h ^ 1) + 63);
+            const float mn = fmaxf(m, fmaxf(top, theirs_top));
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
             m = mn;
             l *= f;
             lr *= f;
             if (i != first) {                         // (the first product overwrites O)
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
+              for (int c = 0; c < 64; c += 16) {
                 float o[16];
                 tmem_ld16(t_o + c, o);
                 tmem_wait_ld();
@@ -248,15 +281,15 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mu, -mu);
           float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
               x.x = ex2_approx(x.x);
               x.y = ex2_approx(x.y);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-              pk[k] = *reinterpret_cast<const uint32_t*>(&h);
+              const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
+              pk[k] = *reinterpret_cast<const uint32_t*>(&r);
               a0 = fadd2(a0, x);
               a1 = fadd2(a1, make_float2(bf16_lo(pk[k]), bf16_hi(pk[k])));
             }
@@ -266,18 +299,17 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           lr += a1.x + a1.y;
           tmem_wait_st();
         }
+        ++jobs;
         if (nv < kStageTok || bad) {
           // rows of V that no query sees (behind the unit's end, or of an invalid page) may hold
           // anything, NaN included, which a weight of 0 would not keep out
-          const int n = 2 * (stage0 + i) + 1, slot = n % kRing;
-          if (!warp_wait_or_dead(&sh.full[slot], (n / kRing) & 1, &sh.dead)) return;
-          if (tid >= nv || (bad >> (tid >> npg_shift) & 1)) {
-            uint4* row = reinterpret_cast<uint4*>(ring + slot * kTileBytes + tid * 128);
+          const int c = 2 * (stage0 + i) + 1, slot = c % kRing;
+          ok = warp_wait_or_dead(&sh.full[slot], (c / kRing) & 1, &sh.dead);
+          if (!ok) break;
+          if (tid >= nv || (bad >> (tid >> p.page_shift) & 1)) {
+            uint4* row = reinterpret_cast<uint4*>(ring + slot * kTileBytes + h * kHalfBytes + tid * 128);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              row[c] = make_uint4(0, 0, 0, 0);
-              row[c + kHalfBytes / 16] = make_uint4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
           }
           proxy_fence_smem();
         }
@@ -285,20 +317,20 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[w]);
       }
-      // this group's half of the piece
-      if (!warp_wait_or_dead(&sh.o_full[w], units & 1, &sh.dead)) return;
+      // this group's part of the piece
+      if (!ok || !warp_wait_or_dead(&sh.o_full[w], units & 1, &sh.dead)) break;
       ++units;
       tc_fence_after();
       if (any) {
-        const int half = u.pair ? 0 : first;              // (of the piece's stages, in turn)
+        const int part = u.pair ? 0 : first;          // (of the piece's stages, in turn)
         const int64_t row = int64_t(qt) * (p.n_kv_heads * p.group) + u.head * p.group + head_in_group;
         // the first piece of a unit by the row, one continued from the block before by the block
-        const int64_t at = u.s0 == 0 ? ((u.group_pages ? 0 : 2) + half) * p.rows + row
-                                     : 4 * p.rows + int64_t(blockIdx.x) * 256 + (u.pair ? w : half) * 128 + tid;
-        float* acc = p.acc + at * kHeadDim;
-        if (valid) p.sums[at] = make_float4(m, l, lr, 0.f);
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        const int64_t at = u.s0 == 0 ? ((u.group_pages ? 0 : 2) + part) * p.rows + row
+                                     : 4 * p.rows + int64_t(blockIdx.x) * 256 + (u.pair ? w : part) * 128 + tid;
+        float* acc = p.acc + at * kHeadDim + 64 * h;
+        if (valid) p.sums[2 * at + h] = make_float4(m, l, lr, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
           float o[32];
           tmem_ld32(t_o + c, o);
           tmem_wait_ld();
@@ -315,6 +347,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
     }
     stage0 += u.stages;
   }
+  meet(kLeft);
 }
 
 // ---- the loading warp -------------------------------------------------------------
@@ -328,6 +361,12 @@ __device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& s
   int qn = 0, stage = 0;
   bool ok = true;
   for (int piece = 0; ok && walk.next(p, u); ++piece) {
+    const int32_t* table = p.block_table + int64_t(u.row) * p.max_pages + u.page0;
+    auto page_of = [&](int s) {                       // lane i has the stage's page i: its block
+      const int page = s * per_stage + lane;
+      return lane < per_stage && page << p.page_shift < u.tokens ? table[page] : INT_MIN;
+    };
+    int next = page_of(u.s0);
     const int box_tokens = u.group_pages ? p.tile_tokens : min(p.n_rows, p.tile_tokens);
     const CUtensorMap* map_q = u.group_pages ? map_qg : map_qo;
     for (int t = 0; ok && t < (u.pair ? 2 : 1); ++t, ++qn) {
@@ -345,21 +384,14 @@ __device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& s
                   &sh.q_full[slot]);
       }
     }
-    const int32_t* table = p.block_table + int64_t(u.row) * p.max_pages + u.page0;
     for (int s = u.s0; ok && s < u.s0 + u.stages; ++s, ++stage) {
-      // lane i has the stage's page i
-      const int page = s * per_stage + lane;
-      bool want = lane < per_stage && page << p.page_shift < u.tokens;
-      int block = 0;
-      if (want) {
-        block = table[page];
-        if (block < 0 || block >= p.num_blocks) {
-          flag_status(p.status, LOCKS_DEV_BAD_BLOCK_ID);
-          block = -1;
-        }
-      }
-      const int bad = __ballot_sync(kFull, want && block < 0);
-      want = want && block >= 0;
+      const int block = next;
+      if (s + 1 < u.s0 + u.stages) next = page_of(s + 1);
+      bool want = block != INT_MIN;
+      const bool there = block >= 0 && block < p.num_blocks;
+      if (want && !there) flag_status(p.status, LOCKS_DEV_BAD_BLOCK_ID);
+      const int bad = __ballot_sync(kFull, want && !there);
+      want = want && there;
       const int n = __popc(__ballot_sync(kFull, want));
       const int z = block * p.n_kv_heads + u.head;
 #pragma unroll
@@ -455,7 +487,7 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
       const uint32_t dv = v_desc + vs * (kTileBytes >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
-        mma_ts(t_o, t_s + 8 * k, dv + k * (2048 >> 4), kIdescO, i != first || k > 0);
+        mma_ts(t_o, t_s + 8 * k + (k >= 4 ? 32 : 0), dv + k * (2048 >> 4), kIdescO, i != first || k > 0);
       mma_commit(&sh.empty[vs]);
       if (last) {
         mma_commit(&sh.o_full[w]);
@@ -475,8 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap map_qo,
                   const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* qtile = smem;
   unsigned char* ring = smem + 2 * kTileBytes;
   Shared& sh = *reinterpret_cast<Shared*>(smem + (kRing + 2) * kTileBytes);
@@ -492,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 2);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
-      mbar_init(&sh.o_empty[i], 4);
+      mbar_init(&sh.o_empty[i], 8);
       mbar_init(&sh.done[i], 1);
     }
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.piece_full[i], 1);
@@ -548,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (share > 0) {
     if (warp < kProducerWarp) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-      softmax_role(p, sh, ring, warp >> 2, share);
+      softmax_role(p, sh, ring, warp >> 3, warp >> 2 & 1, share);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == kProducerWarp) load_role(p, groups, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
@@ -577,15 +608,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
   const int qt = blockIdx.x / p.n_kv_heads, head = blockIdx.x - qt * p.n_kv_heads;
   const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
   const int64_t row0 = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group;
-  griddep_wait();
+  // What the first kernel of the call was given is there before it lets this one start; what it wrote,
+  // after the wait.
+  Entry n = {};
+  int e = 0, g = -1;
   if (warp < 2) {                                     // 0: the group's pages, 1: the sequence's own
     const Groups groups = {p.group_starts, p.prefix_pages};
-    const int total = p.entry_start[p.n_groups + p.batch];
-    const int g = warp == 0 ? groups.of(p, b) : 0, e = warp == 0 ? g : p.n_groups + b;
+    g = warp == 0 ? groups.of(p, b) : 0;
+    e = warp == 0 ? g : p.n_groups + b;
+    if (g >= 0) n = load_entry(p, groups, e);
+  }
+  griddep_wait();
+  if (warp < 2) {
     int pieces = 0;
     if (g >= 0) {
-      const Entry n = load_entry(p, groups, e);
-      const int tq = qt - n.q0, tile = tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
+      const int total = p.entry_start[p.n_groups + p.batch];
+      const int tq = qt - n.q0, tile = n.tiles == 1 ? 0 : tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
       const bool pair = n.nq - tile * 2 * p.tile_tokens > p.tile_tokens;
       const int w = in >= p.tile_tokens, r = (in - w * p.tile_tokens) * p.group;
       const int first = p.entry_start[e] + (head * n.tiles + tile) * n.stages, end = first + n.stages;
@@ -616,7 +654,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
     if (lane == 0) s_n[warp] = 2 * pieces;
   }
   __syncthreads();
-  const int n0 = s_n[0], n = n0 + s_n[1];
+  const int n0 = s_n[0], parts = n0 + s_n[1];
   // warps a row: 8 / G, G rounded up to a power of two
   int each = kJoinWarps;
   while (each > 1 && each * p.group > kJoinWarps) each >>= 1;
@@ -640,15 +678,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
     };
     if (g < p.group) {
       constexpr int kAhead = 4;
-      for (int t0 = sub; t0 < n; t0 += each * kAhead) {
+      for (int t0 = sub; t0 < parts; t0 += each * kAhead) {
         float4 s[kAhead], a[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int t = t0 + k * each;
-          int64_t x = t >= n ? -1 : t < n0 ? s_part[0][t] : s_part[1][t - n0];
+          int64_t x = t >= parts ? -1 : t < n0 ? s_part[0][t] : s_part[1][t - n0];
           s[k].y = 0.f;
           if (x >= 0) {
-            s[k] = p.sums[x + g];
+            // (l and the rounded l of the two halves of the columns, which share m)
+            const float4 z = p.sums[2 * (x + g) + 1];
+            s[k] = p.sums[2 * (x + g)];
+            s[k].y += z.y;
+            s[k].z += z.z;
             a[k] = *reinterpret_cast<const float4*>(p.acc + (x + g) * kHeadDim + 4 * lane);
           }
         }
@@ -685,7 +727,7 @@ PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
   const size_t parts = size_t(4) * rows + size_t(kBatchSms) * 256;
   L.acc = 0;
   L.sums = up(L.acc + parts * kHeadDim * sizeof(float));
-  L.entry_start = up(L.sums + parts * sizeof(float4));
+  L.entry_start = up(L.sums + 2 * parts * sizeof(float4));
   L.total = up(L.entry_start + size_t(entries + 1) * sizeof(int32_t));
   return L;
 }
