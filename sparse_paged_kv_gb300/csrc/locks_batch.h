@@ -26,19 +26,21 @@ struct PrefixParams {
   float* out_lse;                // nullable [batch][n_rows][H_q]
   int32_t* status;               // nullable
   // workspace (see prefix_layout)
-  float* acc;                    // [parts][d]: [2 kinds][2 halves][rows] first pieces, then
+  float4* acc;                   // [32 chunks of 4 dims][parts]: [2 kinds][2 parts][rows] first pieces,
+                                 // rows as [KV head][query token][head of the group], then
                                  // [blocks][256] pieces continued from the block before
   float4* sums;                  // [parts][2 halves of the columns] (m, l, l of the rounded weights, -)
   int32_t* entry_start;          // [n_groups + batch + 1] first stage of each entry; their total
   int batch, n_groups, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift;
   int tile_tokens;               // query tokens of a tile: floor(128 / group)
   uint64_t tile_magic;           // ceil(2^32 / (2 tile_tokens)): n / (2 tile_tokens) = n * magic >> 32 below 2^24
-  int64_t rows;                  // batch * n_rows * n_q_heads
+  int64_t rows, parts;           // batch * n_rows * n_q_heads; 4 rows + 256 blocks
   float scale_log2;
 };
 
 struct PrefixLayout {
   size_t acc, sums, entry_start, total;
+  int64_t parts;
 };
 PrefixLayout prefix_layout(int64_t rows, int64_t entries);
 int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUtensorMap& q_own,

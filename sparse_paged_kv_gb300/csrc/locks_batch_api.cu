@@ -47,12 +47,12 @@ int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
   int rc = check_batch_cfg(c);
   if (rc != LOCKS_OK || (rc = check_rows(c, n_rows)) != LOCKS_OK) return rc;
   if (n_groups < 0 || n_groups > c->batch) return LOCKS_ERR_INVALID_ARG;
-  // stages of the whole list, and rows, are ints: every sequence's own pages and every group's
+  // what the whole list costs (up to 6 a stage, 2 a unit), and rows, are ints: every sequence's own pages and every group's
   // (at most one unit of two tiles more than the sequences fill) over all of the table's pages
   const int64_t stages = (int64_t(c->max_pages) * c->page_size + locks::kStageTok - 1) / locks::kStageTok;
   const int64_t units = int64_t(c->batch) + n_groups +
                         int64_t(c->batch) * n_rows / (2 * tile_tokens(c)) + 1;
-  if (stages * units * c->n_kv_heads >= (int64_t(1) << 31) ||
+  if ((stages * 6 + 2) * units * c->n_kv_heads >= (int64_t(1) << 31) ||
       int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 31) ||
       int64_t(c->batch) * n_rows >= (1 << 24) - 256)
     return LOCKS_ERR_UNSUPPORTED;
@@ -153,7 +153,8 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
   p.out_lse = out_lse;
   p.status = status;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  p.acc = reinterpret_cast<float*>(ws + L.acc);
+  p.acc = reinterpret_cast<float4*>(ws + L.acc);
+  p.parts = L.parts;
   p.sums = reinterpret_cast<float4*>(ws + L.sums);
   p.entry_start = reinterpret_cast<int32_t*>(ws + L.entry_start);
   p.batch = cfg->batch;

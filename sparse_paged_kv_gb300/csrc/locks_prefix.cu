@@ -44,7 +44,9 @@ namespace {
 
 constexpr int kSoftmaxWarps = 16;                     // two groups, two halves of the columns, four quarters of the rows
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
-constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;   // (two issuing warps)
+// (Two issuing warps.  With few rows the softmax works on the first scheduler's warps alone, so none
+// of the others is there.)
+constexpr int kMmaWarp = kSoftmaxWarps + 1, kProducerWarp = kSoftmaxWarps + 3;
 // registers a thread after the split: 512 * 104 + 128 * 64 = 640 * 96, the launch's
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kTileBytes = 128 * 256;                 // 128 rows of 128 bf16
@@ -55,12 +57,15 @@ constexpr int kRing = 5;
 // (n - 5 at the earliest, if every piece has one stage), and the softmax has read that piece's entry.
 constexpr int kPieces = 16;
 constexpr int kGroupsHeld = 64;                       // groups whose bounds a block holds
+// What the list counts: a stage, one that both groups work on, and a unit's beginning and end, in
+// quarters of the first (measured: 1.4 us where memory bounds it, 2.2 us, 0.6 us).
+constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 2;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
 // A unit's stages [s0, s0 + stages) that this block has, as the loading warp hands them to the others.
 struct Piece {
-  int stages;
+  int stages;             // 0: no more pieces
   int pair;               // two tiles: a group each, both on every stage; else stages in turn
   int group_pages;        // the unit is a group's (else a sequence's own pages)
   int head, tokens, row, page0;
@@ -76,6 +81,7 @@ struct Shared {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t done[2];
   uint32_t tmem;
+  int lock;                                           // of the tensor cores, between the groups
   int flag[2][2][4][2];                               // what a softmax warp tells its partner
   int dead;                                           // a wait ran out: every role leaves
   int group_start[kGroupsHeld + 1], group_pages[kGroupsHeld];
@@ -112,12 +118,19 @@ __device__ __forceinline__ int length_of(const PrefixParams& p, int b) {
   return clamp_int(p.seq_lens[b], 0, p.max_pages * p.page_size);
 }
 
-// Entry e < n_groups: the shared pages of group e; else the own pages of sequence e - n_groups.
+// Entry e < n_groups: the shared pages of group e; else the own pages of sequence e - n_groups.  Its
+// units: a KV head, and of a group 2 * tile_tokens query tokens.
 struct Entry {
-  int units, stages;      // units (KV head, and of a group 256 query rows) of so many stages each
-  int tokens, row, page0; // tokens; the block table's row and its first page
-  int q0, nq, tiles;      // first query token (of all), how many, in units of two tiles a head
+  int stages, tokens, row, page0;   // tokens; the block table's row and its first page
+  int q0, nq, tiles;                // first query token (of all), how many, in how many units a head
+  int cost, last_cost;              // of a unit; of a head's last one
+  __device__ __forceinline__ int head_cost() const { return (tiles - 1) * cost + last_cost; }
 };
+// how many of a unit's stages begin before `cost` of it
+__device__ __forceinline__ int stages_before(int cost, bool pair) {
+  const int c = cost - kCostUnit;
+  return c <= 0 ? 0 : pair ? (c + kCostPair - 1) / kCostPair : (c + kCostStage - 1) / kCostStage;
+}
 
 __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) {
   Entry n;
@@ -139,7 +152,12 @@ __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) 
   }
   n.stages = (n.tokens + kStageTok - 1) / kStageTok;
   n.tiles = int(uint64_t(uint32_t(n.nq + 2 * p.tile_tokens - 1)) * p.tile_magic >> 32);
-  n.units = n.tiles * p.n_kv_heads;
+  n.cost = n.last_cost = 0;
+  if (n.stages > 0) {
+    n.cost = n.stages * kCostPair + kCostUnit;
+    const bool pair = n.nq - (n.tiles - 1) * 2 * p.tile_tokens > p.tile_tokens;
+    n.last_cost = n.stages * (pair ? kCostPair : kCostStage) + kCostUnit;
+  }
   return n;
 }
 
@@ -152,26 +170,32 @@ struct Walk {
       : e(sh.place.entry), offset(sh.place.offset), left(share), groups(groups),
         n(load_entry(p, groups, e)) {}
   __device__ bool next(const PrefixParams& p, Piece& u) {
-    if (left <= 0) return false;
-    while (offset >= n.units * n.stages) {
-      offset = 0;
-      if (++e >= p.n_groups + p.batch) return false;
-      n = load_entry(p, groups, e);
+    while (left > 0) {
+      const int head_cost = n.head_cost();
+      if (offset >= head_cost * p.n_kv_heads) {
+        offset = 0;
+        if (++e >= p.n_groups + p.batch) return false;
+        n = load_entry(p, groups, e);
+        continue;
+      }
+      const int head = offset / head_cost, in_head = offset - head * head_cost;
+      const int tile = n.tiles == 1 ? 0 : min(in_head / n.cost, n.tiles - 1);
+      const int at = in_head - tile * n.cost, end = min(at + left, tile == n.tiles - 1 ? n.last_cost : n.cost);
+      offset += end - at;
+      left -= end - at;
+      u.group_pages = e < p.n_groups;
+      u.head = head;
+      u.tokens = n.tokens;
+      u.row = n.row;
+      u.page0 = n.page0;
+      u.q0 = n.q0 + tile * 2 * p.tile_tokens;
+      u.nq = min(n.nq - tile * 2 * p.tile_tokens, 2 * p.tile_tokens);
+      u.pair = u.nq > p.tile_tokens;
+      u.s0 = stages_before(at, u.pair);
+      u.stages = stages_before(end, u.pair) - u.s0;
+      if (u.stages > 0) return true;
     }
-    const int unit = offset / n.stages, tile = n.tiles == 1 ? 0 : unit % n.tiles;
-    u.group_pages = e < p.n_groups;
-    u.head = n.tiles == 1 ? unit : unit / n.tiles;
-    u.tokens = n.tokens;
-    u.row = n.row;
-    u.page0 = n.page0;
-    u.q0 = n.q0 + tile * 2 * p.tile_tokens;
-    u.nq = min(n.nq - tile * 2 * p.tile_tokens, 2 * p.tile_tokens);
-    u.pair = u.nq > p.tile_tokens;
-    u.s0 = offset - unit * n.stages;
-    u.stages = min(n.stages - u.s0, left);
-    offset += u.stages;
-    left -= u.stages;
-    return true;
+    return false;
   }
 };
 
@@ -179,12 +203,11 @@ struct Walk {
 // Warp (w, h, quarter): 32 rows of group w's tile, columns 64 h .. 64 h + 63 of S and of O, so that a
 // row's exponentials are shared by two warps, and four warps are on a scheduler to hide one
 // another's latency.  The two tell each other once a stage whether the row's maximum has to move.
-__device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* ring, int w, int h,
-                             int share) {
+__device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* ring, int w, int h) {
   const int tid = threadIdx.x & 127, lane = tid & 31, quarter = tid >> 5;
   const uint32_t base = sh.tmem + (uint32_t(quarter * 32) << 16) + w * 128;
   const uint32_t t_s = base + 64 * h, t_o = t_s + 256;
-  const int rt = tid / p.group, head_in_group = tid - rt * p.group;
+  const int rt = tid / p.group;
   uint32_t jobs = 0, units = 0;                       // of this group
   int stage0 = 0;
 
@@ -199,9 +222,10 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
     return theirs[jobs & 1];
   };
 
-  for (int n = 0; stage0 < share; ++n) {
+  for (int n = 0;; ++n) {
     if (!warp_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) break;
     const Piece u = sh.piece[n % kPieces];
+    if (u.stages == 0) break;
     const int first = u.pair ? 0 : (stage0 ^ w) & 1, step = u.pair ? 1 : 2;
     if (first < u.stages) {
       const int tq = (u.pair ? w * p.tile_tokens : 0) + rt;
@@ -323,12 +347,13 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
       tc_fence_after();
       if (any) {
         const int part = u.pair ? 0 : first;          // (of the piece's stages, in turn)
-        const int64_t row = int64_t(qt) * (p.n_kv_heads * p.group) + u.head * p.group + head_in_group;
         // the first piece of a unit by the row, one continued from the block before by the block
+        const int64_t row = (int64_t(u.head) * p.batch * p.n_rows + u.q0 + (u.pair ? w * p.tile_tokens : 0)) *
+                                p.group + tid;
         const int64_t at = u.s0 == 0 ? ((u.group_pages ? 0 : 2) + part) * p.rows + row
                                      : 4 * p.rows + int64_t(blockIdx.x) * 256 + (u.pair ? w : part) * 128 + tid;
-        float* acc = p.acc + at * kHeadDim + 64 * h;
         if (valid) p.sums[2 * at + h] = make_float4(m, l, lr, 0.f);
+        float4* acc = p.acc + (16 * h) * p.parts + at;
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {
           float o[32];
@@ -337,7 +362,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           if (valid) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(acc + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              acc[(c + k) / 4 * p.parts] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           }
         }
       }
@@ -358,9 +383,9 @@ __device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& s
   const int per_stage = kStageTok >> p.page_shift;
   Walk walk(p, groups, sh, share);
   Piece u;
-  int qn = 0, stage = 0;
+  int qn = 0, stage = 0, piece = 0;
   bool ok = true;
-  for (int piece = 0; ok && walk.next(p, u); ++piece) {
+  for (; ok && walk.next(p, u); ++piece) {
     const int32_t* table = p.block_table + int64_t(u.row) * p.max_pages + u.page0;
     auto page_of = [&](int s) {                       // lane i has the stage's page i: its block
       const int page = s * per_stage + lane;
@@ -413,6 +438,10 @@ __device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& s
       }
     }
   }
+  if (ok && lane == 0) {
+    sh.piece[piece % kPieces].stages = 0;
+    mbar_arrive(&sh.piece_full[piece % kPieces]);
+  }
   // no block leaves while copies into its memory are in flight: after a wait that ran out, each
   // slot's last copy is waited for once more
   if (!ok) {
@@ -430,7 +459,7 @@ __device__ void load_role(const PrefixParams& p, const Groups& groups, Shared& s
 // whoever waits for a phase has to know that the one before is over: each thread waits for every
 // tile and every piece's queries, also for those that only the other group uses, and each tile is
 // free when both have been there.
-__device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int w, int share) {
+__device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring, int w) {
   constexpr uint32_t kIdescS = mma_idesc(128, 128, false), kIdescO = mma_idesc(128, 128, true);
   const uint32_t t_s = sh.tmem + w * 128, t_o = t_s + 256;
   const uint32_t q_desc = smem_desc_lo(smem_u32(qtile), 16);
@@ -440,15 +469,18 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
   uint32_t jobs = 0, units = 0;                       // of this group
   int stage0 = 0, tile0 = 0;
   bool ok = true;
-  for (int n = 0; ok && stage0 < share; ++n) {
+  for (int n = 0; ok; ++n) {
     if (!mbar_wait_or_dead(&sh.piece_full[n % kPieces], (n / kPieces) & 1, &sh.dead)) break;
     const int stages = sh.piece[n % kPieces].stages, pair = sh.piece[n % kPieces].pair;
+    if (stages == 0) break;
     const int first = pair ? 0 : (stage0 ^ w) & 1, step = 2 - pair;
     const uint32_t t = tile0 + (w & pair), qs = t & 1;
+    const uint32_t da = q_desc + qs * (kTileBytes >> 4);
     if (first >= stages) {
       ok = mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead);
       if (ok) mbar_arrive(&sh.q_empty[qs]);
     }
+    bool scored = false;                              // S of stage i is issued
     for (int i = 0; ok && i < stages; ++i) {
       const uint32_t c = 2 * (stage0 + i), ks = c % kRing, kp = c / kRing & 1;
       const uint32_t vs = (c + 1) % kRing, vp = (c + 1) / kRing & 1;
@@ -461,37 +493,46 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
         mbar_arrive(&sh.empty[vs]);
         continue;
       }
-      const bool last = i + step >= stages;
-      ok = (i != first || mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead)) &&
-           mbar_wait_or_dead(&sh.full[ks], kp, &sh.dead);
-      if (!ok) break;
-      const uint32_t da = q_desc + qs * (kTileBytes >> 4), dk = k_desc + ks * (kTileBytes >> 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {                   // 16 of the 128 dims each, 64 in a half
-        const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-        mma_ss(t_s, da + o, dk + o, kIdescS, k > 0);
-      }
       // (a pair's query tiles are used by one group each, which gives both arrivals)
-      mma_commit(&sh.s_full[w]);
-      mma_commit(&sh.empty[ks]);
-      if (last) {
-        mma_commit(&sh.q_empty[qs]);
-        if (pair) mma_commit(&sh.q_empty[qs]);
+      auto scores = [&](uint32_t slot, bool last) {
+        mma_ss_128(t_s, da, k_desc + slot * (kTileBytes >> 4), kIdescS);
+        mma_commit(&sh.s_full[w]);
+        mma_commit(&sh.empty[slot]);
+        if (last) {
+          mma_commit(&sh.q_empty[qs]);
+          if (pair) mma_commit(&sh.q_empty[qs]);
+        }
+      };
+      const bool last = i + step >= stages;
+      if (!scored) {
+        ok = (i != first || mbar_wait_or_dead(&sh.q_full[qs], t >> 1 & 1, &sh.dead)) &&
+             mbar_wait_or_dead(&sh.full[ks], kp, &sh.dead);
+        if (!ok) break;
+        scores(ks, last);
       }
       ok = mbar_wait_or_dead(&sh.full[vs], vp, &sh.dead) &&
            (i != first || mbar_wait_or_dead(&sh.o_empty[w], (units & 1) ^ 1, &sh.dead)) &&
            mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
       if (!ok) break;
       ++jobs;
+      // With both groups on every stage, P V and the next S go to the tensor cores as one block: two
+      // groups in step would wait for their products together and then crowd the schedulers together
+      // (a stage took 4000 cycles); one block after the other, each group's exponentials meet the other's
+      // products.  The lock is a courtesy: after a while the block goes without it.
+      const uint32_t ns = (c + 2) % kRing;
+      scored = pair && !last && mbar_try_wait(&sh.full[ns], (c + 2) / kRing & 1);
+      if (scored)
+        for (int tries = 0; tries < 64 && atomicCAS_block(&sh.lock, 0, 1); ++tries) {}
       tc_fence_after();
-      const uint32_t dv = v_desc + vs * (kTileBytes >> 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)                     // 16 of the 128 tokens each
-        mma_ts(t_o, t_s + 8 * k + (k >= 4 ? 32 : 0), dv + k * (2048 >> 4), kIdescO, i != first || k > 0);
+      mma_ts_128(t_o, t_s, v_desc + vs * (kTileBytes >> 4), kIdescO, i != first);
       mma_commit(&sh.empty[vs]);
       if (last) {
         mma_commit(&sh.o_full[w]);
         ++units;
+      }
+      if (scored) {
+        scores(ns, i + 2 >= stages);
+        atomicExch_block(&sh.lock, 0);
       }
     }
     stage0 += stages;
@@ -530,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.piece_full[i], 1);
     mbar_fence_init();
-    sh.dead = 0;
+    sh.dead = sh.lock = 0;
     prefetch_map(&map_qg);
     prefetch_map(&map_qo);
     prefetch_map(&map_k);
@@ -555,8 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int total;
   const int share = locate<kThreads>(
       [&](int e) {
-        const Entry n = load_entry(p, groups, e);
-        return n.units * n.stages;
+        return load_entry(p, groups, e).head_cost() * p.n_kv_heads;
       },
       entries, blockIdx.x, kBatchSms, sh.place, total,
       [&](int e, int first) {
@@ -577,13 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch();
 
   if (share > 0) {
-    if (warp < kProducerWarp) {
+    if (warp < kSoftmaxWarps) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-      softmax_role(p, sh, ring, warp >> 3, warp >> 2 & 1, share);
+      softmax_role(p, sh, ring, warp >> 3, warp >> 2 & 1);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == kProducerWarp) load_role(p, groups, sh, qtile, ring, &map_qg, &map_qo, &map_k, &map_v, share);
-      else if (warp < kMmaWarp + 2 && elect_one()) issue_role(sh, qtile, ring, warp - kMmaWarp, share);
+      else if (warp >= kMmaWarp && elect_one()) issue_role(sh, qtile, ring, warp - kMmaWarp);
     }
   }
   tc_fence_before();
@@ -607,7 +647,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int qt = blockIdx.x / p.n_kv_heads, head = blockIdx.x - qt * p.n_kv_heads;
   const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
-  const int64_t row0 = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group;
+  const int64_t row0 = (int64_t(head) * p.batch * p.n_rows + qt) * p.group;            // of the parts
+  const int64_t out0 = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group;
   // What the first kernel of the call was given is there before it lets this one start; what it wrote,
   // after the wait.
   Entry n = {};
@@ -626,27 +667,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
       const int tq = qt - n.q0, tile = n.tiles == 1 ? 0 : tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
       const bool pair = n.nq - tile * 2 * p.tile_tokens > p.tile_tokens;
       const int w = in >= p.tile_tokens, r = (in - w * p.tile_tokens) * p.group;
-      const int first = p.entry_start[e] + (head * n.tiles + tile) * n.stages, end = first + n.stages;
+      const int first = p.entry_start[e] + head * n.head_cost() + tile * n.cost;
+      const int end = first + (tile == n.tiles - 1 ? n.last_cost : n.cost);
       if (n.stages > 0) {
-        // the block of a stage: an estimate, put right
-        auto block_of = [&](int stage) {
-          int c = min(kBatchSms - 1, int(float(stage) * kBatchSms / float(total)));
-          while (share_begin(total, c + 1, kBatchSms) <= stage) ++c;
-          while (share_begin(total, c, kBatchSms) > stage) --c;
+        // the block at a place of the list: an estimate, put right
+        auto block_of = [&](int x) {
+          int c = min(kBatchSms - 1, int(float(x) * kBatchSms / float(total)));
+          while (share_begin(total, c + 1, kBatchSms) <= x) ++c;
+          while (share_begin(total, c, kBatchSms) > x) --c;
           return c;
         };
         const int c0 = block_of(first);
         pieces = block_of(end - 1) - c0 + 1;
         for (int i = lane; i < pieces; i += 32) {
-          const int at = max(first, share_begin(total, c0 + i, kBatchSms));
-          const int to = min(end, share_begin(total, c0 + i + 1, kBatchSms));
+          const int s0 = stages_before(max(first, share_begin(total, c0 + i, kBatchSms)) - first, pair);
+          const int s1 = stages_before(min(end, share_begin(total, c0 + i + 1, kBatchSms)) - first, pair);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            int64_t x = i == 0 ? (2 * warp + half) * p.rows + row0
-                               : 4 * p.rows + int64_t(c0 + i) * 256 + (pair ? w : half) * 128 + r;
-            if (half == 1 && (pair || to - at < 2)) x = -1;
-            if (to <= at) x = -1;
-            s_part[warp][2 * i + half] = x;
+          for (int part = 0; part < 2; ++part) {
+            int64_t x = s0 == 0 ? (2 * warp + part) * p.rows + row0
+                                : 4 * p.rows + int64_t(c0 + i) * 256 + (pair ? w : part) * 128 + r;
+            if (s1 - s0 < (pair ? 1 : part + 1) || (pair && part)) x = -1;
+            s_part[warp][2 * i + part] = x;
           }
         }
       }
@@ -691,7 +732,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
             s[k] = p.sums[2 * (x + g)];
             s[k].y += z.y;
             s[k].z += z.z;
-            a[k] = *reinterpret_cast<const float4*>(p.acc + (x + g) * kHeadDim + 4 * lane);
+            a[k] = p.acc[lane * p.parts + x + g];
           }
         }
 #pragma unroll
@@ -714,8 +755,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParam
     uint2 ow;
     ow.x = *reinterpret_cast<const uint32_t*>(&o01);
     ow.y = *reinterpret_cast<const uint32_t*>(&o23);
-    *reinterpret_cast<uint2*>(p.out + (row0 + g) * kHeadDim + 4 * lane) = ow;
-    if (lane == 0 && p.out_lse) p.out_lse[row0 + g] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+    *reinterpret_cast<uint2*>(p.out + (out0 + g) * kHeadDim + 4 * lane) = ow;
+    if (lane == 0 && p.out_lse) p.out_lse[out0 + g] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
   }
 }
 
@@ -725,6 +766,7 @@ PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
   PrefixLayout L;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t parts = size_t(4) * rows + size_t(kBatchSms) * 256;
+  L.parts = int64_t(parts);
   L.acc = 0;
   L.sums = up(L.acc + parts * kHeadDim * sizeof(float));
   L.entry_start = up(L.sums + 2 * parts * sizeof(float4));

@@ -144,13 +144,40 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
       : "memory");
 }
-// first operand from tensor memory (two bf16 a column)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t add) {
+// The eight instructions of a product of depth 128 in one piece, descriptors stepped in 64 bits:
+// the issuing thread shares its scheduler with busy warps, where every instruction that it needs
+// beside the products costs some 25 cycles.
+// D = A B, A and B in shared memory, both with the summed dimension along the rows' 256 bytes
+__device__ __forceinline__ void mma_ss_128(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %5};\n"
-      " setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.u32 p, 0, 0;\n setp.eq.u32 q, 0, 0;\n"
+      " mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, %5;\n add.s64 b, b, %5;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n add.s64 a, a, 2;\n add.s64 b, b, 2;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "n"(16384 / 16 - 6)
+      : "memory");
+}
+// D (+)= A B, A in tensor memory (two values a column; its second half 64 columns on), B's summed
+// dimension its rows: 16 rows of 128 bytes a step
+__device__ __forceinline__ void mma_ts_128(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                           uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n .reg .b32 x;\n setp.ne.u32 p, %4, 0;\n"
+      " setp.eq.u32 q, 0, 0;\n mov.b64 b, {%2, %5};\n mov.b32 x, %1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 40;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n add.u32 x, x, 8;\n add.s64 b, b, 128;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n}\n" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(idesc), "r"(add), "n"(kDescHi)
       : "memory");
 }
