@@ -61,6 +61,7 @@ constexpr int kGroupsHeld = 64;                       // groups whose bounds a b
 // quarters of the first (measured: 1.4 us where memory bounds it, 2.2 us, 0.6 us).
 constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 2;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
+constexpr int kChunk = 32;                            // columns of S at a time
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
 // A unit's stages [s0, s0 + stages) that this block has, as the loading warp hands them to the others.
@@ -81,6 +82,7 @@ struct Shared {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t done[2];
   uint32_t tmem;
+  float top[2][128];                                  // a row's new maximum, between the halves
   int lock;                                           // of the tensor cores, between the groups
   int flag[2][2][4][2];                               // what a softmax warp tells its partner
   int dead;                                           // a wait ran out: every role leaves
@@ -211,6 +213,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
   uint32_t jobs = 0, units = 0;                       // of this group
   int stage0 = 0;
 
+  auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory"); };
   // The partners meet: what the other one says.  A warp that leaves says so at the meeting that the
   // other is at or comes to next; every way out of here has exactly one such last meeting.
   constexpr int kLeft = 2;
@@ -218,8 +221,24 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
   volatile int* theirs = sh.flag[w][h ^ 1][quarter];
   auto meet = [&](int say) {
     if (lane == 0) mine[jobs & 1] = say;
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory");
+    pair_sync();
     return theirs[jobs & 1];
+  };
+
+  auto load_scores = [&](float* s, int c) {
+    if constexpr (kChunk == 32) tmem_ld32(t_s + c, s);
+    else tmem_ld16(t_s + c, s);
+    tmem_wait_ld();
+  };
+  // columns that the row does not see, or of pages whose block is invalid (col0: of the stage)
+  auto mask_scores = [&](float* s, int seen, int bad, int col0) {
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) s[k] = k < seen ? s[k] : -INFINITY;
+    if (bad) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (bad >> ((col0 + k) >> p.page_shift) & 1) s[k] = -INFINITY;
+    }
   };
 
   for (int n = 0;; ++n) {
@@ -251,40 +270,37 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
         tc_fence_after();
         const int bad = *static_cast<volatile int*>(&sh.bad[(stage0 + i) & 7]);
         if (any) {
-          float s[64];
-          tmem_ld32(t_s, s);
-          tmem_ld32(t_s + 32, s + 32);
-          tmem_wait_ld();
+          // Twice over the columns, kChunk at a time in loops: short enough for the instruction cache,
+          // which the issuing threads share, and S stays in tensor memory meanwhile.
           const int seen = lim - tok - 64 * h;
-          if (__any_sync(kFull, seen < 64)) {
+          const bool masked = __any_sync(kFull, seen < 64) || bad;
+          float s[kChunk], x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += kChunk) {
+            load_scores(s, c);
+            if (masked) mask_scores(s, seen - c, bad, 64 * h + c);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : -INFINITY;
+            for (int k = 0; k < kChunk; k += 4) {
+              x0 = fmaxf(fmaxf(x0, s[k]), s[k + 1]);
+              x1 = fmaxf(fmaxf(x1, s[k + 2]), s[k + 3]);
+            }
           }
-          if (bad) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (bad >> ((64 * h + c) >> p.page_shift) & 1) s[c] = -INFINITY;
-          }
-          float x0 = s[0], x1 = s[1];
-#pragma unroll
-          for (int c = 2; c < 62; c += 4) {
-            x0 = fmaxf(fmaxf(x0, s[c]), s[c + 1]);
-            x1 = fmaxf(fmaxf(x1, s[c + 2]), s[c + 3]);
-          }
-          const float top = fmaxf(fmaxf(x0, x1), fmaxf(s[62], s[63])) * p.scale_log2;
+          const float top = fmaxf(x0, x1) * p.scale_log2;
           // (rows past the unit's last hold whatever the tile held, and decide nothing)
           const int need = __any_sync(kFull, valid && top > m + kLazy);
           const int other = meet(need);
           if (other == kLeft) return;                 // (that was the last meeting)
           if (need | other) {
-            // both halves' maxima, through a column of S that P leaves free
-            tmem_st1(t_s + 63, top);
-            tmem_wait_st();
-            tc_fence_before();
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory");
-            tc_fence_after();
-            const float theirs_top = tmem_ld1(base + 64 * (h ^ 1) + 63);
-            const float mn = fmaxf(m, fmaxf(top, theirs_top));
+            // both halves' maximum, by way of the second one's
+            float mn;
+            if (h == 1) sh.top[w][tid] = top;
+            pair_sync();
+            if (h == 0) {
+              mn = fmaxf(m, fmaxf(top, sh.top[w][tid]));
+              sh.top[w][tid] = mn;
+            }
+            pair_sync();
+            if (h == 1) mn = sh.top[w][tid];
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
             m = mn;
             l *= f;
@@ -304,12 +320,14 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           const float mu = m == -INFINITY ? 0.f : m;
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mu, -mu);
           float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += kChunk) {
+            load_scores(s, c);
+            if (masked) mask_scores(s, seen - c, bad, 64 * h + c);
+            uint32_t pk[kChunk / 2];
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
+            for (int k = 0; k < kChunk / 2; ++k) {
+              float2 x = ffma2(make_float2(s[2 * k], s[2 * k + 1]), sc, off);
               x.x = ex2_approx(x.x);
               x.y = ex2_approx(x.y);
               const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
@@ -317,7 +335,8 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
               a0 = fadd2(a0, x);
               a1 = fadd2(a1, make_float2(bf16_lo(pk[k]), bf16_hi(pk[k])));
             }
-            tmem_st16(t_s + c / 2, pk);
+            if constexpr (kChunk == 32) tmem_st16(t_s + c / 2, pk);
+            else tmem_st8(t_s + c / 2, pk);
           }
           l += a0.x + a0.y;
           lr += a1.x + a1.y;
