@@ -13,16 +13,33 @@ struct ListPlace {
   int scan[32];
 };
 
-__device__ __forceinline__ int share_begin(int total, int block, int blocks) {
-  return int(int64_t(total) * block / blocks);
-}
+// A list of `total` in equal parts for as many blocks as get `least` of it each, up to `most`: block b
+// begins at floor(total * b / blocks), in 32 bits.
+struct Split {
+  int total, blocks, each, rest;
+  float inv;
+  __device__ __forceinline__ Split(int total, int least, int most)
+      : total(total), blocks(min(max(total / least, 1), most)), each(total / blocks),
+        rest(total - each * blocks), inv(1.f / float(blocks)) {}
+  // (b * rest < 2^15, at least half a 152nd away from the next integer)
+  __device__ __forceinline__ int begin(int b) const {
+    return b >= blocks ? total : b * each + int((float(b * rest) + 0.5f) * inv);
+  }
+  // the block at a place of the list: an estimate, put right
+  __device__ __forceinline__ int block_of(int x) const {
+    int b = min(blocks - 1, int(float(x) * float(blocks) / float(total)));
+    while (begin(b + 1) <= x) ++b;
+    while (begin(b) > x) --b;
+    return b;
+  }
+};
 
-// Every thread of the block calls it; returns the block's stages and fills place.  stages(e) is asked for
+// Every thread of the block calls it; returns the block's share and fills place.  stages(e) is asked for
 // every entry: a thread has ceil(entries / THREADS) neighbouring ones.  `visit(e, first)` is called
 // for each entry by the thread that has it.  Ends with a __syncthreads().
 template <int THREADS, typename Stages, typename Visit>
-__device__ int locate(Stages stages, int entries, int block, int blocks, ListPlace& place, int& total,
-                      Visit visit) {
+__device__ int locate(Stages stages, int entries, int block, int least, int most, ListPlace& place,
+                      int& total, Visit visit) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (entries + THREADS - 1) / THREADS;
   const int e_lo = min(entries, tid * each), e_hi = min(entries, e_lo + each);
@@ -42,8 +59,8 @@ __device__ int locate(Stages stages, int entries, int block, int blocks, ListPla
     if (i < warp) before += place.scan[i];
     total += place.scan[i];
   }
-  const int lo = share_begin(total, block, blocks);
-  const int share = share_begin(total, block + 1, blocks) - lo;
+  const Split split(total, least, most);
+  const int lo = split.begin(block), share = split.begin(block + 1) - lo;
   int at = before;
   for (int e = e_lo; e < e_hi; ++e) {
     const int n = each == 1 ? sum : stages(e);
@@ -59,9 +76,9 @@ __device__ int locate(Stages stages, int entries, int block, int blocks, ListPla
 }
 
 template <int THREADS, typename Stages>
-__device__ int locate(Stages stages, int entries, int block, int blocks, ListPlace& place) {
+__device__ int locate(Stages stages, int entries, int block, int least, int most, ListPlace& place) {
   int total;
-  return locate<THREADS>(stages, entries, block, blocks, place, total, [](int, int) {});
+  return locate<THREADS>(stages, entries, block, least, most, place, total, [](int, int) {});
 }
 
 }  // namespace locks

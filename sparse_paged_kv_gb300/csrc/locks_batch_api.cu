@@ -53,7 +53,7 @@ int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
   const int64_t units = int64_t(c->batch) + n_groups +
                         int64_t(c->batch) * n_rows / (2 * tile_tokens(c)) + 1;
   if ((stages * 6 + 2) * units * c->n_kv_heads >= (int64_t(1) << 31) ||
-      int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 31) ||
+      int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 28) ||
       int64_t(c->batch) * n_rows >= (1 << 24) - 256)
     return LOCKS_ERR_UNSUPPORTED;
   return LOCKS_OK;
@@ -156,7 +156,7 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
   p.acc = reinterpret_cast<float4*>(ws + L.acc);
   p.parts = L.parts;
   p.sums = reinterpret_cast<float4*>(ws + L.sums);
-  p.entry_start = reinterpret_cast<int32_t*>(ws + L.entry_start);
+  p.entry_info = reinterpret_cast<int4*>(ws + L.entry_info);
   p.batch = cfg->batch;
   p.n_groups = n_groups;
   p.n_rows = n_rows;

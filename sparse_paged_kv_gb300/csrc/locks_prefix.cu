@@ -617,21 +617,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       [&](int e) {
         return load_entry(p, groups, e).head_cost() * p.n_kv_heads;
       },
-      entries, blockIdx.x, kBatchSms, sh.place, total,
+      entries, blockIdx.x, kCostStage, kBatchSms, sh.place, total,
       [&](int e, int first) {
         if (blockIdx.x) return;
         // for the kernel that joins the pieces; and the arguments' check
-        p.entry_start[e] = first;
+        const Entry n = load_entry(p, groups, e);
         if (e >= p.n_groups) {
           const int t = p.seq_lens[e - p.n_groups];
+          p.entry_info[e] = make_int4(first, n.stages, groups.of(p, e - p.n_groups), 0);
           if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
         } else {
+          p.entry_info[e] = make_int4(first, n.stages, n.q0, n.nq);
           const int a = groups.start[e], z = groups.start[e + 1], n_pages = groups.pages[e];
           if (a < 0 || z < a || z > p.batch || n_pages < 0 || n_pages > p.max_pages)
             flag_status(p.status, LOCKS_DEV_BAD_GROUP);
         }
       });
-  if (blockIdx.x == 0 && tid == 0) p.entry_start[entries] = total;
+  if (blockIdx.x == 0 && tid == 0) p.entry_info[entries] = make_int4(total, 0, 0, 0);
   tc_fence_after();
   griddep_launch();
 
@@ -653,130 +655,174 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- joining the pieces ---------------------------------------------------------------
-// A block of 8 warps has one (query token, KV head).  Where the parts of its rows lie (a piece of the
-// group's pages or of the sequence's own, for either softmax group) is found once, lane = piece.  With
-// fewer rows than warps several warps share a row's parts and are joined in shared memory.
-constexpr int kJoinWarps = 8;
+// A block has RB rows (of [KV head][query token][head of the group], as the parts lie).  First a thread
+// per row and kind (the group's pages, the sequence's own) finds the unit's place in the list, from which
+// it follows where the row's parts are (a piece, for either softmax group): all threads write that down,
+// kListed pieces a unit at a time.  Then thread = (row, chunks of 4 dims): neighbouring threads have
+// neighbouring rows, whose parts lie side by side.  With fewer than 8 rows the threads left over split
+// the parts, and are joined in shared memory.
+constexpr int kJoinThreads = 256, kListed = 32;
 
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefixParams p) {
-  __shared__ int s_n[2];
-  __shared__ int64_t s_part[2][2 * kBatchSms];        // index of the first row's part, or -1
-  __shared__ __align__(16) float s_acc[kJoinWarps][kHeadDim];
-  __shared__ float4 s_sum[kJoinWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int qt = blockIdx.x / p.n_kv_heads, head = blockIdx.x - qt * p.n_kv_heads;
-  const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
-  const int64_t row0 = (int64_t(head) * p.batch * p.n_rows + qt) * p.group;            // of the parts
-  const int64_t out0 = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group;
-  // What the first kernel of the call was given is there before it lets this one start; what it wrote,
-  // after the wait.
-  Entry n = {};
-  int e = 0, g = -1;
-  if (warp < 2) {                                     // 0: the group's pages, 1: the sequence's own
-    const Groups groups = {p.group_starts, p.prefix_pages};
-    g = warp == 0 ? groups.of(p, b) : 0;
-    e = warp == 0 ? g : p.n_groups + b;
-    if (g >= 0) n = load_entry(p, groups, e);
+struct UnitParts {
+  int first, end, c0, pieces;                         // its place in the list; blocks from c0 on
+  int pair;
+  int64_t base, carry;                                // the row's index in a first part; in block 0's
+
+  // how many parts a piece may have, and where the row is in part `which` of piece i (-1: it has none)
+  __device__ __forceinline__ int each() const { return pair ? 1 : 2; }
+  __device__ __forceinline__ int64_t part(int i, int which, const Split& split, int64_t rows) const {
+    const int c = c0 + i;
+    const int s0 = stages_before(max(first, split.begin(c)) - first, pair);
+    const int s1 = stages_before(min(end, split.begin(c + 1)) - first, pair);
+    if (s1 - s0 <= which) return -1;
+    return s0 == 0 ? base + which * rows : carry + int64_t(c) * 256 + which * 128;
   }
+};
+
+template <int RB>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PrefixParams p) {
+  constexpr int kChunkThreads = RB >= 8 ? kJoinThreads / RB : 32, kChunks = 32 / kChunkThreads;
+  constexpr int kSplits = kJoinThreads / (RB * kChunkThreads);
+  __shared__ UnitParts s_unit[2 * RB];
+  __shared__ int s_part[2 * RB][2 * kListed];         // (parts are fewer than 2^31)
+  __shared__ int s_most;                              // pieces of the block's unit that has most
+  const int tid = threadIdx.x;
+  const int64_t row0 = int64_t(blockIdx.x) * RB;
+  const int qts = p.batch * p.n_rows;
+  if (tid == 0) s_most = 0;
+  __syncthreads();
   griddep_wait();
-  if (warp < 2) {
-    int pieces = 0;
-    if (g >= 0) {
-      const int total = p.entry_start[p.n_groups + p.batch];
-      const int tq = qt - n.q0, tile = n.tiles == 1 ? 0 : tq / (2 * p.tile_tokens), in = tq - tile * 2 * p.tile_tokens;
-      const bool pair = n.nq - tile * 2 * p.tile_tokens > p.tile_tokens;
-      const int w = in >= p.tile_tokens, r = (in - w * p.tile_tokens) * p.group;
-      const int first = p.entry_start[e] + head * n.head_cost() + tile * n.cost;
-      const int end = first + (tile == n.tiles - 1 ? n.last_cost : n.cost);
-      if (n.stages > 0) {
-        // the block at a place of the list: an estimate, put right
-        auto block_of = [&](int x) {
-          int c = min(kBatchSms - 1, int(float(x) * kBatchSms / float(total)));
-          while (share_begin(total, c + 1, kBatchSms) <= x) ++c;
-          while (share_begin(total, c, kBatchSms) > x) --c;
-          return c;
-        };
-        const int c0 = block_of(first);
-        pieces = block_of(end - 1) - c0 + 1;
-        for (int i = lane; i < pieces; i += 32) {
-          const int s0 = stages_before(max(first, share_begin(total, c0 + i, kBatchSms)) - first, pair);
-          const int s1 = stages_before(min(end, share_begin(total, c0 + i + 1, kBatchSms)) - first, pair);
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            int64_t x = s0 == 0 ? (2 * warp + part) * p.rows + row0
-                                : 4 * p.rows + int64_t(c0 + i) * 256 + (pair ? w : part) * 128 + r;
-            if (s1 - s0 < (pair ? 1 : part + 1) || (pair && part)) x = -1;
-            s_part[warp][2 * i + part] = x;
-          }
-        }
+  const Split split(p.entry_info[p.n_groups + p.batch].x, kCostStage, kBatchSms);
+  if (tid < 2 * RB) {
+    const int64_t row = row0 + (tid >> 1);
+    const int kind = tid & 1;
+    UnitParts u = {};
+    if (row < p.rows) {
+      const int item = int(row) / p.group, head = item / qts, qt = item - head * qts;   // (rows < 2^31)
+      const int b = p.n_rows == 1 ? qt : qt / p.n_rows;
+      // (place in the list, stages, then of a group: first query token and how many; of a sequence: its group)
+      int4 info = p.entry_info[p.n_groups + b];
+      int q0 = b * p.n_rows, nq = p.n_rows;
+      if (kind == 0) {
+        if (info.z >= 0) info = p.entry_info[info.z];
+        else info.y = 0;
+        q0 = info.z;
+        nq = info.w;
+      }
+      if (info.y > 0) {
+        const int step = 2 * p.tile_tokens;
+        const int tiles = int(uint64_t(uint32_t(nq + step - 1)) * p.tile_magic >> 32);
+        const int tq = qt - q0, tile = int(uint64_t(uint32_t(tq)) * p.tile_magic >> 32);
+        const int in = tq - tile * step, w = in >= p.tile_tokens;
+        const bool last_pair = nq - (tiles - 1) * step > p.tile_tokens;
+        const int cost = info.y * kCostPair + kCostUnit;
+        const int last_cost = info.y * (last_pair ? kCostPair : kCostStage) + kCostUnit;
+        u.pair = nq - tile * step > p.tile_tokens;
+        u.first = info.x + head * ((tiles - 1) * cost + last_cost) + tile * cost;
+        u.end = u.first + (tile == tiles - 1 ? last_cost : cost);
+        u.c0 = split.block_of(u.first);
+        u.pieces = split.block_of(u.end - 1) - u.c0 + 1;
+        u.base = 2 * kind * p.rows + row;
+        u.carry = 4 * p.rows + (u.pair ? w * 128 : 0) + (in - w * p.tile_tokens) * p.group + int(row) - item * p.group;
       }
     }
-    if (lane == 0) s_n[warp] = 2 * pieces;
+    s_unit[tid] = u;
+    if (u.pieces) atomicMax(&s_most, u.pieces);
   }
   __syncthreads();
-  const int n0 = s_n[0], parts = n0 + s_n[1];
-  // warps a row: 8 / G, G rounded up to a power of two
-  int each = kJoinWarps;
-  while (each > 1 && each * p.group > kJoinWarps) each >>= 1;
-  const int sub = warp & (each - 1);
-  for (int g0 = 0; g0 < p.group; g0 += kJoinWarps / each) {
-    const int g = g0 + warp / each;
-    float M = -INFINITY, L = 0.f, LR = 0.f;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float4 s, float4 a) {
-      // (a part in which the row sees nothing has no sum, and an accumulator of no account)
-      if (s.y == 0.f) return;
-      const float mn = fmaxf(M, s.x);
-      const float f = M == -INFINITY ? 0.f : exp2f(M - mn), h = exp2f(s.x - mn);
-      A.x = A.x * f + a.x * h;
-      A.y = A.y * f + a.y * h;
-      A.z = A.z * f + a.z * h;
-      A.w = A.w * f + a.w * h;
-      L = L * f + s.y * h;
-      LR = LR * f + s.z * h;
-      M = mn;
-    };
-    if (g < p.group) {
-      constexpr int kAhead = 4;
-      for (int t0 = sub; t0 < parts; t0 += each * kAhead) {
-        float4 s[kAhead], a[kAhead];
+
+  const int r = tid % RB, chunk0 = tid / RB % kChunkThreads * kChunks, sub = tid / (RB * kChunkThreads);
+  const int64_t row = row0 + r;
+  float M = -INFINITY, L = 0.f, LR = 0.f;
+  float4 A[kChunks];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int t = t0 + k * each;
-          int64_t x = t >= parts ? -1 : t < n0 ? s_part[0][t] : s_part[1][t - n0];
-          s[k].y = 0.f;
-          if (x >= 0) {
-            // (l and the rounded l of the two halves of the columns, which share m)
-            const float4 z = p.sums[2 * (x + g) + 1];
-            s[k] = p.sums[2 * (x + g)];
-            s[k].y += z.y;
-            s[k].z += z.z;
-            a[k] = p.acc[lane * p.parts + x + g];
-          }
+  for (int c = 0; c < kChunks; ++c) A[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float4 s, const float4* a) {
+    // (a part in which the row sees nothing has no sum, and an accumulator of no account)
+    if (s.y == 0.f) return;
+    const float mn = fmaxf(M, s.x);
+    const float f = M == -INFINITY ? 0.f : ex2_approx(M - mn), h = ex2_approx(s.x - mn);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      A[c].x = A[c].x * f + a[c].x * h;
+      A[c].y = A[c].y * f + a[c].y * h;
+      A[c].z = A[c].z * f + a[c].z * h;
+      A[c].w = A[c].w * f + a[c].w * h;
+    }
+    L = L * f + s.y * h;
+    LR = LR * f + s.z * h;
+    M = mn;
+  };
+  const int most = s_most, each0 = s_unit[2 * r].each(), each1 = s_unit[2 * r + 1].each();
+  for (int i0 = 0; i0 < most; i0 += kListed) {
+    if (i0) __syncthreads();
+    const int round = min(kListed, most - i0);
+    for (int j = tid; j < 2 * RB * round; j += kJoinThreads) {
+      const int unit = j % (2 * RB), i = j / (2 * RB);
+      const UnitParts& u = s_unit[unit];
+      for (int which = 0; which < u.each(); ++which)
+        s_part[unit][i * u.each() + which] =
+            i0 + i < u.pieces ? int(u.part(i0 + i, which, split, p.rows)) : -1;
+    }
+    __syncthreads();
+    const int n0 = each0 * round, n = n0 + each1 * round;
+    constexpr int kAhead = kChunks > 1 ? 2 : 4;
+    for (int t0 = sub; t0 < n; t0 += kSplits * kAhead) {
+      float4 s[kAhead], z[kAhead], a[kAhead][kChunks];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = t0 + k * kSplits;
+        s[k].y = z[k].y = 0.f;
+        const int at = t >= n ? -1 : t < n0 ? s_part[2 * r][t] : s_part[2 * r + 1][t - n0];
+        if (at >= 0) {
+          s[k] = p.sums[2 * int64_t(at)];             // (l and the rounded l of the two halves of the
+          z[k] = p.sums[2 * int64_t(at) + 1];         // columns, which share m)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) a[k][c] = p.acc[(chunk0 + c) * p.parts + at];
         }
+      }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) add(s[k], a[k]);
+      for (int k = 0; k < kAhead; ++k) {
+        s[k].y += z[k].y;
+        s[k].z += z[k].z;
+        add(s[k], a[k]);
       }
     }
-    if (each > 1) {
-      __syncthreads();
-      *reinterpret_cast<float4*>(&s_acc[warp][4 * lane]) = A;
-      if (lane == 0) s_sum[warp] = make_float4(M, L, LR, 0.f);
-      __syncthreads();
-      if (sub == 0)
-        for (int k = 1; k < each; ++k)
-          add(s_sum[warp + k], *reinterpret_cast<const float4*>(&s_acc[warp + k][4 * lane]));
-    }
-    if (sub != 0 || g >= p.group) continue;
-    const float inv = LR == 0.f ? 0.f : 1.f / LR;
-    const __nv_bfloat162 o01 = __floats2bfloat162_rn(A.x * inv, A.y * inv);
-    const __nv_bfloat162 o23 = __floats2bfloat162_rn(A.z * inv, A.w * inv);
-    uint2 ow;
-    ow.x = *reinterpret_cast<const uint32_t*>(&o01);
-    ow.y = *reinterpret_cast<const uint32_t*>(&o23);
-    *reinterpret_cast<uint2*>(p.out + (out0 + g) * kHeadDim + 4 * lane) = ow;
-    if (lane == 0 && p.out_lse) p.out_lse[out0 + g] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
   }
+  if constexpr (kSplits > 1) {
+    __shared__ float4 s_acc[kJoinThreads], s_sum[kJoinThreads];
+    s_acc[tid] = A[0];
+    s_sum[tid] = make_float4(M, L, LR, 0.f);
+    __syncthreads();
+    if (sub == 0)
+      for (int k = 1; k < kSplits; ++k) add(s_sum[tid + k * RB * kChunkThreads], &s_acc[tid + k * RB * kChunkThreads]);
+  }
+  if (sub != 0 || row >= p.rows) return;
+  const int g = int(row) % p.group, item = int(row) / p.group, head = item / qts, qt = item - head * qts;
+  const int64_t out = int64_t(qt) * (p.n_kv_heads * p.group) + head * p.group + g;
+  const float inv = LR == 0.f ? 0.f : 1.f / LR;
+  uint2 ow[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const __nv_bfloat162 o01 = __floats2bfloat162_rn(A[c].x * inv, A[c].y * inv);
+    const __nv_bfloat162 o23 = __floats2bfloat162_rn(A[c].z * inv, A[c].w * inv);
+    ow[c].x = *reinterpret_cast<const uint32_t*>(&o01);
+    ow[c].y = *reinterpret_cast<const uint32_t*>(&o23);
+  }
+  __nv_bfloat16* o = p.out + out * kHeadDim + 4 * chunk0;
+  if constexpr (kChunks >= 2) {
+#pragma unroll
+    for (int c = 0; c < kChunks; c += 2)
+      *reinterpret_cast<uint4*>(o + 4 * c) = make_uint4(ow[c].x, ow[c].y, ow[c + 1].x, ow[c + 1].y);
+  } else {
+    *reinterpret_cast<uint2*>(o) = ow[0];
+  }
+  if (chunk0 == 0 && p.out_lse) p.out_lse[out] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+}
+
+template <int RB>
+int launch_join(const PrefixParams& p, cudaStream_t stream) {
+  return launch_dependent(join_kernel<RB>, dim3(unsigned((p.rows + RB - 1) / RB)), kJoinThreads, 0, p, stream);
 }
 
 }  // namespace
@@ -788,8 +834,8 @@ PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
   L.parts = int64_t(parts);
   L.acc = 0;
   L.sums = up(L.acc + parts * kHeadDim * sizeof(float));
-  L.entry_start = up(L.sums + 2 * parts * sizeof(float4));
-  L.total = up(L.entry_start + size_t(entries + 1) * sizeof(int32_t));
+  L.entry_info = up(L.sums + 2 * parts * sizeof(float4));
+  L.total = up(L.entry_info + size_t(entries + 1) * sizeof(int4));
   return L;
 }
 
@@ -813,7 +859,11 @@ int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUten
   lc.numAttrs = 1;
   if (cudaLaunchKernelEx(&lc, prefix_kernel, p, q_group, q_own, k, v) != cudaSuccess)
     return LOCKS_ERR_CUDA;
-  return launch_dependent(join_kernel, dim3(unsigned(p.batch) * p.n_rows * p.n_kv_heads), kJoinWarps * 32, 0, p, stream);
+  // Rows a block: 32 (parts are read 512 bytes at a time) or 8 where that leaves two blocks or one an SM;
+  // a few rows of a long sequence have up to 600 parts each, which four threads split.
+  if (p.rows >= 32 * 2 * kBatchSms) return launch_join<32>(p, stream);
+  if (p.rows >= 8 * kBatchSms) return launch_join<8>(p, stream);
+  return launch_join<2>(p, stream);
 }
 
 }  // namespace locks

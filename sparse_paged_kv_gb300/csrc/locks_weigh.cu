@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   tc_fence_before();
   const int share = locate<kThreads>(
-      [&](int b) { return stages_of(p, b) * p.n_kv_heads; }, p.batch, blockIdx.x, kBatchSms, sh.place);
+      [&](int b) { return stages_of(p, b) * p.n_kv_heads; }, p.batch, blockIdx.x, 1, kBatchSms, sh.place);
   tc_fence_after();
   if (blockIdx.x == 0)
     for (int b = tid; b < p.batch; b += kThreads)
