@@ -59,7 +59,7 @@ constexpr int kPieces = 16;
 constexpr int kGroupsHeld = 64;                       // groups whose bounds a block holds
 // What the list counts: a stage, one that both groups work on, and a unit's beginning and end, in
 // quarters of the first (measured: 1.4 us where memory bounds it, 2.2 us, 0.6 us).
-constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 2;
+constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 3;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
 constexpr int kChunk = 32;                            // columns of S at a time
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
@@ -530,16 +530,17 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
         scores(ks, last);
       }
       ok = mbar_wait_or_dead(&sh.full[vs], vp, &sh.dead) &&
-           (i != first || mbar_wait_or_dead(&sh.o_empty[w], (units & 1) ^ 1, &sh.dead)) &&
-           mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
+           (i != first || mbar_wait_or_dead(&sh.o_empty[w], (units & 1) ^ 1, &sh.dead));
+      if (!ok) break;
+      const uint32_t ns = (c + 2) % kRing;
+      scored = pair && !last && mbar_try_wait(&sh.full[ns], (c + 2) / kRing & 1);
+      ok = mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
       if (!ok) break;
       ++jobs;
       // With both groups on every stage, P V and the next S go to the tensor cores as one block: two
       // groups in step would wait for their products together and then crowd the schedulers together
       // (a stage took 4000 cycles); one block after the other, each group's exponentials meet the other's
       // products.  The lock is a courtesy: after a while the block goes without it.
-      const uint32_t ns = (c + 2) % kRing;
-      scored = pair && !last && mbar_try_wait(&sh.full[ns], (c + 2) / kRing & 1);
       if (scored)
         for (int tries = 0; tries < 64 && atomicCAS_block(&sh.lock, 0, 1); ++tries) {}
       tc_fence_after();
@@ -859,10 +860,11 @@ int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUten
   lc.numAttrs = 1;
   if (cudaLaunchKernelEx(&lc, prefix_kernel, p, q_group, q_own, k, v) != cudaSuccess)
     return LOCKS_ERR_CUDA;
-  // Rows a block: 32 (parts are read 512 bytes at a time) or 8 where that leaves two blocks or one an SM;
+  // Rows a block: 32 (parts are read 512 bytes at a time) where that leaves two blocks an SM, or 4 (2048
+  // rows of 16 parts: 11 us, with 8 rows 17 us, with 2 15 us);
   // a few rows of a long sequence have up to 600 parts each, which four threads split.
   if (p.rows >= 32 * 2 * kBatchSms) return launch_join<32>(p, stream);
-  if (p.rows >= 8 * kBatchSms) return launch_join<8>(p, stream);
+  if (p.rows >= 8 * kBatchSms) return launch_join<4>(p, stream);
   return launch_join<2>(p, stream);
 }
 
