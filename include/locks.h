@@ -636,9 +636,10 @@ size_t locks_evict_workspace_bytes(const locks_cfg_t* cfg, int32_t budget);
  *   seq_lens      int32 [batch]; written
  *   fixed         nullable int32 [batch], >= 0 (NULL: 0): slots that are kept
  *                 where they are (a shared prefix, the first tokens)
- *   weights, positions  pools as for locks_weigh; written
+ *   weights, positions  pools as for locks_weigh, 16-byte aligned; written
  *   evicted       int32 [batch]; written
- *   workspace     >= locks_evict_workspace_bytes bytes, 16-byte aligned
+ *   workspace     >= locks_evict_workspace_bytes bytes, 16-byte aligned,
+ *                 zero-filled before its first use
  * A slot of a block id outside the pool weighs less than any other; moves from
  * or to one are left out (LOCKS_DEV_BAD_BLOCK_ID).
  */

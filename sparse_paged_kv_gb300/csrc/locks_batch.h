@@ -72,7 +72,7 @@ struct EvictParams {
   int32_t* positions;            // [num_blocks][H_kv][B]
   int32_t* evicted;              // [batch], raised
   int32_t* tickets;              // [batch] zeros, left as zeros
-  int32_t* lists;                // [batch * H_kv][2][list_len]
+  int64_t* lists;                // [batch * H_kv][2][list_len] pool rows
   int32_t* status;               // nullable
   int batch, n_kv_heads, max_pages, num_blocks, page_size, page_shift, budget, recent, list_len;
   int keys;                      // set by the launch: keys a block holds

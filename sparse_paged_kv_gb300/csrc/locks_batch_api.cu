@@ -217,7 +217,7 @@ int locks_weigh(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const flo
 
 size_t locks_evict_workspace_bytes(const locks_cfg_t* cfg, int32_t budget) {
   if (check_evict(cfg, budget) != LOCKS_OK) return 0;
-  return evict_list_offset(cfg) + size_t(cfg->batch) * cfg->n_kv_heads * 2 * evict_list(cfg, budget) * 4;
+  return evict_list_offset(cfg) + size_t(cfg->batch) * cfg->n_kv_heads * 2 * evict_list(cfg, budget) * 8;
 }
 
 int locks_evict(const locks_cfg_t* cfg, int32_t budget, int32_t recent, void* k_cache, void* v_cache,
@@ -230,7 +230,9 @@ int locks_evict(const locks_cfg_t* cfg, int32_t budget, int32_t recent, void* k_
   if (cfg->batch == 0) return LOCKS_OK;
   if (!k_cache || !v_cache || !block_table || !seq_lens || !weights || !positions || !evicted || !workspace)
     return LOCKS_ERR_INVALID_ARG;
-  if (misaligned(k_cache) || misaligned(v_cache) || misaligned(workspace)) return LOCKS_ERR_INVALID_ARG;
+  if (misaligned(k_cache) || misaligned(v_cache) || misaligned(weights) || misaligned(positions) ||
+      misaligned(workspace))
+    return LOCKS_ERR_INVALID_ARG;                     // rows, and four slots' records, move as 16-byte words
   if (workspace_bytes < locks_evict_workspace_bytes(cfg, budget)) return LOCKS_ERR_WORKSPACE;
   locks::EvictParams p = {};
   p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
@@ -242,7 +244,7 @@ int locks_evict(const locks_cfg_t* cfg, int32_t budget, int32_t recent, void* k_
   p.positions = positions;
   p.evicted = evicted;
   p.tickets = static_cast<int32_t*>(workspace);
-  p.lists = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + evict_list_offset(cfg));
+  p.lists = reinterpret_cast<int64_t*>(static_cast<unsigned char*>(workspace) + evict_list_offset(cfg));
   p.status = status;
   p.batch = cfg->batch;
   p.n_kv_heads = cfg->n_kv_heads;
