@@ -256,9 +256,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     for (int c0 = lo; c0 < hi; c0 += p.keys) {
       const int c1 = min(hi, c0 + p.keys);
       load(c0, c1);
-      for (int i = c0 + tid; i < c1; i += kThreads) {
-        const uint32_t k = key(i);
-        if (pass == 0 || k >> top == T >> top) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      const int from = shifted, to = c1 - c0 + shifted;        // of the keys held
+      for (int i = 4 * tid; i < to; i += 4 * kThreads) {
+        const uint4 four = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t k4[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j >= from && i + j < to && (pass == 0 || k4[j] >> top == T >> top))
+            atomicAdd(&sh.hist[(k4[j] >> shift) & ((1u << bits) - 1)], 1);
       }
     }
     meet();
@@ -458,9 +463,9 @@ int evict_list_len(int budget, int64_t slots) { return int(budget < slots / 2 ? 
 int launch_evict(EvictParams p, cudaStream_t stream) {
   const int units = p.batch * p.n_kv_heads;
   const int64_t slots = int64_t(p.max_pages) * p.page_size;
-  // Blocks a head: as many as fill the SMs, while each still has some thousand slots.
+  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.
   int C = 1;
-  while (C < 16 && units * C * 2 <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
+  while (C < 16 && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
   const int64_t share = (slots + C - 1) / C;
   p.keys = int(share < kMaxKeys ? (share + 31) / 32 * 32 : kMaxKeys);
   static LaunchOnce once;
