@@ -86,6 +86,15 @@ class LocksConfig:
                            self.page_size, self.rank, self.max_pages, self.num_blocks,
                            self.summary_dtype)
 
+    @functools.cached_property
+    def ref(self):
+        """Reference to the C structure, made once (a decode step passes it at every call)."""
+        return ctypes.byref(self.c())
+
+    def __reduce__(self):
+        # made anew from its fields: a reference to a C structure can't be copied or sent
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
+
     @property
     def group(self) -> int:
         return self.n_q_heads // self.n_kv_heads
@@ -519,7 +528,7 @@ def locks_kv_decode(cfg: LocksKvConfig, q, k_pool, v_pool, block_table, seq_lens
 # a batch that shares prefixes and lives within a budget (C names)
 # --------------------------------------------------------------------------
 def prefix_workspace_bytes(cfg: LocksConfig, n_groups: int, n_rows: int = 1) -> int:
-    return int(load_library().locks_prefix_workspace_bytes(ctypes.byref(cfg.c()), n_groups, n_rows))
+    return int(load_library().locks_prefix_workspace_bytes(cfg.ref, n_groups, n_rows))
 
 
 def _here(x, what: str):
@@ -562,7 +571,7 @@ def locks_prefix_decode(cfg: LocksConfig, q, k_cache, v_cache, block_table, seq_
     wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
     row = (cfg.head_dim,)
     rc = load_library().locks_prefix_decode(
-        ctypes.byref(cfg.c()), _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
+        cfg.ref, _sized(q, "bfloat16", shape, "q"), rows,
         _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", row),
         _pages(v_cache, cfg, "bfloat16", "v_cache", row),
         _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
@@ -585,7 +594,7 @@ def locks_weigh(cfg: LocksConfig, q, lse, k_cache, block_table, seq_lens, weight
     if q.dim() == 4:
         shape = (cfg.batch, rows, cfg.n_q_heads, cfg.head_dim)
     rc = load_library().locks_weigh(
-        ctypes.byref(cfg.c()), _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
+        cfg.ref, _sized(q, "bfloat16", shape, "q"), rows,
         _sized(lse, "float32", shape[:-1], "lse"),
         _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", (cfg.head_dim,)),
         _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
@@ -599,7 +608,7 @@ def locks_weigh(cfg: LocksConfig, q, lse, k_cache, block_table, seq_lens, weight
 
 
 def evict_workspace_bytes(cfg: LocksConfig, budget: int) -> int:
-    return int(load_library().locks_evict_workspace_bytes(ctypes.byref(cfg.c()), budget))
+    return int(load_library().locks_evict_workspace_bytes(cfg.ref, budget))
 
 
 def locks_evict(cfg: LocksConfig, budget: int, recent: int, k_cache, v_cache, block_table, seq_lens,
@@ -611,7 +620,7 @@ def locks_evict(cfg: LocksConfig, budget: int, recent: int, k_cache, v_cache, bl
     wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
     row = (cfg.head_dim,)
     rc = load_library().locks_evict(
-        ctypes.byref(cfg.c()), int(budget), int(recent),
+        cfg.ref, int(budget), int(recent),
         _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", row),
         _pages(v_cache, cfg, "bfloat16", "v_cache", row),
         _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),

@@ -39,7 +39,7 @@ struct Shared {
   uint32_t tmem;
   int dead;
   ListPlace place;
-  float lse[2][256];                                  // of the unit, times log2 e; units in turn
+  alignas(16) float minus_lse[2][256];                // of the unit, times log2 e; units in turn
 };
 
 struct Unit {
@@ -177,6 +177,18 @@ __device__ void issue_role(const WeighParams& p, Shared& sh, unsigned char* qbuf
   mbar_wait_bounded(&sh.done, 0);
 }
 
+__device__ __forceinline__ void add_weights(const float* x, const float* minus, float2 scale, float2& a0,
+                                            float2& a1) {
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    const float4 m = *reinterpret_cast<const float4*>(minus + k);
+    float2 y = ffma2(make_float2(x[k], x[k + 1]), scale, make_float2(m.x, m.y));
+    float2 z = ffma2(make_float2(x[k + 2], x[k + 3]), scale, make_float2(m.z, m.w));
+    a0 = fadd2(a0, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+    a1 = fadd2(a1, make_float2(ex2_approx(z.x), ex2_approx(z.y)));
+  }
+}
+
 __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const uint32_t d = sh.tmem + (uint32_t(tid >> 5 << 5) << 16) + w * p.n_cols;
@@ -185,15 +197,18 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
   Unit u;
   int stage = 0, units = 0;
   while (walk.next(p, u)) {
-    // this unit's log-sum-exps (a row that sees nothing has -inf, and its weights none), a part a
-    // warp.  A warp that gets here has finished the unit before, so once all have arrived for
+    // This unit's log-sum-exps, a part a warp.  (A row that sees nothing has -inf, and gives no weight: as
+    // the columns behind the rows, whose queries are zeros, it gets the factor 2^-inf.)
+    // A warp that gets here has finished the unit before, so once all have arrived for
     // unit n, nobody reads the buffer of unit n - 1, which unit n + 1 takes.
-    float* lse = sh.lse[units & 1];
-    for (int c = threadIdx.x; c < rows; c += 256) {
+    float* minus = sh.minus_lse[units & 1];
+    for (int c = threadIdx.x; c < p.n_cols; c += 256) {
       const int r = c / p.group;
-      const float x = p.lse[(int64_t(u.b) * p.n_rows + r) * (p.n_kv_heads * p.group) +
-                            u.head * p.group + c - r * p.group];
-      lse[c] = x == -INFINITY ? INFINITY : x * kLog2e;
+      float x = -INFINITY;
+      if (c < rows)
+        x = p.lse[(int64_t(u.b) * p.n_rows + r) * (p.n_kv_heads * p.group) + u.head * p.group +
+                  c - r * p.group];
+      minus[c] = x == -INFINITY ? -INFINITY : -x * kLog2e;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.lse_full);
@@ -218,22 +233,38 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
       tc_fence_after();
       // rows from c0 on see this slot
       const int c0 = max(0, slot - (u.len - p.n_rows)) * p.group;
-      float a[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < rows; c += 16) {
-        float x[16];
-        tmem_ld16(d + c, x);
-        tmem_wait_ld();
+      const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+      float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+      if (__any_sync(kFull, there && c0 > 0)) {
+        for (int c = 0; c < p.n_cols; c += 16) {
+          float x[16];
+          tmem_ld16(d + c, x);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float y = ex2_approx(fmaf(x[k], p.scale_log2, -lse[c + k]));
-          if (c + k >= c0 && c + k < rows) a[k & 3] += y;
+          for (int k = 0; k < 16; ++k) {
+            const float y = ex2_approx(fmaf(x[k], p.scale_log2, minus[c + k]));
+            if (c + k >= c0) a0.x += y;
+          }
+        }
+      } else {
+        // two columns an instruction, sixteen loaded while sixteen are added up
+        float x[2][16];
+        tmem_ld16(d, x[0]);
+        for (int c = 0; c < p.n_cols; c += 32) {
+          tmem_wait_ld();
+          if (c + 16 < p.n_cols) tmem_ld16(d + c + 16, x[1]);
+          add_weights(x[0], minus + c, scale, a0, a1);
+          if (c + 16 >= p.n_cols) break;
+          tmem_wait_ld();
+          if (c + 32 < p.n_cols) tmem_ld16(d + c + 32, x[0]);
+          add_weights(x[1], minus + c + 16, scale, a0, a1);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.d_empty[w]);
       if (at >= 0) {
-        p.out[at] = fmaf(p.decay, old, (a[0] + a[1]) + (a[2] + a[3]));
+        p.out[at] = fmaf(p.decay, old, (a0.x + a0.y) + (a1.x + a1.y));
         if (fresh && p.positions) p.positions[at] = slot + (p.evicted ? p.evicted[u.b] : 0);
       }
     }
@@ -268,8 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(&map_q);
     prefetch_map(&map_k);
   }
-  // columns behind the rows are loaded with the last of them: whatever they hold goes unused
-  for (int i = tid; i < 512; i += kThreads) sh.lse[i >> 8][i & 255] = 0.f;
+  // the rows behind the queries' last, which no load writes, become zeros
+  for (int i = tid; i < 4 * p.q_half / 16; i += kThreads)
+    reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  proxy_fence_smem();
   griddep_wait();
   tc_fence_before();
   const int share = locate<kThreads>(
@@ -295,11 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int launch_weigh(WeighParams p, const CUtensorMap& q, const CUtensorMap& k, cudaStream_t stream) {
   const int rows = p.n_rows * p.group;
-  p.q_half = (rows + 7) / 8 * 1024;                   // 64 columns of the unit's queries, whole swizzle atoms
   p.n_cols = (rows + 15) / 16 * 16;
+  p.q_half = p.n_cols * 128;                          // 64 columns of the unit's queries, and zeros
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.n_cols) p.tmem_cols *= 2;
-  // (the product reads n_cols rows of each half: up to 8 behind the second one)
   const int fixed = 4 * p.q_half + int(sizeof(Shared));
   p.ring = (int(kMaxSmemBlock) - fixed) / kTileBytes;
   if (p.ring > kMaxRing) p.ring = kMaxRing;
