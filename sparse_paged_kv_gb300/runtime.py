@@ -366,6 +366,171 @@ class QuantCache:
         return cuda.stream(stream)
 
 
+class BatchCache:
+    """The bf16 paged cache of one attention layer for a batch whose sequences share prefixes, kept
+    within a budget: attention reads a shared prefix once for its whole group, every cached token
+    gathers the attention weight it receives, and a sequence with more than `budget_tokens` tokens
+    behind its fixed ones loses those of least weight (each KV head for itself), but for the
+    `recent_tokens` newest.
+
+    Sequences group_starts[g] .. group_starts[g + 1] - 1 have their first prefix_pages[g] pages in
+    common (host integers; None: nothing is shared); block_table names a group's pages in each of
+    its rows.  `fixed` is how many first tokens of each sequence are never weighed nor evicted: its
+    prefix by default, and at least that.  `max_rows` is the most query rows a sequence in a call
+    (drafted tokens, the last tokens of a prompt).  Without budget_tokens nothing is weighed.
+
+    Keys are cached as they are given, rotated: the token that a step appends stands at
+    next_positions().  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
+    1, 2, 4 or 8 query heads a KV head)."""
+
+    def __init__(self, cfg: B.LocksConfig, block_table, group_starts=None, prefix_pages=None,
+                 budget_tokens: int = 0, recent_tokens: int = 0, decay: float = 1.0, fixed=None,
+                 max_rows: int = 1, device: str = "cuda"):
+        import torch
+        self.torch, self.cfg, self.device = torch, cfg, device
+        table = np.asarray(block_table, np.int32)
+        if table.shape != (cfg.batch, cfg.max_pages):
+            raise ValueError(f"block_table: shape {(cfg.batch, cfg.max_pages)} expected, got {table.shape}")
+        if (group_starts is None) != (prefix_pages is None):
+            raise ValueError("group_starts, prefix_pages: both or neither expected")
+        shared = np.zeros(cfg.batch, np.int64)          # tokens of each sequence's prefix
+        starts = pages = None
+        if group_starts is not None:
+            starts, pages = np.asarray(group_starts, np.int32), np.asarray(prefix_pages, np.int32)
+            if starts.shape != (pages.size + 1,) or (np.diff(starts) < 0).any() or starts[0] < 0 or \
+                    starts[-1] > cfg.batch:
+                raise ValueError("group_starts: ascending, within the batch, one more than prefix_pages expected")
+            if (pages < 0).any() or (pages > cfg.max_pages).any():
+                raise ValueError(f"prefix_pages: 0 to {cfg.max_pages} expected")
+            for a, z, n in zip(starts, starts[1:], pages):
+                if (table[a:z, :n] != table[a:a + 1, :n]).any():
+                    raise ValueError("block_table: a group's rows name the same blocks for its prefix")
+                shared[a:z] = int(n) * cfg.page_size
+        held = shared if fixed is None else np.asarray(fixed, np.int64)
+        if held.shape != (cfg.batch,) or (held < shared).any():
+            raise ValueError("fixed: a number for every sequence, its prefix at least, expected")
+        self.budget, self.recent, self.decay = int(budget_tokens), int(recent_tokens), float(decay)
+        if self.budget < 0 or not 0 <= self.recent <= self.budget:
+            raise ValueError("budget_tokens >= 0 and recent_tokens of 0 to budget_tokens expected")
+        size = B.prefix_workspace_bytes(cfg, 0 if pages is None else pages.size, max_rows)
+        if size == 0 and cfg.batch:
+            raise B.LocksError("locks_prefix_workspace_bytes", B.LOCKS_ERR_UNSUPPORTED, "unsupported cfg")
+        self.max_rows = int(max_rows)
+
+        def zeros(*shape, dtype=torch.uint8):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        def ints(x):
+            return None if x is None else torch.from_numpy(np.asarray(x, np.int32)).to(device)
+
+        pool = (cfg.num_blocks, cfg.n_kv_heads, cfg.page_size)
+        self.k_cache = zeros(*pool, cfg.head_dim, dtype=torch.bfloat16)
+        self.v_cache = zeros(*pool, cfg.head_dim, dtype=torch.bfloat16)
+        self.block_table, self.group_starts, self.prefix_pages = ints(table), ints(starts), ints(pages)
+        self.fixed = ints(held)
+        self.seq_lens = zeros(cfg.batch, dtype=torch.int32)
+        self.evicted = zeros(cfg.batch, dtype=torch.int32)
+        self.status = zeros(1, dtype=torch.int32)
+        self.workspace = zeros(max(1, size))
+        self.out = zeros(cfg.batch, cfg.n_q_heads, cfg.head_dim, dtype=torch.bfloat16)
+        self.out_lse = zeros(cfg.batch, cfg.n_q_heads, dtype=torch.float32)
+        self.weights = self.positions = None
+        if self.budget:
+            self.weights = zeros(*pool, dtype=torch.float32)
+            self.positions = zeros(*pool, dtype=torch.int32)
+            self.ws_evict = zeros(max(1, B.evict_workspace_bytes(cfg, self.budget)))
+
+    def next_positions(self):
+        """Position of each sequence's next token (int32 [batch] on the device): its cached tokens
+        and the evicted ones."""
+        return self.seq_lens + self.evicted
+
+    def append(self, k, v, stream=None):
+        """One token per sequence, k, v bf16 [batch][H_kv][d], at its current length."""
+        B.locks_append_kv(self.cfg, k, v, self.k_cache, self.v_cache, self.block_table,
+                          self.seq_lens, status=self.status, stream=stream)
+
+    def attend(self, q, out=None, out_lse=None, stream=None):
+        """(out, log-sum-exp) of q [batch][H_q][d], the newest token of each sequence, or
+        [batch][rows][H_q][d], its newest `rows` tokens; into self.out and self.out_lse for one row
+        (unless others are given), else into new tensors."""
+        torch = self.torch
+        if q.dim() == 4 and q.shape[1] > self.max_rows:
+            raise ValueError(f"q: at most max_rows = {self.max_rows} rows a sequence expected, got {q.shape[1]}")
+        if out is None:
+            out = self.out if q.dim() == 3 else torch.empty_like(q)
+        if out_lse is None:
+            out_lse = self.out_lse if q.dim() == 3 else torch.empty(
+                q.shape[:-1], dtype=torch.float32, device=q.device)
+        B.locks_prefix_decode(self.cfg, q, self.k_cache, self.v_cache, self.block_table, self.seq_lens,
+                              self.group_starts, self.prefix_pages, out, self.workspace,
+                              out_lse=out_lse, status=self.status, stream=stream)
+        return out, out_lse
+
+    def weigh(self, q, lse, n_new: int, fresh: bool = False, stream=None):
+        """Add the weight that q's rows (with their log-sum-exps) give every token behind the fixed
+        ones; the last n_new tokens, or with `fresh` all of them, had none."""
+        if not self.budget:
+            raise ValueError("a BatchCache made without budget_tokens weighs nothing")
+        B.locks_weigh(self.cfg, q, lse, self.k_cache, self.block_table, self.seq_lens,
+                      None if fresh else self.weights, self.weights, n_new=n_new, decay=self.decay,
+                      fixed=self.fixed, positions=self.positions, evicted=self.evicted,
+                      status=self.status, stream=stream)
+
+    def evict(self, stream=None):
+        """Cut every sequence to its budget."""
+        if not self.budget:
+            raise ValueError("a BatchCache made without budget_tokens evicts nothing")
+        B.locks_evict(self.cfg, self.budget, self.recent, self.k_cache, self.v_cache,
+                      self.block_table, self.seq_lens, self.weights, self.positions, self.evicted,
+                      self.ws_evict, fixed=self.fixed, status=self.status, stream=stream)
+
+    def observe(self, q, stream=None):
+        """The end of a prompt that stands in the cache: attention of its last rows, q
+        [batch][rows][H_q][d]; with a budget they weigh every token, and the least are evicted."""
+        out, lse = self.attend(q, stream=stream)
+        if self.budget:
+            self.weigh(q, lse, n_new=0, fresh=True, stream=stream)
+            self.evict(stream=stream)
+        return out, lse
+
+    def step(self, q, k, v, stream=None):
+        """One decode step: append each sequence's token, attend (-> self.out, self.out_lse), and
+        with a budget weigh and evict."""
+        self.append(k, v, stream=stream)
+        self.attend(q, self.out, self.out_lse, stream=stream)
+        if self.budget:
+            self.weigh(q, self.out_lse, n_new=1, stream=stream)
+            self.evict(stream=stream)
+        return self.out, self.out_lse
+
+    def capture_step(self, q, k, v):
+        """A CUDA graph of step() over these buffers: fill q, k, v and replay.  The kernels run once
+        before the capture, on lengths that let them do nothing, so the cache stays as it is."""
+        torch, c = self.torch, self.cfg
+        lens, gone, status = torch.zeros_like(self.seq_lens), self.evicted.clone(), torch.zeros_like(self.status)
+        full = torch.full_like(lens, c.max_pages * c.page_size)      # (a full sequence takes no token)
+        cur = torch.cuda.current_stream(self.device)
+        side = torch.cuda.Stream(device=self.device)
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            B.locks_append_kv(c, k, v, self.k_cache, self.v_cache, self.block_table, full, status=status)
+            out, lse = torch.empty_like(self.out), torch.empty_like(self.out_lse)
+            B.locks_prefix_decode(c, q, self.k_cache, self.v_cache, self.block_table, lens, None, None,
+                                  out, self.workspace, out_lse=lse, status=status)
+            if self.budget:
+                B.locks_weigh(c, q, lse, self.k_cache, self.block_table, lens, self.weights, self.weights,
+                              fixed=self.fixed, positions=self.positions, evicted=gone, status=status)
+                B.locks_evict(c, self.budget, self.recent, self.k_cache, self.v_cache, self.block_table,
+                              lens, self.weights, self.positions, gone, self.ws_evict, fixed=self.fixed,
+                              status=status)
+        cur.wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.step(q, k, v)
+        return graph
+
+
 class DecodeLoop:
     """Decode steps of one layer as an engine runs them, with no host round
     trip: each step appends the new token (current stream), builds the
