@@ -528,7 +528,11 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
  * synchronisation, status bits).  The calls take a locks_cfg_t of which rank
  * and summary_dtype are not read; supported are head_dim = 128; page_size 64,
  * 32 or 16; any G from 1 to 16; max_pages < 2^24, max_pages * page_size < 2^31;
- * num_blocks * n_kv_heads < 2^31; batch * n_q_heads < 2^24.
+ * num_blocks * n_kv_heads < 2^31; batch * n_q_heads < 2^24.  locks_weigh takes
+ * batch * n_kv_heads * (ceil(max_pages * page_size / 128) + 1) < 2^31, and
+ * locks_prefix_decode, with six times the first term and two more units a
+ * sequence and group, correspondingly less, with batch * n_rows < 2^24 - 256 and
+ * batch * n_rows * n_q_heads < 2^28 (LOCKS_ERR_UNSUPPORTED otherwise).
  *
  * The newest tokens of a sequence: the calls take the queries of the last
  * n_rows tokens of every sequence, q [batch][n_rows][n_q_heads][d]: 1 in a
@@ -566,7 +570,7 @@ size_t locks_prefix_workspace_bytes(const locks_cfg_t* cfg, int32_t n_groups, in
  *   workspace     >= locks_prefix_workspace_bytes bytes, 16-byte aligned
  *
  * Logits, maxima, sums and accumulators are float32.  Weights are rounded to
- * bf16 before their product with the values (2^-9 of each at most), and the
+ * bf16 before their product with the values (2^-8 of each at most), and the
  * output divides by their sum.  Slots that no row of a sequence (of a group,
  * within the prefix) sees may hold anything; a NaN or an infinity in the value of a token that only some
  * of the rows see (one of the last n_rows tokens, or a token of the prefix behind

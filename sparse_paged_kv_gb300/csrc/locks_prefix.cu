@@ -27,7 +27,7 @@
 // A second kernel joins the pieces of each row.
 //
 // P is rounded to bf16 because V is bf16 and both operands of a matrix
-// instruction have one type: each weight is off by 2^-9 of itself at most (the
+// instruction have one type: each weight is off by 2^-8 of itself at most (the
 // output's own rounding is as large).  The output divides by the sum of the
 // rounded weights, so that a row with one dominant token keeps that token's
 // value exactly; the log-sum-exp comes from the unrounded sum.
