@@ -47,6 +47,7 @@ struct Shared {
   int2 count[kMaxKeys / 32];                          // (holes or ties, movers) of 32 slots; then before them
   int2 total;                                         // of this block
   int digit, above, equal;
+  int4 found;                                         // T, need and equal, from the cluster's first block
   uint64_t least[2][kThreads / 32], block_least[2];   // by rounds
   int hole[kFew], mover[kFew], few_moves;
 };
@@ -246,40 +247,12 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
 
   // ---- the budget-th largest key, T; `need` slots of that key stay, of `equal` ----
   uint32_t T = 0;
-  int need = p.budget, equal = 0, shift = 32;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, top = shift;
-    shift -= bits;
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int c0 = lo; c0 < hi; c0 += p.keys) {
-      const int c1 = min(hi, c0 + p.keys);
-      load(c0, c1);
-      const int from = shifted, to = c1 - c0 + shifted;        // of the keys held
-      for (int i = 4 * tid; i < to; i += 4 * kThreads) {
-        const uint4 four = *reinterpret_cast<const uint4*>(keys + i);
-        const uint32_t k4[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j >= from && i + j < to && (pass == 0 || k4[j] >> top == T >> top))
-            atomicAdd(&sh.hist[(k4[j] >> shift) & ((1u << bits) - 1)], 1);
-      }
-    }
-    meet();
-    // thread t has bins 4t .. 4t + 3 from the top down.  A cluster's counts are added up in its first
-    // block, where few bins hold anything, and every block reads them there.
+  int need = p.budget, equal = 0;
+  // the digit at `shift` of T, from the block's histogram or its cluster's first block's: thread t has
+  // bins 4t .. 4t + 3 from the top down
+  auto take = [&](const int* hist) {
     const int bin = kBins - 4 - 4 * tid;
-    if (C > 1) {
-      if (rank > 0) {
-        int* sum = cluster.map_shared_rank(sh.hist, 0) + bin;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (sh.hist[bin + k]) atomicAdd(sum + k, sh.hist[bin + k]);
-      }
-      cluster.sync();
-    }
-    const int4 bins = *reinterpret_cast<const int4*>((C > 1 ? cluster.map_shared_rank(sh.hist, 0) : sh.hist) + bin);
+    const int4 bins = *reinterpret_cast<const int4*>(hist + bin);
     const int v[4] = {bins.w, bins.z, bins.y, bins.x}, sum = v[0] + v[1] + v[2] + v[3];
     int2 unused;
     const int before = scan(sh, make_int2(sum, 0), unused).x;
@@ -295,10 +268,88 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
         at += v[k];
       }
     }
-    meet();                                           // (and the histograms are cleared next)
+  };
+  auto taken = [&](int shift) {
     T |= uint32_t(sh.digit) << shift;
     need -= sh.above;
     equal = sh.equal;
+  };
+  constexpr int kShift[3] = {21, 10, 0}, kDigits[3] = {2047, 2047, 1023};
+  uint32_t* few = reinterpret_cast<uint32_t*>(sh.count);
+  if (tid == 0) sh.few_moves = 0;                     // (how many keys are in `few`)
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = kShift[pass], top = pass ? kShift[pass - 1] : 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    for (int c0 = lo; c0 < hi; c0 += p.keys) {
+      const int c1 = min(hi, c0 + p.keys);
+      load(c0, c1);
+      const int from = shifted, to = c1 - c0 + shifted;        // of the keys held
+      for (int i = 4 * tid; i < to; i += 4 * kThreads) {
+        const uint4 four = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t k4[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j >= from && i + j < to && (pass == 0 || k4[j] >> top == T >> top))
+            atomicAdd(&sh.hist[(k4[j] >> shift) & kDigits[pass]], 1);
+      }
+    }
+    meet();
+    // a cluster's counts are added up in its first block, where few bins hold anything
+    if (C > 1) {
+      const int bin = 4 * tid;
+      if (rank > 0) {
+        int* sum = cluster.map_shared_rank(sh.hist, 0) + bin;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (sh.hist[bin + k]) atomicAdd(sum + k, sh.hist[bin + k]);
+      }
+      cluster.sync();
+    }
+    take(C > 1 ? cluster.map_shared_rank(sh.hist, 0) : sh.hist);
+    meet();                                           // (and the histograms are cleared next)
+    taken(shift);
+    if (pass == 0 && equal <= int(sizeof(sh.count) / 4)) {
+      // The keys of T's first digit are few: the first block takes them and the other two digits
+      // alone, which spares the cluster six meetings.
+      uint32_t* all = C > 1 ? cluster.map_shared_rank(few, 0) : few;
+      int* used = C > 1 ? cluster.map_shared_rank(&sh.few_moves, 0) : &sh.few_moves;
+      for (int c0 = lo; c0 < hi; c0 += p.keys) {
+        const int c1 = min(hi, c0 + p.keys);
+        load(c0, c1);
+        const int from = shifted, to = c1 - c0 + shifted;
+        for (int i = 4 * tid; i < to; i += 4 * kThreads) {
+          const uint4 four = *reinterpret_cast<const uint4*>(keys + i);
+          const uint32_t k4[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (i + j >= from && i + j < to && k4[j] >> shift == T >> shift) all[atomicAdd(used, 1)] = k4[j];
+        }
+      }
+      meet();
+      if (rank == 0) {
+        const int n_few = equal;
+#pragma unroll 1
+        for (int digit = 1; digit < 3; ++digit) {
+          for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+          __syncthreads();
+          for (int i = tid; i < n_few; i += kThreads)
+            if (few[i] >> kShift[digit - 1] == T >> kShift[digit - 1])
+              atomicAdd(&sh.hist[(few[i] >> kShift[digit]) & kDigits[digit]], 1);
+          __syncthreads();
+          take(sh.hist);
+          __syncthreads();
+          taken(kShift[digit]);
+        }
+        if (tid < C) *(C > 1 ? cluster.map_shared_rank(&sh.found, tid) : &sh.found) = make_int4(int(T), need, equal, 0);
+      }
+      meet();
+      T = uint32_t(sh.found.x);
+      need = sh.found.y;
+      equal = sh.found.z;
+      break;
+    }
   }
 
   // ---- numbers of ties, holes and movers ----
@@ -411,8 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     at.y += sum.y;
     if (chunks) __syncthreads();
   }
-  __threadfence();
-  meet();
+  meet();                                             // (orders the lists in global memory too)
 
   finish();
 
