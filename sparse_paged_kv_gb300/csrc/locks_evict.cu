@@ -455,8 +455,11 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
       const int2 x = i < c1 - c0 ? moved(c0 + i, key(c0 + i)) : make_int2(0, 0);
       const unsigned vx = __ballot_sync(kFull, x.x), vy = __ballot_sync(kFull, x.y);
       const unsigned less = (1u << lane) - 1;
-      if (x.x) to[at.x + sh.count[i >> 5].x + __popc(vx & less)] = place(c0 + i);
-      if (x.y) from[at.y + sh.count[i >> 5].y + __popc(vy & less)] = place(c0 + i);
+      if (x.x | x.y) {
+        const int2 before = sh.count[i >> 5];
+        int64_t* entry = x.x ? to + at.x + before.x + __popc(vx & less) : from + at.y + before.y + __popc(vy & less);
+        *entry = place(c0 + i);
+      }
     }
     at.x += sum.x;
     at.y += sum.y;
