@@ -534,15 +534,16 @@ __device__ void issue_role(Shared& sh, unsigned char* qtile, unsigned char* ring
       if (!ok) break;
       const uint32_t ns = (c + 2) % kRing;
       scored = pair && !last && mbar_try_wait(&sh.full[ns], (c + 2) / kRing & 1);
-      ok = mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
-      if (!ok) break;
-      ++jobs;
       // With both groups on every stage, P V and the next S go to the tensor cores as one block: two
       // groups in step would wait for their products together and then crowd the schedulers together
       // (a stage took 4000 cycles); one block after the other, each group's exponentials meet the other's
-      // products.  The lock is a courtesy: after a while the block goes without it.
+      // products.  The lock is taken before the wait for P, so that nothing is left to do after it;
+      // it is a courtesy: after a while the block goes without it.
       if (scored)
         for (int tries = 0; tries < 64 && atomicCAS_block(&sh.lock, 0, 1); ++tries) {}
+      ok = mbar_wait_or_dead(&sh.p_full[w], jobs & 1, &sh.dead);
+      if (!ok) break;
+      ++jobs;
       tc_fence_after();
       mma_ts_128(t_o, t_s, v_desc + vs * (kTileBytes >> 4), kIdescO, i != first);
       mma_commit(&sh.empty[vs]);
