@@ -61,7 +61,6 @@ constexpr int kGroupsHeld = 64;                       // groups whose bounds a b
 // quarters of the first (measured: 1.4 us where memory bounds it, 2.2 us, 0.6 us).
 constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 3;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
-constexpr int kChunk = 32;                            // columns of S at a time
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
 // A unit's stages [s0, s0 + stages) that this block has, as the loading warp hands them to the others.
@@ -225,18 +224,13 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
     return theirs[jobs & 1];
   };
 
-  auto load_scores = [&](float* s, int c) {
-    if constexpr (kChunk == 32) tmem_ld32(t_s + c, s);
-    else tmem_ld16(t_s + c, s);
-    tmem_wait_ld();
-  };
   // columns that the row does not see, or of pages whose block is invalid (col0: of the stage)
   auto mask_scores = [&](float* s, int seen, int bad, int col0) {
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) s[k] = k < seen ? s[k] : -INFINITY;
+    for (int k = 0; k < 64; ++k) s[k] = k < seen ? s[k] : -INFINITY;
     if (bad) {
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k)
+      for (int k = 0; k < 64; ++k)
         if (bad >> ((col0 + k) >> p.page_shift) & 1) s[k] = -INFINITY;
     }
   };
@@ -270,20 +264,17 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
         tc_fence_after();
         const int bad = *static_cast<volatile int*>(&sh.bad[(stage0 + i) & 7]);
         if (any) {
-          // Twice over the columns, kChunk at a time in loops: short enough for the instruction cache,
-          // which the issuing threads share, and S stays in tensor memory meanwhile.
           const int seen = lim - tok - 64 * h;
           const bool masked = __any_sync(kFull, seen < 64) || bad;
-          float s[kChunk], x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 64; c += kChunk) {
-            load_scores(s, c);
-            if (masked) mask_scores(s, seen - c, bad, 64 * h + c);
+          float s[64], x0 = -INFINITY, x1 = -INFINITY;
+          tmem_ld32(t_s, s);
+          tmem_ld32(t_s + 32, s + 32);
+          tmem_wait_ld();
+          if (masked) mask_scores(s, seen, bad, 64 * h);
 #pragma unroll
-            for (int k = 0; k < kChunk; k += 4) {
-              x0 = fmaxf(fmaxf(x0, s[k]), s[k + 1]);
-              x1 = fmaxf(fmaxf(x1, s[k + 2]), s[k + 3]);
-            }
+          for (int k = 0; k < 64; k += 4) {
+            x0 = fmaxf(fmaxf(x0, s[k]), s[k + 1]);
+            x1 = fmaxf(fmaxf(x1, s[k + 2]), s[k + 3]);
           }
           const float top = fmaxf(x0, x1) * p.scale_log2;
           // (rows past the unit's last hold whatever the tile held, and decide nothing)
@@ -320,14 +311,12 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
           const float mu = m == -INFINITY ? 0.f : m;
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mu, -mu);
           float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-#pragma unroll 1
-          for (int c = 0; c < 64; c += kChunk) {
-            load_scores(s, c);
-            if (masked) mask_scores(s, seen - c, bad, 64 * h + c);
-            uint32_t pk[kChunk / 2];
 #pragma unroll
-            for (int k = 0; k < kChunk / 2; ++k) {
-              float2 x = ffma2(make_float2(s[2 * k], s[2 * k + 1]), sc, off);
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
               x.x = ex2_approx(x.x);
               x.y = ex2_approx(x.y);
               const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
@@ -335,8 +324,7 @@ __device__ void softmax_role(const PrefixParams& p, Shared& sh, unsigned char* r
               a0 = fadd2(a0, x);
               a1 = fadd2(a1, make_float2(bf16_lo(pk[k]), bf16_hi(pk[k])));
             }
-            if constexpr (kChunk == 32) tmem_st16(t_s + c / 2, pk);
-            else tmem_st8(t_s + c / 2, pk);
+            tmem_st16(t_s + c / 2, pk);
           }
           l += a0.x + a0.y;
           lr += a1.x + a1.y;
