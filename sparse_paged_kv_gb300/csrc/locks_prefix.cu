@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // kListed pieces a unit at a time.  Then thread = (row, chunks of 4 dims): neighbouring threads have
 // neighbouring rows, whose parts lie side by side.  With fewer than 8 rows the threads left over split
 // the parts, and are joined in shared memory.
+// (Few loads ahead and four blocks an SM: with twice the loads and two blocks 16384 rows took 18 us, not 14.)
 constexpr int kJoinThreads = 256, kListed = 32;
 
 struct UnitParts {
@@ -670,7 +671,7 @@ struct UnitParts {
 };
 
 template <int RB>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const PrefixParams p) {
   constexpr int kChunkThreads = RB >= 8 ? kJoinThreads / RB : 32, kChunks = 32 / kChunkThreads;
   constexpr int kSplits = kJoinThreads / (RB * kChunkThreads);
   __shared__ UnitParts s_unit[2 * RB];
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PrefixParams p
     }
     __syncthreads();
     const int n0 = each0 * round, n = n0 + each1 * round;
-    constexpr int kAhead = kChunks > 1 ? 2 : 4;
+    constexpr int kAhead = kChunks > 1 ? 1 : 3;
     for (int t0 = sub; t0 < n; t0 += kSplits * kAhead) {
       float4 s[kAhead], z[kAhead], a[kAhead][kChunks];
 #pragma unroll
