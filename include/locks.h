@@ -67,7 +67,7 @@ extern "C" {
 #define LOCKS_DEV_NOT_CONVERGED  0x4  /* Jacobi hit max_sweeps before its tolerance       */
 #define LOCKS_DEV_BAD_PAGE_ID    0x8  /* selected page id outside [0, n): entry skipped   */
 #define LOCKS_DEV_BAD_SEQ_LEN    0x10 /* seq_len > max_pages * page_size: clamped         */
-#define LOCKS_DEV_BAD_GROUP      0x20 /* group_starts or prefix_pages out of range: clamped */
+#define LOCKS_DEV_BAD_GROUP      0x20 /* group_starts not ascending: no group; prefix_pages: clamped */
 
 /* summary record element type */
 #define LOCKS_SUMMARY_F32  0
@@ -527,7 +527,7 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
  * The conventions at the top hold (device pointers, no allocation, no
  * synchronisation, status bits).  The calls take a locks_cfg_t of which rank
  * and summary_dtype are not read; supported are head_dim = 128; page_size 64,
- * 32 or 16; any G from 1 to 16; max_pages < 2^24, max_pages * page_size < 2^31;
+ * 32 or 16; any G from 1 to 16; max_pages < 2^24, max_pages * page_size < 2^30;
  * num_blocks * n_kv_heads < 2^31; batch * n_q_heads < 2^24.  locks_weigh takes
  * batch * n_kv_heads * (ceil(max_pages * page_size / 128) + 1) < 2^31, and
  * locks_prefix_decode, with six times the first term and two more units a
@@ -560,7 +560,8 @@ size_t locks_prefix_workspace_bytes(const locks_cfg_t* cfg, int32_t n_groups, in
  *   seq_lens      int32 [batch], the new tokens included.  A sequence may end
  *                 inside its group's prefix
  *   group_starts  int32 [n_groups + 1], ascending, within 0 .. batch; sequences
- *                 outside every group share nothing
+ *                 outside every group share nothing.  If they are not, every
+ *                 sequence is read through its own row (LOCKS_DEV_BAD_GROUP)
  *   prefix_pages  int32 [n_groups], each 0 .. max_pages
  *   n_groups      0 .. batch (0: the two arrays are not read and may be NULL)
  *   out           bf16 [batch][n_rows][n_q_heads][d], 16-byte aligned; a row

@@ -27,7 +27,7 @@ int check_batch_cfg(const locks_cfg_t* c) {
     return LOCKS_ERR_UNSUPPORTED;
   if (c->n_q_heads / c->n_kv_heads > locks::kBatchMaxGroup) return LOCKS_ERR_UNSUPPORTED;
   // slots and (block, head) indices are ints
-  if (c->max_pages >= (1 << 24) || int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 31) ||
+  if (c->max_pages >= (1 << 24) || int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 30) ||
       int64_t(c->num_blocks) * c->n_kv_heads >= (int64_t(1) << 31) ||
       int64_t(c->batch) * c->n_q_heads >= (1 << 24))
     return LOCKS_ERR_UNSUPPORTED;

@@ -19,6 +19,7 @@
 // mover its number.  The lists of pool rows go through the workspace, and all warps of the
 // cluster move rows, 16 bytes a lane: lanes 0-15 the key, 16-31 the value.
 // Bound: long prompts by the moves' traffic, a decode step by latency.
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -516,21 +517,37 @@ int evict_list_len(int budget, int64_t slots) { return int(budget < slots / 2 ? 
 int launch_evict(EvictParams p, cudaStream_t stream) {
   const int units = p.batch * p.n_kv_heads;
   const int64_t slots = int64_t(p.max_pages) * p.page_size;
-  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.
-  int C = 1;
-  while (C < 16 && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
-  const int64_t share = (slots + C - 1) / C;
-  p.keys = int(share < kMaxKeys ? (share + 31) / 32 * 32 : kMaxKeys);
   static LaunchOnce once;
+  static std::atomic<int> largest{8};                 // blocks a cluster
   constexpr int kMost = int(sizeof(Shared)) + (kMaxKeys + 4) * 4;
   static_assert(kMost <= int(kMaxSmemBlock), "shared memory of a block");
   if (!once.run([] {
-        return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) ==
-                   cudaSuccess &&
-               cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                   cudaSuccess;
+        if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
+            cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+          return false;
+        // sixteen blocks a cluster are more than every device has to offer
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(16);
+        lc.blockDim = dim3(kThreads);
+        lc.dynamicSmemBytes = kMost;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        int n = 0;
+        largest = cudaOccupancyMaxActiveClusters(&n, evict_kernel, &lc) == cudaSuccess && n > 0 ? 16 : 8;
+        cudaGetLastError();                           // (a refusal is an answer)
+        return true;
       }))
     return LOCKS_ERR_CUDA;
+  const int most = largest;
+  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.
+  int C = 1;
+  while (C < most && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
+  const int64_t share = (slots + C - 1) / C;
+  p.keys = int(share < kMaxKeys ? (share + 31) / 32 * 32 : kMaxKeys);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(unsigned(units) * C);
   lc.blockDim = dim3(kThreads);

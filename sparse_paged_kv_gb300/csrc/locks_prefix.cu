@@ -98,6 +98,7 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max
 // bounds and pages of the groups, held in shared memory or (many of them) as given
 struct Groups {
   const int32_t *start, *pages;
+  bool ascending;         // else no group counts (two could claim a sequence, and the list outgrow an int)
   __device__ __forceinline__ int start_of(const PrefixParams& p, int g) const {
     return clamp_int(start[g], 0, p.batch);
   }
@@ -106,7 +107,7 @@ struct Groups {
   }
   // the group of sequence b, or -1
   __device__ int of(const PrefixParams& p, int b) const {
-    int lo = 0, hi = p.n_groups;                      // the groups that start at or before b
+    int lo = 0, hi = ascending ? p.n_groups : 0;      // the groups that start at or before b
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (start_of(p, mid) <= b) lo = mid + 1;
@@ -142,7 +143,7 @@ __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) 
     n.page0 = 0;
     n.q0 = a * p.n_rows;
     n.nq = seqs * p.n_rows;
-    if (n.nq == 0) n.tokens = 0;
+    if (n.nq == 0 || !groups.ascending) n.tokens = 0;
   } else {
     const int b = e - p.n_groups, len = length_of(p, b), g = groups.of(p, b);
     n.page0 = g >= 0 ? groups.pages_of(p, g) : 0;
@@ -588,18 +589,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // what follows reads memory that the kernel before this one may write
   griddep_wait();
-  Groups groups = {p.group_starts, p.prefix_pages};
-  if (p.n_groups <= kGroupsHeld) {
-    for (int i = tid; i <= p.n_groups && p.n_groups; i += kThreads) {
-      sh.group_start[i] = p.group_starts[i];
-      if (i < p.n_groups) sh.group_pages[i] = p.prefix_pages[i];
+  Groups groups = {p.group_starts, p.prefix_pages, true};
+  if (tid < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + tid));
+  const bool held = p.n_groups <= kGroupsHeld;
+  bool out_of_order = false;
+  for (int i = tid; i < p.n_groups; i += kThreads) {
+    const int a = p.group_starts[i], z = p.group_starts[i + 1];
+    out_of_order |= a < 0 || z < a || z > p.batch;
+    if (held) {
+      sh.group_start[i] = a;
+      sh.group_pages[i] = p.prefix_pages[i];
+      if (i == p.n_groups - 1) sh.group_start[i + 1] = z;
     }
-    if (tid < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + tid));
+  }
+  if (held) {
     groups.start = sh.group_start;
     groups.pages = sh.group_pages;
-    __syncthreads();
   }
-
+  groups.ascending = !__syncthreads_or(out_of_order);
   tc_fence_before();
   const int entries = p.n_groups + p.batch;
   int total;
@@ -618,8 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
         } else {
           p.entry_info[e] = make_int4(first, n.stages, n.q0, n.nq);
-          const int a = groups.start[e], z = groups.start[e + 1], n_pages = groups.pages[e];
-          if (a < 0 || z < a || z > p.batch || n_pages < 0 || n_pages > p.max_pages)
+          if (!groups.ascending || groups.pages[e] < 0 || groups.pages[e] > p.max_pages)
             flag_status(p.status, LOCKS_DEV_BAD_GROUP);
         }
       });

@@ -174,6 +174,11 @@ def test_prefix_bad_blocks_and_groups():
         b.pp.copy_(b.ints(pages))
         b.attend()
         assert b.status.item() & B.LOCKS_DEV_BAD_GROUP
+        if pages != [99]:                                   # every sequence through its own row, whole
+            b.check(status=B.LOCKS_DEV_BAD_GROUP)
+    # many groups out of order that claim every sequence again and again
+    b = Batch([200 + i for i in range(80)], 4, 1, 64, [0] + [79, 0] * 39 + [79], [2] * 79, 1, seed=10)
+    b.attend().check(status=B.LOCKS_DEV_BAD_GROUP, sequences=[0, 41, 79])
 
 
 def test_prefix_is_deterministic_and_replays():
