@@ -529,9 +529,9 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
  * and summary_dtype are not read; supported are head_dim = 128; page_size 64,
  * 32 or 16; any G from 1 to 16; max_pages < 2^24, max_pages * page_size < 2^30;
  * num_blocks * n_kv_heads < 2^31; batch * n_q_heads < 2^24.  locks_weigh takes
- * batch * n_kv_heads * (ceil(max_pages * page_size / 128) + 1) < 2^31, and
- * locks_prefix_decode, with six times the first term and two more units a
- * sequence and group, correspondingly less, with batch * n_rows < 2^24 - 256 and
+ * batch * n_kv_heads * (s + 1) < 2^31 with s = ceil(max_pages * page_size / 128), and
+ * locks_prefix_decode (11 s + 8) * n_kv_heads * (batch + n_groups + 1 +
+ * floor(batch * n_rows / (2 floor(128 / G)))) < 2^31, batch * n_rows < 2^24 - 256 and
  * batch * n_rows * n_q_heads < 2^28 (LOCKS_ERR_UNSUPPORTED otherwise).
  *
  * The newest tokens of a sequence: the calls take the queries of the last

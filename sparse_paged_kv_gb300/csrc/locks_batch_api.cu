@@ -47,12 +47,12 @@ int check_prefix(const locks_cfg_t* c, int32_t n_groups, int32_t n_rows) {
   int rc = check_batch_cfg(c);
   if (rc != LOCKS_OK || (rc = check_rows(c, n_rows)) != LOCKS_OK) return rc;
   if (n_groups < 0 || n_groups > c->batch) return LOCKS_ERR_INVALID_ARG;
-  // what the whole list costs (up to 6 a stage, 2 a unit), and rows, are ints: every sequence's own pages and every group's
+  // what the whole list costs (up to 11 a stage, 8 a unit), and rows, are ints: every sequence's own pages and every group's
   // (at most one unit of two tiles more than the sequences fill) over all of the table's pages
   const int64_t stages = (int64_t(c->max_pages) * c->page_size + locks::kStageTok - 1) / locks::kStageTok;
   const int64_t units = int64_t(c->batch) + n_groups +
                         int64_t(c->batch) * n_rows / (2 * tile_tokens(c)) + 1;
-  if ((stages * 6 + 2) * units * c->n_kv_heads >= (int64_t(1) << 31) ||
+  if ((stages * 11 + 8) * units * c->n_kv_heads >= (int64_t(1) << 31) ||
       int64_t(c->batch) * n_rows * c->n_q_heads >= (int64_t(1) << 28) ||
       int64_t(c->batch) * n_rows >= (1 << 24) - 256)
     return LOCKS_ERR_UNSUPPORTED;

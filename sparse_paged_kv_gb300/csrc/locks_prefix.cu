@@ -58,8 +58,10 @@ constexpr int kRing = 5;
 constexpr int kPieces = 16;
 constexpr int kGroupsHeld = 64;                       // groups whose bounds a block holds
 // What the list counts: a stage, one that both groups work on, and a unit's beginning and end, in
-// quarters of the first (measured: 1.4 us where memory bounds it, 2.2 us, 0.6 us).
-constexpr int kCostStage = 4, kCostPair = 6, kCostUnit = 3;
+// eighths of the first.  (A pair's stage takes 1.4 to 2 times as long, more where memory does not bound
+// either; of 14 settings tried these were best or within 2% in all cases: 256 samples of a 16K prompt 161
+// us, with 8, 12, 6 178, with 8, 8, 6 167.)
+constexpr int kCostStage = 8, kCostPair = 11, kCostUnit = 8;
 constexpr uint32_t kTmemCols = 512;                   // S0 S1 O0 O1
 constexpr float kLazy = 8.f;                          // log2 growth of a maximum that is left alone
 
