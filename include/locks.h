@@ -538,7 +538,8 @@ int locks_kv_decode(const locks_kv_cfg_t* cfg, const void* q, const void* k_pool
  * n_rows tokens of every sequence, q [batch][n_rows][n_q_heads][d]: 1 in a
  * decode step, more for drafted tokens or the last tokens of a prompt.  Query
  * row r of a sequence of t tokens is that of slot t - n_rows + r and sees the
- * slots up to it.  A row whose slot would be negative sees nothing.
+ * slots up to it.  A row whose slot would be negative sees nothing.  (Eviction
+ * moves rows: several rows are the newest tokens' if they were appended since.)
  * n_rows <= 2 * floor(128 / G).
  * =========================================================================== */
 
@@ -608,8 +609,8 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
  *   decay         >= 0, 1 to accumulate
  *   positions     nullable int32 pool
  *   evicted       nullable int32 [batch]: tokens that locks_evict took so far
- * All of it in float32.  Slots of a block id outside the pool are left out
- * (LOCKS_DEV_BAD_BLOCK_ID).
+ * All of it in float32.  A key that is not finite gives its slot a NaN.  Slots of
+ * a block id outside the pool are left out (LOCKS_DEV_BAD_BLOCK_ID).
  */
 int locks_weigh(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const float* lse,
                 const void* k_cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -644,7 +645,8 @@ size_t locks_evict_workspace_bytes(const locks_cfg_t* cfg, int32_t budget);
  *   weights, positions  pools as for locks_weigh, 16-byte aligned; written
  *   evicted       int32 [batch]; written
  *   workspace     >= locks_evict_workspace_bytes bytes, 16-byte aligned,
- *                 zero-filled before its first use
+ *                 zero-filled before its first use; shared only by calls of this
+ *                 kind with the same batch (any budget)
  * A slot of a block id outside the pool weighs less than any other; moves from
  * or to one are left out (LOCKS_DEV_BAD_BLOCK_ID).
  */

@@ -452,7 +452,8 @@ class BatchCache:
 
     def attend(self, q, out=None, out_lse=None, stream=None):
         """(out, log-sum-exp) of q [batch][H_q][d], the newest token of each sequence, or
-        [batch][rows][H_q][d], its newest `rows` tokens; into self.out and self.out_lse for one row
+        [batch][rows][H_q][d], its newest `rows` tokens (appended since the last eviction, which
+        moves rows); into self.out and self.out_lse for one row
         (unless others are given), else into new tensors."""
         torch = self.torch
         if q.dim() == 4 and q.shape[1] > self.max_rows:

@@ -434,6 +434,54 @@ def test_evict_bad_blocks():
         assert torch.equal(k[1], before[1])                    # (a block that nobody named)
 
 
+def test_evict_workspace_of_several_budgets():
+    """One workspace for falling budgets, on a stream of its own: each call finds its counters ready."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    batch, hkv, page, pages = 3, 2, 32, 10
+    cfg = B.LocksConfig(batch=batch, n_q_heads=hkv, n_kv_heads=hkv, head_dim=128, page_size=page, rank=8,
+                        max_pages=pages, num_blocks=batch * pages)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(batch * pages, hkv, page, 128, generator=gen, device="cuda").bfloat16() for _ in "kv")
+    w = torch.rand(batch * pages, hkv, page, generator=gen, device="cuda")
+    heaviest = w.view(batch, pages, hkv, page).transpose(1, 2).reshape(batch, hkv, -1).sort(-1, descending=True).values
+    pos = torch.arange(pages * page, dtype=torch.int32, device="cuda").view(pages, 1, page).repeat(batch, hkv, 1)
+    table = torch.arange(batch * pages, dtype=torch.int32, device="cuda").view(batch, pages)
+    lens, gone, status = Batch.ints([pages * page] * batch), Batch.ints([0] * batch), Batch.ints([0])
+    budgets = (200, 197, 60, 59, 1)
+    ws = torch.zeros(max(B.evict_workspace_bytes(cfg, n) for n in budgets), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for n in budgets:
+        B.locks_evict(cfg, n, 0, k, v, table, lens, w, pos, gone, ws, status=status, stream=side)
+        side.synchronize()
+        assert lens.tolist() == [n] * batch and gone.tolist() == [pages * page - n] * batch
+        left = w.view(batch, pages, hkv, page).transpose(1, 2).reshape(batch, hkv, -1)[..., :n]
+        assert torch.equal(left.sort(-1, descending=True).values, heaviest[..., :n])
+    assert status.item() == 0
+
+
+def test_prefix_on_two_streams_at_once():
+    """Two batches on two streams, a workspace each: the bits of the calls one after the other."""
+    import torch
+    batches = [Batch([900 + 7 * i for i in range(12)], 16, 2, 32, [0, 6, 12], [20, 3], rows=2, seed=seed)
+               for seed in (1, 2)]
+    want = []
+    for b in batches:
+        b.attend()
+        want.append((b.out.clone(), b.lse.clone()))
+        b.out.zero_(), b.lse.zero_()
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for b, s in zip(batches, streams):
+            with torch.cuda.stream(s):
+                b.attend()
+    torch.cuda.synchronize()
+    for b, (out, lse) in zip(batches, want):
+        assert torch.equal(b.out, out) and torch.equal(b.lse, lse) and b.status.item() == 0
+
+
 # --------------------------------------------------------------------------
 # together
 # --------------------------------------------------------------------------
