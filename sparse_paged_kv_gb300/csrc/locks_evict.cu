@@ -19,7 +19,7 @@
 // mover its number.  The lists of pool rows go through the workspace, and all warps of the
 // cluster move rows, 16 bytes a lane: lanes 0-15 the key, 16-31 the value.
 // Bound: long prompts by the chain of phases and then the moves' traffic (four 32K prompts cut to 4096
-// tokens: 28 us, and 16 for 117 MB read and written at 7.3 TB/s), a decode step by latency (8 us).
+// tokens: 25 us, and 16 for 117 MB read and written at 7.3 TB/s), a decode step by latency (8 us).
 #include <atomic>
 #include <climits>
 
@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kMostCluster = 16;
 constexpr int kMaxKeys = 40 * 1024;                   // kept in shared memory by a block
 constexpr int kAhead = 2, kMoveAhead = 4;             // loads ahead: four slots of a thread, rows of a warp
 // Up to so many slots to evict are found one after another, as least keys (a decode step evicts as many
@@ -47,7 +48,7 @@ struct Shared {
   alignas(16) int hist[kBins];
   int2 warp[kThreads / 32];
   int2 count[kMaxKeys / 32];                          // (holes or ties, movers) of 32 slots; then before them
-  int2 total;                                         // of this block
+  int2 total[3];                                      // of this block, a count each
   int digit, above, equal;
   int4 found;                                         // T, need and equal, from the cluster's first block
   uint64_t least[2][kThreads / 32], block_least[2];   // by rounds
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     const int shift = kShift[pass], top = pass ? kShift[pass - 1] : 0;
     for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     for (int c0 = lo; c0 < hi; c0 += p.keys) {
       const int c1 = min(hi, c0 + p.keys);
       load(c0, c1);
@@ -297,9 +299,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
             atomicAdd(&sh.hist[(k4[j] >> shift) & kDigits[pass]], 1);
       }
     }
-    meet();
+    __syncthreads();
     // a cluster's counts are added up in its first block, where few bins hold anything
     if (C > 1) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // (the first block's bins are cleared)
       const int bin = 4 * tid;
       if (rank > 0) {
         int* sum = cluster.map_shared_rank(sh.hist, 0) + bin;
@@ -356,24 +359,16 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
 
   // ---- numbers of ties, holes and movers ----
   // what is before this block of the cluster, of two counts; their sums over the cluster in all
-  auto before_block = [&](int2 mine, int2& all) {
+  auto before_block = [&](int which, int2 mine, int2& all) {
     all = mine;
     if (C == 1) return make_int2(0, 0);
-    if (tid == 0) sh.total = mine;
+    if (tid == 0) sh.total[which] = mine;
     cluster.sync();
-    int2 at = make_int2(0, 0);
-    all = at;
-    for (int r = 0; r < C; ++r) {
-      const int2 x = *cluster.map_shared_rank(&sh.total, r);
-      if (r < rank) {
-        at.x += x.x;
-        at.y += x.y;
-      }
-      all.x += x.x;
-      all.y += x.y;
-    }
-    cluster.sync();                                   // (the next count takes its place)
-    return at;
+    // (a block's counts a lane: one after another the 128K prompt took 59 us, not 57.5)
+    const int2 x = lane < C ? *cluster.map_shared_rank(&sh.total[which], lane) : make_int2(0, 0);
+    const bool before = lane < rank;
+    all = make_int2(__reduce_add_sync(kFull, x.x), __reduce_add_sync(kFull, x.y));
+    return make_int2(__reduce_add_sync(kFull, before ? x.x : 0), __reduce_add_sync(kFull, before ? x.y : 0));
   };
   // Counts f(slot of the n, key) -> (first, second) over the block's chunk by 32 slots, and turns the counts
   // into what is before each 32 within the chunk; the chunk's sums
@@ -408,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
       load(c0, c1);
       mine.x += count(c0, c1, tie).x;
     }
-    int at = before_block(mine, all).x;
+    int at = before_block(0, mine, all).x;
     if (tid == 0) sh.digit = INT_MAX;
     __syncthreads();
     for (int c0 = lo; c0 < hi; c0 += p.keys) {
@@ -427,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     // (blocks before the cut's keep all of theirs, blocks behind it none)
     const int here = cut != INT_MAX;
     int2 found;
-    const int2 past = before_block(make_int2(here, 0), found);
+    const int2 past = before_block(1, make_int2(here, 0), found);
     if (!here) cut = past.x ? lo : INT_MAX;
   }
   auto stays = [&](int i, uint32_t k) { return k > T || (k == T && i < cut); };
@@ -443,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     mine.x += sum.x;
     mine.y += sum.y;
   }
-  int2 at = before_block(mine, all);
+  int2 at = before_block(2, mine, all);
   const int moves = all.y;
   int64_t* to = p.lists + int64_t(unit) * 2 * p.list_len;
   int64_t* from = to + p.list_len;
@@ -519,35 +514,39 @@ int launch_evict(EvictParams p, cudaStream_t stream) {
   const int units = p.batch * p.n_kv_heads;
   const int64_t slots = int64_t(p.max_pages) * p.page_size;
   static LaunchOnce once;
-  static std::atomic<int> largest{8};                 // blocks a cluster
+  static std::atomic<int> fit[kMostCluster + 1];      // clusters of so many blocks that run at once, a block an SM
   constexpr int kMost = int(sizeof(Shared)) + (kMaxKeys + 4) * 4;
-  static_assert(kMost <= int(kMaxSmemBlock), "shared memory of a block");
+  static_assert(kMost <= int(kMaxSmemBlock) && kMost > int(kMaxSmemBlock) / 2, "shared memory of a block");
   if (!once.run([] {
         if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
             cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
           return false;
-        // sixteen blocks a cluster are more than every device has to offer
-        cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(16);
-        lc.blockDim = dim3(kThreads);
-        lc.dynamicSmemBytes = kMost;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 16;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        lc.attrs = attr;
-        lc.numAttrs = 1;
-        int n = 0;
-        const bool asked = cudaOccupancyMaxActiveClusters(&n, evict_kernel, &lc) == cudaSuccess;
-        largest = asked && n > 0 ? 16 : 8;
-        if (!asked) cudaGetLastError();               // (a refusal is an answer)
+        for (int c = 1; c <= kMostCluster; ++c) {
+          cudaLaunchConfig_t lc = {};
+          lc.gridDim = dim3(c);
+          lc.blockDim = dim3(kThreads);
+          lc.dynamicSmemBytes = kMost;
+          cudaLaunchAttribute attr[1];
+          attr[0].id = cudaLaunchAttributeClusterDimension;
+          attr[0].val.clusterDim.x = c;
+          attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+          lc.attrs = attr;
+          lc.numAttrs = 1;
+          int n = 0;
+          const bool asked = cudaOccupancyMaxActiveClusters(&n, evict_kernel, &lc) == cudaSuccess;
+          if (!asked) cudaGetLastError();             // (a refusal is an answer)
+          fit[c] = asked ? n : 0;
+        }
         return true;
       }))
     return LOCKS_ERR_CUDA;
-  const int most = largest;
-  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.
+  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.  Where
+  // one block an SM is all there is, as many as have an SM each: two clusters in one part of the chip while
+  // others are idle (16 blocks a head of eight) took 57 us where 12 blocks take 53.6.
   int C = 1;
-  while (C < most && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
+  while (2 * C <= kMostCluster && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
+  if (units * C <= kBatchSms)
+    while (C > 1 && fit[C] < units) --C;
   const int64_t share = (slots + C - 1) / C;
   p.keys = int(share < kMaxKeys ? (share + 31) / 32 * 32 : kMaxKeys);
   cudaLaunchConfig_t lc = {};

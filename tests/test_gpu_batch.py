@@ -364,6 +364,7 @@ EVICT = [
     ([40000], 2, 16, 39995, 500, [6], 0, 0),
     ([30001], 1, 64, 15000, 500, None, 1, 0),
     ([700000], 1, 16, 5000, 100, [3], 50, 0),                  # chunks of the keys
+    ([30000], 8, 16, 4000, 300, [5], 0, 0),                    # eight heads on one large cluster each
 ]
 
 
