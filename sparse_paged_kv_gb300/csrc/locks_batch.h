@@ -31,6 +31,7 @@ struct PrefixParams {
                                  // [blocks][256] pieces continued from the block before
   float4* sums;                  // [parts][2 halves of the columns] (m, l, l of the rounded weights, -)
   int4* entry_info;              // [n_groups + batch + 1] of each entry of the list: see join_kernel
+  int32_t* longest;              // [blocks][n_groups] of many groups: see Groups
   int batch, n_groups, n_rows, n_kv_heads, group, max_pages, num_blocks, page_size, page_shift;
   int tile_tokens;               // query tokens of a tile: floor(128 / group)
   uint64_t tile_magic;           // ceil(2^32 / (2 tile_tokens)): n / (2 tile_tokens) = n * magic >> 32 below 2^24
@@ -39,10 +40,10 @@ struct PrefixParams {
 };
 
 struct PrefixLayout {
-  size_t acc, sums, entry_info, total;
+  size_t acc, sums, entry_info, longest, total;
   int64_t parts;
 };
-PrefixLayout prefix_layout(int64_t rows, int64_t entries);
+PrefixLayout prefix_layout(int64_t rows, int64_t batch, int64_t groups);
 int launch_prefix(const PrefixParams& p, const CUtensorMap& q_group, const CUtensorMap& q_own,
                   const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
 

@@ -123,8 +123,7 @@ extern "C" {
 
 size_t locks_prefix_workspace_bytes(const locks_cfg_t* cfg, int32_t n_groups, int32_t n_rows) {
   if (check_prefix(cfg, n_groups, n_rows) != LOCKS_OK) return 0;
-  return locks::prefix_layout(int64_t(cfg->batch) * n_rows * cfg->n_q_heads,
-                              int64_t(n_groups) + cfg->batch).total;
+  return locks::prefix_layout(int64_t(cfg->batch) * n_rows * cfg->n_q_heads, cfg->batch, n_groups).total;
 }
 
 int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const void* k_cache,
@@ -143,7 +142,7 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
     return LOCKS_ERR_INVALID_ARG;
   locks::PrefixParams p;
   p.rows = int64_t(cfg->batch) * n_rows * cfg->n_q_heads;
-  const locks::PrefixLayout L = locks::prefix_layout(p.rows, int64_t(n_groups) + cfg->batch);
+  const locks::PrefixLayout L = locks::prefix_layout(p.rows, cfg->batch, n_groups);
   if (workspace_bytes < L.total) return LOCKS_ERR_WORKSPACE;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
@@ -157,6 +156,7 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
   p.parts = L.parts;
   p.sums = reinterpret_cast<float4*>(ws + L.sums);
   p.entry_info = reinterpret_cast<int4*>(ws + L.entry_info);
+  p.longest = reinterpret_cast<int32_t*>(ws + L.longest);
   p.batch = cfg->batch;
   p.n_groups = n_groups;
   p.n_rows = n_rows;

@@ -10,7 +10,8 @@
 // whole group, 256 rows (query token, head of the KV head's group) at a time.
 //
 // Work is a list of stages of 128 tokens: first every (group, KV head, 256 rows)
-// over the group's pages, then every (sequence, KV head) over its own.  152
+// over the group's pages, as far as the longest of its sequences sees them, then
+// every (sequence, KV head) over its own.  152
 // blocks, one per SM, take equal shares of the list, so that any mix of lengths
 // fills the chip; a unit cut by a share's border leaves a piece in either block.
 // A block's warps are: one that loads (tensor maps, a ring of five 32 KB
@@ -92,7 +93,7 @@ struct Shared {
   int lock;                                           // of the tensor cores, between the groups
   int flag[2][2][4][2];                               // what a softmax warp tells its partner
   int dead;                                           // a wait ran out: every role leaves
-  int group_start[kGroupsHeld + 1], group_pages[kGroupsHeld];
+  int group_start[kGroupsHeld + 1], group_pages[kGroupsHeld], group_longest[kGroupsHeld];
   int bad[8];                                         // pages of a stage whose block is invalid, by stage & 7
   ListPlace place;
 };
@@ -102,9 +103,12 @@ static_assert(kSmemBytes <= kMaxSmemBlock, "shared memory of a block");
 // ---- the list of work -----------------------------------------------------------
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-// bounds and pages of the groups, held in shared memory or (many of them) as given
+// bounds and pages of the groups, held in shared memory or (many of them) as given, and the length of each
+// group's longest sequence, there or in this block's part of the workspace
 struct Groups {
   const int32_t *start, *pages;
+  int32_t* longest;       // INT_MAX: some sequence sees the whole prefix; 0: none found so far
+  bool bounded;           // prefixes end at the longest sequence (else all are seen whole)
   bool ascending;         // else no group counts (two could claim a sequence, and the list outgrow an int)
   __device__ __forceinline__ int start_of(const PrefixParams& p, int g) const {
     return clamp_int(start[g], 0, p.batch);
@@ -133,6 +137,7 @@ struct Entry {
   int stages, tokens, row, page0;   // tokens; the block table's row and its first page
   int q0, nq, tiles;                // first query token (of all), how many, in how many units a head
   int cost, last_cost;              // of a unit; of a head's last one
+  int group;                        // of a sequence that sees its whole prefix, else -1
   __device__ __forceinline__ int head_cost() const { return (tiles - 1) * cost + last_cost; }
 };
 // how many of a unit's stages begin before `cost` of it
@@ -146,6 +151,9 @@ __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) 
   if (e < p.n_groups) {
     const int a = groups.start_of(p, e), seqs = max(0, groups.start_of(p, e + 1) - a);
     n.tokens = groups.pages_of(p, e) * p.page_size;
+    // (what no row of the group sees is neither read nor multiplied: it may hold anything)
+    if (groups.bounded) n.tokens = min(n.tokens, groups.longest[e]);
+    n.group = -1;
     n.row = a;
     n.page0 = 0;
     n.q0 = a * p.n_rows;
@@ -155,6 +163,7 @@ __device__ Entry load_entry(const PrefixParams& p, const Groups& groups, int e) 
     const int b = e - p.n_groups, len = length_of(p, b), g = groups.of(p, b);
     n.page0 = g >= 0 ? groups.pages_of(p, g) : 0;
     n.tokens = max(0, len - n.page0 * p.page_size);
+    n.group = len < n.page0 * p.page_size ? -1 : g;
     n.row = b;
     n.q0 = b * p.n_rows;
     n.nq = p.n_rows;
@@ -596,13 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // what follows reads memory that the kernel before this one may write
   griddep_wait();
-  Groups groups = {p.group_starts, p.prefix_pages, true};
-  if (tid < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + tid));
   const bool held = p.n_groups <= kGroupsHeld;
+  Groups groups = {p.group_starts, p.prefix_pages,
+                   held ? sh.group_longest : p.longest + int64_t(blockIdx.x) * p.n_groups, false, true};
+  if (tid < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + tid));
   bool out_of_order = false;
   for (int i = tid; i < p.n_groups; i += kThreads) {
     const int a = p.group_starts[i], z = p.group_starts[i + 1];
     out_of_order |= a < 0 || z < a || z > p.batch;
+    groups.longest[i] = 0;
     if (held) {
       sh.group_start[i] = a;
       sh.group_pages[i] = p.prefix_pages[i];
@@ -616,26 +627,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   groups.ascending = !__syncthreads_or(out_of_order);
   tc_fence_before();
   const int entries = p.n_groups + p.batch;
-  int total;
-  const int share = locate<kThreads>(
-      [&](int e) {
-        return load_entry(p, groups, e).head_cost() * p.n_kv_heads;
-      },
-      entries, blockIdx.x, kCostStage, kBatchSms, sh.place, total,
-      [&](int e, int first) {
-        if (blockIdx.x) return;
-        // for the kernel that joins the pieces; and the arguments' check
-        const Entry n = load_entry(p, groups, e);
-        if (e >= p.n_groups) {
-          const int t = p.seq_lens[e - p.n_groups];
-          p.entry_info[e] = make_int4(first, n.stages, groups.of(p, e - p.n_groups), 0);
-          if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
-        } else {
-          p.entry_info[e] = make_int4(first, n.stages, n.q0, n.nq);
-          if (!groups.ascending || groups.pages[e] < 0 || groups.pages[e] > p.max_pages)
-            flag_status(p.status, LOCKS_DEV_BAD_GROUP);
-        }
-      });
+  int total, share;
+  for (;;) {
+    bool unseen = false;
+    share = locate<kThreads>(
+        [&](int e) {
+          const Entry n = load_entry(p, groups, e);
+          if (n.group >= 0) groups.longest[n.group] = INT_MAX;
+          return n.head_cost() * p.n_kv_heads;
+        },
+        entries, blockIdx.x, kCostStage, kBatchSms, sh.place, total,
+        [&](int e, int first) {
+          // (called once every thread's entries have been asked for their stages)
+          if (e < p.n_groups && groups.longest[e] == 0) unseen |= load_entry(p, groups, e).tokens > 0;
+          if (blockIdx.x) return;
+          // for the kernel that joins the pieces; and the arguments' check
+          const Entry n = load_entry(p, groups, e);
+          if (e >= p.n_groups) {
+            const int t = p.seq_lens[e - p.n_groups];
+            p.entry_info[e] = make_int4(first, n.stages, groups.of(p, e - p.n_groups), 0);
+            if (t < 0 || t > p.max_pages * p.page_size) flag_status(p.status, LOCKS_DEV_BAD_SEQ_LEN);
+          } else {
+            p.entry_info[e] = make_int4(first, n.stages, n.q0, n.nq);
+            if (!groups.ascending || groups.pages[e] < 0 || groups.pages[e] > p.max_pages)
+              flag_status(p.status, LOCKS_DEV_BAD_GROUP);
+          }
+        });
+    if (groups.bounded || !__syncthreads_or(unseen)) break;
+    // Some prefix is seen whole by none of its sequences (only then is this worth 0.3 us): the longest of
+    // each group, a sequence a thread, and the list once more.  A warp in one group adds one number.
+    groups.bounded = true;
+    for (int b0 = tid & ~31; b0 < p.batch; b0 += kThreads) {
+      const int b = b0 + (tid & 31), g = b < p.batch ? groups.of(p, b) : -1;
+      const int len = g >= 0 ? length_of(p, b) : 0;
+      if (__all_sync(kFull, g == __shfl_sync(kFull, g, 0))) {
+        const int most = __reduce_max_sync(kFull, len);
+        if (g >= 0 && (tid & 31) == 0) atomicMax(groups.longest + g, most);
+      } else if (g >= 0) {
+        atomicMax(groups.longest + g, len);
+      }
+    }
+    __syncthreads();
+  }
   if (blockIdx.x == 0 && tid == 0) p.entry_info[entries] = make_int4(total, 0, 0, 0);
   tc_fence_after();
   griddep_launch();
@@ -831,7 +864,7 @@ int launch_join(const PrefixParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
+PrefixLayout prefix_layout(int64_t rows, int64_t batch, int64_t groups) {
   PrefixLayout L;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t parts = size_t(4) * rows + size_t(kBatchSms) * 256;
@@ -839,7 +872,8 @@ PrefixLayout prefix_layout(int64_t rows, int64_t entries) {
   L.acc = 0;
   L.sums = up(L.acc + parts * kHeadDim * sizeof(float));
   L.entry_info = up(L.sums + 2 * parts * sizeof(float4));
-  L.total = up(L.entry_info + size_t(entries + 1) * sizeof(int4));
+  L.longest = up(L.entry_info + size_t(groups + batch + 1) * sizeof(int4));
+  L.total = L.longest + (groups > kGroupsHeld ? up(size_t(kBatchSms) * groups * sizeof(int32_t)) : 0);
   return L;
 }
 

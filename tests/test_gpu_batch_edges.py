@@ -1,0 +1,42 @@
+"""The operators of a batch that shares prefixes and lives within a budget, on the GPU, where their inputs
+are unusual: prefixes that nobody sees whole, rows without weight, recent tokens, many long heads, other streams."""
+import numpy as np
+import pytest
+
+from tests import batch_ref as R
+from tests.test_gpu_batch import Batch, _lib  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+INSIDE = [
+    # lens, hq, hkv, page, starts, prefix pages, rows
+    ([40, 30], 8, 2, 32, [0, 2], [2], 1),                       # in the last page of the prefix
+    ([100, 70], 4, 1, 64, [0, 2], [4], 1),                      # a stage before its end
+    ([300, 130, 5, 0], 6, 2, 64, [0, 4], [20], 1),              # many stages before it
+    ([0, 0, 50], 4, 1, 32, [0, 2], [3], 1),                     # nobody sees any of it
+    ([700, 690, 30, 20], 4, 1, 16, [0, 2, 4], [40, 4], 3),      # one group past its prefix, one within
+    ([200 - i for i in range(40)], 8, 1, 64, [0, 40], [9], 1),  # 320 rows: a pair of tiles and a lone one
+    ([90 - i % 50 for i in range(210)], 2, 1, 16, list(range(0, 211, 3)), [8] * 70, 1),   # many groups
+    ([150, 0, 20] * 25, 4, 1, 64, list(range(76)), [2, 1, 1] * 25, 2),                     # one sequence each
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,page,starts,prefix,rows", INSIDE)
+def test_prefix_that_nobody_sees_whole(lens, hq, hkv, page, starts, prefix, rows):
+    """Sequences end inside their group's prefix: what none of them sees may hold NaN and infinities, and its
+    pages may have no block yet."""
+    import torch
+    b = Batch(lens, hq, hkv, page, starts, prefix, rows, seed=len(lens))
+    used = torch.zeros(b.k.shape[:3], dtype=torch.bool)
+    for i, n in enumerate(lens):
+        t = np.arange(n)
+        used[b.table[i, t // page], :, t % page] = True
+    for pool in (b.k, b.v):
+        pool[~used.cuda()] = torch.tensor([float("nan"), float("inf")] * 64, device="cuda").bfloat16()
+    table = b.table.copy()
+    for a, z in zip(starts, starts[1:]):
+        for i in range(a, z):
+            table[i, -(-max(lens[a:z]) // page):] = -1
+    b.block_table = b.ints(table)
+    b.ws = torch.full_like(b.ws, 255)
+    b.attend().check()
