@@ -440,10 +440,13 @@ class BatchCache:
             self.positions = zeros(*pool, dtype=torch.int32)
             self.ws_evict = zeros(max(1, B.evict_workspace_bytes(cfg, self.budget)))
 
-    def next_positions(self):
+    _on = QuantCache._on
+
+    def next_positions(self, stream=None):
         """Position of each sequence's next token (int32 [batch] on the device): its cached tokens
         and the evicted ones."""
-        return self.seq_lens + self.evicted
+        with self._on(stream):
+            return self.seq_lens + self.evicted
 
     def append(self, k, v, stream=None):
         """One token per sequence, k, v bf16 [batch][H_kv][d], at its current length."""
@@ -454,15 +457,16 @@ class BatchCache:
         """(out, log-sum-exp) of q [batch][H_q][d], the newest token of each sequence, or
         [batch][rows][H_q][d], its newest `rows` tokens (appended since the last eviction, which
         moves rows); into self.out and self.out_lse for one row
-        (unless others are given), else into new tensors."""
+        (unless others are given), else into new tensors, allocated on the stream."""
         torch = self.torch
         if q.dim() == 4 and q.shape[1] > self.max_rows:
             raise ValueError(f"q: at most max_rows = {self.max_rows} rows a sequence expected, got {q.shape[1]}")
-        if out is None:
-            out = self.out if q.dim() == 3 else torch.empty_like(q)
-        if out_lse is None:
-            out_lse = self.out_lse if q.dim() == 3 else torch.empty(
-                q.shape[:-1], dtype=torch.float32, device=q.device)
+        with self._on(stream):
+            if out is None:
+                out = self.out if q.dim() == 3 else torch.empty_like(q)
+            if out_lse is None:
+                out_lse = self.out_lse if q.dim() == 3 else torch.empty(
+                    q.shape[:-1], dtype=torch.float32, device=q.device)
         B.locks_prefix_decode(self.cfg, q, self.k_cache, self.v_cache, self.block_table, self.seq_lens,
                               self.group_starts, self.prefix_pages, out, self.workspace,
                               out_lse=out_lse, status=self.status, stream=stream)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import batch_ref as R
-from tests.test_gpu_batch import Batch, _lib  # noqa: F401
+from tests.test_gpu_batch import Batch, _lib, cache  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,32 @@ def test_prefix_that_nobody_sees_whole(lens, hq, hkv, page, starts, prefix, rows
     b.block_table = b.ints(table)
     b.ws = torch.full_like(b.ws, 255)
     b.attend().check()
+
+
+def test_observe_on_another_stream():
+    """observe() and steps on a busy side stream, their results dropped while the current stream takes memory
+    and writes it: the bits of the same run on one stream."""
+    import torch
+    runs = []
+    for side in (None, torch.cuda.Stream()):
+        c, gen = cache([200, 130, 64], 4, 60, 8, seed=3)
+        q = torch.randn(3, 4, 8, 128, generator=gen).bfloat16().cuda()
+        rows = [[torch.randn(3, h, 128, generator=gen).bfloat16().cuda() for h in (8, 2, 2)] for _ in range(5)]
+        drafted = torch.randn(3, 2, 8, 128, generator=gen).bfloat16().cuda()
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big = torch.ones(8192, 8192, device="cuda", dtype=torch.bfloat16)
+                for _ in range(20):
+                    big @ big
+        c.observe(q, stream=side)
+        taken = [torch.full_like(q, float("nan")), torch.full(q.shape[:-1], -1e30, device="cuda")]
+        for r in rows:
+            c.step(*r, stream=side)
+        out, lse = c.attend(drafted, stream=side)
+        taken += [torch.full_like(drafted, float("nan")), torch.full(drafted.shape[:-1], -1e30, device="cuda")]
+        nxt = c.next_positions(stream=side)
+        torch.cuda.synchronize()
+        runs.append([out, lse, nxt, c.out, c.k_cache, c.v_cache, c.weights, c.positions, c.seq_lens, c.evicted, c.status])
+        del taken
+    assert all(torch.equal(a, b) for a, b in zip(*runs))

@@ -1,0 +1,66 @@
+"""runtime.BatchCache on the host: what it allocates where, and what it refuses (no GPU)."""
+import contextlib
+import types
+
+import numpy as np
+import pytest
+
+from sparse_paged_kv_gb300 import binding as B
+from sparse_paged_kv_gb300 import build_lib, runtime
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    B.load_library(build_lib.build())
+
+
+def cache(batch=2, max_pages=4, prefix=2, **kw):
+    """A cache in host memory, `prefix` pages shared by all of its sequences."""
+    table = np.arange(batch * max_pages).reshape(batch, max_pages)
+    table[:, :prefix] = table[0, :prefix]
+    cfg = B.LocksConfig(batch=batch, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=64, rank=8, max_pages=max_pages,
+                        num_blocks=batch * max_pages)
+    return runtime.BatchCache(cfg, table, [0, batch], [prefix], device="cpu", **kw)
+
+
+class Recorder:
+    """torch for one cache: notes the stream on which each allocation is made."""
+
+    def __init__(self, torch):
+        self.torch, self.current, self.made = torch, None, []
+        self.cuda = types.SimpleNamespace(stream=self._stream, ExternalStream=lambda x: ("external", x),
+                                          default_stream=lambda: "default")
+
+    @contextlib.contextmanager
+    def _stream(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+    def _note(self, make, *a, **kw):
+        self.made.append(self.current)
+        return make(*a, **kw)
+
+    def empty(self, *a, **kw):
+        return self._note(self.torch.empty, *a, **kw)
+
+    def empty_like(self, *a, **kw):
+        return self._note(self.torch.empty_like, *a, **kw)
+
+    def __getattr__(self, name):
+        return getattr(self.torch, name)
+
+
+@pytest.mark.parametrize("stream,on", [(None, None), ("side", "side"), (7, ("external", 7)), (0, "default")])
+def test_results_are_allocated_on_the_stream_of_the_call(monkeypatch, stream, on):
+    import torch
+    calls = []
+    for name in ("locks_prefix_decode", "locks_weigh", "locks_evict"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **kw: calls.append((_n, kw["stream"])))
+    c = cache(budget_tokens=64, recent_tokens=8, max_rows=4)
+    c.torch = rec = Recorder(torch)
+    c.observe(torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16), stream=stream)
+    assert rec.made == [on, on]
+    assert calls == [(n, stream) for n in ("locks_prefix_decode", "locks_weigh", "locks_evict")]
+    c.attend(torch.zeros(2, 8, 128, dtype=torch.bfloat16), stream=stream)
+    assert rec.made == [on, on]                       # (one row: the cache's own buffers)
