@@ -377,7 +377,8 @@ class BatchCache:
     common (host integers; None: nothing is shared); block_table names a group's pages in each of
     its rows.  `fixed` is how many first tokens of each sequence are never weighed nor evicted: its
     prefix by default, and at least that.  `max_rows` is the most query rows a sequence in a call
-    (drafted tokens, the last tokens of a prompt).  Without budget_tokens nothing is weighed.
+    (drafted tokens, the last tokens of a prompt).  Without budget_tokens nothing is weighed; with it
+    a sequence's pages hold more than its fixed tokens and the budget.
 
     Keys are cached as they are given, rotated: the token that a step appends stands at
     next_positions().  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
@@ -412,6 +413,12 @@ class BatchCache:
         self.budget, self.recent, self.decay = int(budget_tokens), int(recent_tokens), float(decay)
         if self.budget < 0 or not 0 <= self.recent <= self.budget:
             raise ValueError("budget_tokens >= 0 and recent_tokens of 0 to budget_tokens expected")
+        # a step evicts once it has appended; without room for that token a sequence would fill up and
+        # stay full, its further tokens refused
+        room = cfg.max_pages * cfg.page_size - int(held.max(initial=0))
+        if self.budget and self.budget >= room:
+            raise ValueError(f"budget_tokens: fewer than the {room} tokens of a sequence's pages behind its fixed "
+                             f"ones expected, got {self.budget}")
         size = B.prefix_workspace_bytes(cfg, 0 if pages is None else pages.size, max_rows)
         if size == 0 and cfg.batch:
             raise B.LocksError("locks_prefix_workspace_bytes", B.LOCKS_ERR_UNSUPPORTED, "unsupported cfg")

@@ -69,3 +69,23 @@ def test_observe_on_another_stream():
         runs.append([out, lse, nxt, c.out, c.k_cache, c.v_cache, c.weights, c.positions, c.seq_lens, c.evicted, c.status])
         del taken
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_steps_with_room_for_one_token():
+    """A budget that leaves one slot of a sequence's pages: every step appends, evicts one and goes on."""
+    import torch
+    c, gen = cache([384, 100, 383], 4, 319, 8, seed=5)          # 384 slots: 64 of a prefix, 319 and one
+    c.observe(torch.randn(3, 4, 8, 128, generator=gen).bfloat16().cuda())
+    nxt = c.next_positions().tolist()
+    assert nxt == [384, 100, 383]
+    for step in range(1, 301):
+        c.step(*(torch.randn(3, h, 128, generator=gen).bfloat16().cuda() for h in (8, 2, 2)))
+        if step in (1, 2, 283, 284, 300):
+            assert c.next_positions().tolist() == [n + step for n in nxt]
+            assert c.seq_lens.tolist() == [383, min(383, 100 + step), 383]
+            for b in range(3):                                  # what is held: the newest 8, nothing twice
+                n = int(c.seq_lens[b])
+                for h in range(2):
+                    pos = R.slots(c.positions.cpu().numpy(), c.block_table.cpu().numpy()[b], h, n)[64:]
+                    assert np.unique(pos).size == pos.size and (np.sort(pos)[-8:] == nxt[b] + step - 8 + np.arange(8)).all()
+    assert c.status.item() == 0

@@ -64,3 +64,11 @@ def test_results_are_allocated_on_the_stream_of_the_call(monkeypatch, stream, on
     assert calls == [(n, stream) for n in ("locks_prefix_decode", "locks_weigh", "locks_evict")]
     c.attend(torch.zeros(2, 8, 128, dtype=torch.bfloat16), stream=stream)
     assert rec.made == [on, on]                       # (one row: the cache's own buffers)
+
+
+def test_a_budget_leaves_room_for_a_token():
+    for kw in (dict(budget_tokens=128), dict(budget_tokens=200), dict(budget_tokens=64, fixed=[128, 192])):
+        with pytest.raises(ValueError, match="budget_tokens"):
+            cache(**kw)                               # 256 slots a sequence, 128 of them its prefix
+    for kw in (dict(budget_tokens=127), dict(budget_tokens=63, fixed=[128, 192]), dict(fixed=[128, 256])):
+        cache(**kw)
