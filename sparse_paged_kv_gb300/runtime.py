@@ -484,10 +484,12 @@ class BatchCache:
         ones; the last n_new tokens, or with `fresh` all of them, had none."""
         if not self.budget:
             raise ValueError("a BatchCache made without budget_tokens weighs nothing")
-        B.locks_weigh(self.cfg, q, lse, self.k_cache, self.block_table, self.seq_lens,
-                      None if fresh else self.weights, self.weights, n_new=n_new, decay=self.decay,
-                      fixed=self.fixed, positions=self.positions, evicted=self.evicted,
-                      status=self.status, stream=stream)
+        self._weigh(q, lse, self.seq_lens, None if fresh else self.weights, n_new, stream)
+
+    def _weigh(self, q, lse, lens, weights, n_new, stream):
+        B.locks_weigh(self.cfg, q, lse, self.k_cache, self.block_table, lens, weights, self.weights,
+                      n_new=n_new, decay=self.decay, fixed=self.fixed, positions=self.positions,
+                      evicted=self.evicted, status=self.status, stream=stream)
 
     def evict(self, stream=None):
         """Cut every sequence to its budget."""
@@ -497,12 +499,25 @@ class BatchCache:
                       self.block_table, self.seq_lens, self.weights, self.positions, self.evicted,
                       self.ws_evict, fixed=self.fixed, status=self.status, stream=stream)
 
-    def observe(self, q, stream=None):
-        """The end of a prompt that stands in the cache: attention of its last rows, q
-        [batch][rows][H_q][d]; with a budget they weigh every token, and the least are evicted."""
+    def observe(self, q, stream=None, sequences=None):
+        """The end of prompts that stand in the cache: attention of the last rows of every sequence, q
+        [batch][rows][H_q][d]; with a budget they weigh every token, and the least are evicted.
+
+        Weighing numbers the tokens of a sequence by their slots, so it is for one whose slots are in
+        order: those of `sequences` (a bool for each, on the host or the device; a sequence that joins a
+        running batch is observed alone), by default all that have lost no token.  The others keep their
+        weights and positions.  A program that gives a row of the batch to another sequence sets its
+        entries of seq_lens and evicted."""
+        torch = self.torch
+        if sequences is not None and len(sequences) != self.cfg.batch:
+            raise ValueError(f"sequences: {self.cfg.batch} bools expected, got {len(sequences)}")
         out, lse = self.attend(q, stream=stream)
         if self.budget:
-            self.weigh(q, lse, n_new=0, fresh=True, stream=stream)
+            with self._on(stream):
+                chosen = self.evicted == 0 if sequences is None else torch.as_tensor(
+                    sequences, dtype=torch.bool, device=self.device)
+                lens = torch.where(chosen, self.seq_lens, 0)
+            self._weigh(q, lse, lens, None, 0, stream)
             self.evict(stream=stream)
         return out, lse
 

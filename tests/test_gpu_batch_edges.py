@@ -89,3 +89,75 @@ def test_steps_with_room_for_one_token():
                     pos = R.slots(c.positions.cpu().numpy(), c.block_table.cpu().numpy()[b], h, n)[64:]
                     assert np.unique(pos).size == pos.size and (np.sort(pos)[-8:] == nxt[b] + step - 8 + np.arange(8)).all()
     assert c.status.item() == 0
+
+
+def _running():
+    """A batch of which sequences 0 and 3 have lost tokens, and queries for its newest rows."""
+    import torch
+    c, gen = cache([200, 100, 80, 150], 4, 60, 8, seed=9)
+    c.observe(torch.randn(4, 4, 8, 128, generator=gen).bfloat16().cuda())
+    for _ in range(6):
+        c.step(*(torch.randn(4, h, 128, generator=gen).bfloat16().cuda() for h in (8, 2, 2)))
+    assert c.evicted.tolist() == [82, 0, 0, 32]
+    return c, torch.randn(4, 4, 8, 128, generator=gen).bfloat16().cuda()
+
+
+def _held(c, b):
+    import torch
+    n, page = int(c.seq_lens[b]), c.cfg.page_size
+    at = torch.arange(n, device="cuda")
+    blk = c.block_table[b].long()[at // page]
+    return [x[blk, :, at % page].clone() for x in (c.k_cache, c.v_cache, c.weights, c.positions)]
+
+
+def test_observe_keeps_the_order_of_sequences_that_lost_tokens():
+    import torch
+    c, q = _running()
+    before = [_held(c, b) for b in range(4)]
+    c.observe(q)
+    for b in (0, 3):
+        assert all(torch.equal(x, y) for x, y in zip(_held(c, b), before[b]))
+    for b, n in ((1, 106), (2, 86)):
+        now = _held(c, b)
+        assert (now[3][64:] == torch.arange(64, n, device="cuda")[:, None]).all()
+        # four rows of four heads hand out one each, and what was gathered before is gone
+        assert (now[2][64:].sum(0) <= 16 * (1 + 1e-5)).all() and not torch.equal(now[2][64:], before[b][2][64:])
+    assert c.evicted.tolist() == [82, 0, 0, 32] and c.status.item() == 0
+
+
+@pytest.mark.parametrize("on_device", [False, True])
+def test_a_sequence_that_joins_is_observed_alone(on_device):
+    """Its tokens as in a batch of its own; those of the others as they were."""
+    import torch
+    c, q = _running()
+    gen = torch.Generator().manual_seed(1)
+    n, page = 170, c.cfg.page_size
+    at = torch.arange(64, n, device="cuda")
+    blk = c.block_table[3].long()[at // page]
+    for pool in (c.k_cache, c.v_cache):
+        pool[blk, :, at % page] = torch.randn(n - 64, 2, 128, generator=gen).bfloat16().cuda()
+    c.seq_lens[3], c.evicted[3] = n, 0
+    whole = [x[c.block_table[3].long()[torch.arange(n, device="cuda") // page], :, torch.arange(n, device="cuda") % page].double()
+             .cpu().numpy() for x in (c.k_cache, c.v_cache)]
+    before = [_held(c, b) for b in range(3)]
+    joins = torch.tensor([0, 0, 0, 1], device="cuda").bool() if on_device else [False, False, False, True]
+    lse = c.observe(q, sequences=joins)[1]
+    for b in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(_held(c, b), before[b]))
+    assert c.seq_lens.tolist() == [124, 106, 86, 124] and c.evicted.tolist() == [82, 0, 0, 46]
+    k, v, w, pos = (x.cpu() for x in _held(c, 3))
+    for h in range(2):
+        a = slice(4 * h, 4 * h + 4)
+        want, bound = R.weigh(q[3, :, a].double().cpu().numpy(), lse[3, :, a].double().cpu().numpy(), whole[0][:, h], n, 64,
+                              None, 0, 1.0)
+        t = pos[64:, h].numpy()
+        assert np.unique(t).size == 60 and t.min() >= 64 and (np.sort(t)[-8:] == np.arange(n - 8, n)).all()
+        assert (np.abs(w[64:, h].double().numpy() - want[t - 64]) <= bound[t - 64]).all()
+        for x, y in ((k, whole[0]), (v, whole[1])):
+            assert (x[64:, h].double().numpy() == y[t, h]).all()
+        lost = np.setdiff1d(np.arange(64, n - 8), t)
+        kept = np.setdiff1d(t, np.arange(n - 8, n))
+        assert want[lost - 64].max() <= want[kept - 64].min() + 2 * bound.max()
+    with pytest.raises(ValueError):
+        c.observe(q, sequences=[True])
+    assert c.status.item() == 0

@@ -72,3 +72,9 @@ def test_a_budget_leaves_room_for_a_token():
             cache(**kw)                               # 256 slots a sequence, 128 of them its prefix
     for kw in (dict(budget_tokens=127), dict(budget_tokens=63, fixed=[128, 192]), dict(fixed=[128, 256])):
         cache(**kw)
+
+
+def test_a_bool_for_each_sequence_is_expected():
+    import torch
+    with pytest.raises(ValueError, match="sequences"):
+        cache(budget_tokens=64).observe(torch.zeros(2, 8, 128, dtype=torch.bfloat16), sequences=[True])
