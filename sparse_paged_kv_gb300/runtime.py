@@ -381,7 +381,8 @@ class BatchCache:
     a sequence's pages hold more than its fixed tokens and the budget.
 
     Keys are cached as they are given, rotated: the token that a step appends stands at
-    next_positions().  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
+    next_positions().  Until observe() has weighed a prompt, its tokens have weight 0 and stand
+    where the block table first put them.  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
     1, 2, 4 or 8 query heads a KV head)."""
 
     def __init__(self, cfg: B.LocksConfig, block_table, group_starts=None, prefix_pages=None,
@@ -444,7 +445,12 @@ class BatchCache:
         self.weights = self.positions = None
         if self.budget:
             self.weights = zeros(*pool, dtype=torch.float32)
-            self.positions = zeros(*pool, dtype=torch.int32)
+            # every token stands where its slot is until eviction moves it
+            stands = np.zeros((cfg.num_blocks, cfg.page_size), np.int32)
+            named = (table >= 0) & (table < cfg.num_blocks)
+            stands[table[named]] = np.arange(cfg.max_pages * cfg.page_size, dtype=np.int32).reshape(
+                1, cfg.max_pages, -1).repeat(cfg.batch, 0)[named]
+            self.positions = ints(stands)[:, None].repeat(1, cfg.n_kv_heads, 1)
             self.ws_evict = zeros(max(1, B.evict_workspace_bytes(cfg, self.budget)))
 
     _on = QuantCache._on

@@ -161,3 +161,18 @@ def test_a_sequence_that_joins_is_observed_alone(on_device):
     with pytest.raises(ValueError):
         c.observe(q, sequences=[True])
     assert c.status.item() == 0
+
+
+def test_steps_of_a_prompt_that_was_not_observed():
+    """Its newest tokens count as recent all the same."""
+    import torch
+    c, gen = cache([200, 160, 90], 4, 60, 40, seed=11)
+    for step in range(1, 4):
+        c.step(*(torch.randn(3, h, 128, generator=gen).bfloat16().cuda() for h in (8, 2, 2)))
+        assert c.next_positions().tolist() == [200 + step, 160 + step, 90 + step]
+        for b, n in enumerate((200, 160, 90)):
+            pos = _held(c, b)[3][64:].sort(0).values
+            for h in range(2):
+                assert pos[:, h].unique().numel() == pos.shape[0] == min(60, n + step - 64)
+                held = min(pos.shape[0], 40)
+                assert pos[-held:, h].tolist() == list(range(n + step - held, n + step))

@@ -78,3 +78,14 @@ def test_a_bool_for_each_sequence_is_expected():
     import torch
     with pytest.raises(ValueError, match="sequences"):
         cache(budget_tokens=64).observe(torch.zeros(2, 8, 128, dtype=torch.bfloat16), sequences=[True])
+
+
+def test_positions_before_anything_is_observed():
+    c = cache(budget_tokens=64)
+    table = c.block_table.numpy()
+    for b in range(2):
+        assert (c.positions.numpy()[table[b]] == np.arange(256).reshape(4, 1, 64)).all()
+    assert c.positions.shape == (8, 2, 64) and c.positions.is_contiguous()
+    cfg = B.LocksConfig(batch=1, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=64, rank=8, max_pages=3, num_blocks=4)
+    c = runtime.BatchCache(cfg, [[3, -1, 9]], budget_tokens=64, device="cpu")         # pages without a block yet
+    assert (c.positions.numpy()[3] == np.arange(64)).all() and (c.positions.numpy()[:3] == 0).all()
