@@ -599,7 +599,8 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
  * counts as 0, and their entry of `positions` becomes slot + evicted[b].
  *
  *   q             bf16 [batch][n_rows][n_q_heads][d], 16-byte aligned
- *   lse           float [batch][n_rows][n_q_heads]; -inf: the row adds nothing
+ *   lse           float [batch][n_rows][n_q_heads]; infinite: the row adds
+ *                 nothing, whatever its query holds
  *   k_cache       the K pool, 16-byte aligned
  *   fixed         nullable int32 [batch], >= 0 (NULL: 0)
  *   weights       nullable float pool (NULL: every slot is new)
@@ -609,7 +610,7 @@ int locks_prefix_decode(const locks_cfg_t* cfg, const void* q, int32_t n_rows, c
  *   decay         >= 0, 1 to accumulate
  *   positions     nullable int32 pool
  *   evicted       nullable int32 [batch]: tokens that locks_evict took so far
- * All of it in float32.  A key that is not finite gives its slot a NaN.  Slots of
+ * All of it in float32.  A key that is not finite may give its slot a NaN.  Slots of
  * a block id outside the pool are left out (LOCKS_DEV_BAD_BLOCK_ID).
  */
 int locks_weigh(const locks_cfg_t* cfg, const void* q, int32_t n_rows, const float* lse,

@@ -40,6 +40,7 @@ struct Shared {
   uint32_t tmem;
   int dead;
   ListPlace place;
+  int off[2][8];                                      // a row of the warp's part has no weight; units in turn
   alignas(16) float minus_lse[2][256];                // of the unit, times log2 e; units in turn
 };
 
@@ -199,10 +200,12 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
   int stage = 0, units = 0;
   while (walk.next(p, u)) {
     // This unit's log-sum-exps, a part a warp.  (A row that sees nothing has -inf, and gives no weight: as
-    // the columns behind the rows, whose queries are zeros, it gets the factor 2^-inf.)
+    // the columns behind the rows, whose queries are zeros, it gets the factor 2^-inf.  Its own query may
+    // hold anything, NaN included, so a unit that has such a row takes the loop that looks at each.)
     // A warp that gets here has finished the unit before, so once all have arrived for
     // unit n, nobody reads the buffer of unit n - 1, which unit n + 1 takes.
     float* minus = sh.minus_lse[units & 1];
+    bool off = false;
     for (int c = threadIdx.x; c < p.n_cols; c += 256) {
       const int r = c / p.group;
       float x = -INFINITY;
@@ -210,10 +213,16 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
         x = p.lse[(int64_t(u.b) * p.n_rows + r) * (p.n_kv_heads * p.group) + u.head * p.group +
                   c - r * p.group];
       minus[c] = x == -INFINITY ? -INFINITY : -x * kLog2e;
+      off |= c < rows && minus[c] == -INFINITY;
     }
+    off = __any_sync(kFull, off);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.lse_full);
+    if (lane == 0) {
+      sh.off[units & 1][threadIdx.x >> 5] = off;
+      mbar_arrive(&sh.lse_full);
+    }
     if (!warp_wait_or_dead(&sh.lse_full, units & 1, &sh.dead)) return;
+    off = __any_sync(kFull, sh.off[units & 1][lane & 7]);
     ++units;
     const int32_t* table = p.block_table + int64_t(u.b) * p.max_pages;
     for (int s = u.s0; s < u.s1; ++s, ++stage) {
@@ -236,7 +245,7 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
       const int c0 = max(0, slot - (u.len - p.n_rows)) * p.group;
       const float2 scale = make_float2(p.scale_log2, p.scale_log2);
       float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-      if (__any_sync(kFull, there && c0 > 0)) {
+      if (off || __any_sync(kFull, there && c0 > 0)) {
         for (int c = 0; c < p.n_cols; c += 16) {
           float x[16];
           tmem_ld16(d + c, x);
@@ -244,7 +253,7 @@ __device__ void weigh_role(const WeighParams& p, Shared& sh, int w, int share) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float y = ex2_approx(fmaf(x[k], p.scale_log2, minus[c + k]));
-            if (c + k >= c0) a0.x += y;
+            if (c + k >= c0 && minus[c + k] != -INFINITY) a0.x += y;
           }
         }
       } else {

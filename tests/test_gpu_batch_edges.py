@@ -176,3 +176,31 @@ def test_steps_of_a_prompt_that_was_not_observed():
                 assert pos[:, h].unique().numel() == pos.shape[0] == min(60, n + step - 64)
                 held = min(pos.shape[0], 40)
                 assert pos[-held:, h].tolist() == list(range(n + step - held, n + step))
+
+
+@pytest.mark.parametrize("hq,hkv,rows", [(4, 1, 4), (8, 2, 2), (16, 1, 16)])
+def test_weigh_rows_that_are_off_may_hold_anything(hq, hkv, rows):
+    """Query rows whose log-sum-exp is -inf, NaN and infinities in them: no weight.  A row that counts and
+    holds a NaN gives one to what it sees."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    lens, g = [200, 1, 0, 150], hq // hkv
+    b = Batch(lens, hq, hkv, 32, rows=rows, seed=rows).attend()
+    q = b.q.double().cpu().numpy()
+    b.lse[0, rows - 1, 1], b.lse[0, 0] = -float("inf"), -float("inf")       # (the one token of sequence 1 has the last row)
+    b.q[0, rows - 1, 1], b.q[0, 0], b.q[1, :rows - 1] = float("nan"), float("inf"), -float("inf")
+    out = torch.zeros(b.cfg.num_blocks, hkv, 32, device="cuda")
+    B.locks_weigh(b.cfg, b.q, b.lse, b.k, b.block_table, b.seq_lens, None, out, status=b.status)
+    got, lse = out.double().cpu().numpy(), b.lse.double().cpu().numpy()
+    for i, n in enumerate(lens):
+        for h in range(hkv):
+            a = slice(h * g, h * g + g)
+            want, bound = R.weigh(q[i, :, a], lse[i, :, a], b.rows_of(i, h)[0], n, 0, None, 0, 1.0)
+            assert (np.abs(R.slots(got, b.table[i], h, n) - want) <= bound).all(), (i, h)
+    b.q[3, rows - 1, g - 1, 5] = float("nan")
+    B.locks_weigh(b.cfg, b.q, b.lse, b.k, b.block_table, b.seq_lens, None, out, status=b.status)
+    now = out.double().cpu().numpy()
+    assert np.isnan(R.slots(now, b.table[3], 0, 150)).all()
+    for i, h in [(i, h) for i in range(4) for h in range(hkv) if (i, h) != (3, 0)]:
+        assert (R.slots(now, b.table[i], h, lens[i]) == R.slots(got, b.table[i], h, lens[i])).all()
+    assert b.status.item() == 0
