@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kMostCluster = 16;
+constexpr int kMostCluster = kEvictMostBlocks;
 constexpr int kMaxKeys = 40 * 1024;                   // kept in shared memory by a block
 constexpr int kAhead = 2, kMoveAhead = 4;             // loads ahead: four slots of a thread, rows of a warp
 // Up to so many slots to evict are found one after another, as least keys (a decode step evicts as many
@@ -540,13 +540,7 @@ int launch_evict(EvictParams p, cudaStream_t stream) {
         return true;
       }))
     return LOCKS_ERR_CUDA;
-  // Blocks a head: as many as fill the SMs with two each, while each still has a thousand slots.  Where
-  // one block an SM is all there is, as many as have an SM each: two clusters in one part of the chip while
-  // others are idle (16 blocks a head of eight) took 57 us where 12 blocks take 53.6.
-  int C = 1;
-  while (2 * C <= kMostCluster && units * C <= kBatchSms && slots / (2 * C) >= 1024) C *= 2;
-  if (units * C <= kBatchSms)
-    while (C > 1 && fit[C] < units) --C;
+  const int C = evict_blocks(units, slots, fit);
   const int64_t share = (slots + C - 1) / C;
   p.keys = int(share < kMaxKeys ? (share + 31) / 32 * 32 : kMaxKeys);
   cudaLaunchConfig_t lc = {};

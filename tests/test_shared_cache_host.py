@@ -1,5 +1,9 @@
-"""runtime.BatchCache on the host: what it allocates where, and what it refuses (no GPU)."""
+"""runtime.BatchCache on the host: what it allocates where, and what it refuses; the cluster that eviction
+launches (no GPU)."""
 import contextlib
+import os
+import shutil
+import subprocess
 import types
 
 import numpy as np
@@ -89,3 +93,47 @@ def test_positions_before_anything_is_observed():
     cfg = B.LocksConfig(batch=1, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=64, rank=8, max_pages=3, num_blocks=4)
     c = runtime.BatchCache(cfg, [[3, -1, 9]], budget_tokens=64, device="cpu")         # pages without a block yet
     assert (c.positions.numpy()[3] == np.arange(64)).all() and (c.positions.numpy()[:3] == 0).all()
+
+
+RULE = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "locks_batch.h"
+// units, slots and what fits, for 1 to 16 blocks -> the blocks of a cluster
+int main(int, char** a) {
+  int fit[17] = {0};
+  for (int c = 1; c <= 16; ++c) fit[c] = std::atoi(a[2 + c]);
+  std::printf("%d", locks::evict_blocks(std::atoi(a[1]), std::atoll(a[2]), fit));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rule(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("needs a C++ compiler")
+    at = tmp_path_factory.mktemp("rule")
+    (at / "rule.cpp").write_text(RULE)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build_lib.nvcc()))), "include")
+    subprocess.run([cxx, "-std=c++17", "-I" + build_lib.CSRC, "-I" + cuda, "-o", str(at / "rule"), str(at / "rule.cpp")],
+                   check=True)
+
+    def run(units, slots, fit):
+        return int(subprocess.run([str(at / "rule"), str(units), str(slots), *map(str, fit)], check=True,
+                                  capture_output=True, text=True).stdout)
+    return run
+
+
+def test_eviction_launches_clusters_that_the_device_takes(rule):
+    whole = [152 // c for c in range(1, 17)]
+    small = [n if c <= 8 else 0 for c, n in enumerate(whole, 1)]      # clusters above 8 blocks are refused
+    for slots in (100, 2047, 2048, 5000, 40000, 1 << 20):
+        for units in (1, 2, 7, 8, 9, 10, 15, 19, 20, 38, 76, 77, 152, 153, 400):
+            for fit in (whole, small):
+                c = rule(units, slots, fit)
+                assert c == 1 or (fit[c - 1] > 0 and slots // c >= 1024), (units, slots, c)
+                assert units * c > 152 or c == 1 or fit[c - 1] >= units
+    assert rule(10, 1 << 16, whole) == 16 and rule(10, 1 << 16, small) == 8
+    assert rule(8, 1 << 17, [152 // c if c < 13 else 6 for c in range(1, 17)]) == 12
+    assert rule(200, 1 << 17, whole) == 1 and rule(3, 2047, whole) == 1
