@@ -204,3 +204,95 @@ def test_weigh_rows_that_are_off_may_hold_anything(hq, hkv, rows):
     for i, h in [(i, h) for i in range(4) for h in range(hkv) if (i, h) != (3, 0)]:
         assert (R.slots(now, b.table[i], h, lens[i]) == R.slots(got, b.table[i], h, lens[i])).all()
     assert b.status.item() == 0
+
+
+# --------------------------------------------------------------------------
+# eviction whose recent tokens lie among many others
+# --------------------------------------------------------------------------
+RECENT = [
+    # lens, hkv, page, budget, recent, fixed
+    ([5000, 4990], 1, 64, 1000, 300, 3),                        # a block a head
+    ([40000], 2, 16, 3000, 500, 7),                             # clusters
+    ([40000], 2, 16, 39995, 500, 6),                            # none to evict
+    ([40000, 39998], 2, 16, 39990, 500, 6),                     # a few
+    ([30001], 1, 64, 15000, 15000, 0),                          # nothing but recent ones
+    ([700000], 1, 16, 5000, 100, 3),                            # chunks of the keys
+    ([30000], 8, 16, 4000, 300, 5),                             # eight heads on one large cluster each
+    ([33000, 32900], 8, 64, 2000, 100, 4),                      # sixteen heads of two blocks an SM
+]
+
+
+def run_evict(lens, hkv, page, budget, recent, fixed, w, pos, gone):
+    """One call on heads whose n slots have weights and positions w, pos [sequence][head][n], against the plain form."""
+    import torch
+    from sparse_paged_kv_gb300 import binding as B
+    batch, pages = len(lens), max(-(-n // page) for n in lens)
+    rng = np.random.default_rng(batch + budget)
+    blocks = batch * pages + 2
+    table = rng.permutation(blocks)[:batch * pages].reshape(batch, pages).astype(np.int32)
+    pools = [np.full((blocks, hkv, page), 123.0, np.float32), np.full((blocks, hkv, page), -5, np.int32)]
+    gen = torch.Generator(device="cuda").manual_seed(budget)
+    kv = [torch.randn(blocks, hkv, page, 128, generator=gen, device="cuda").bfloat16() for _ in "kv"]
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        for h in range(hkv):
+            for pool, x in zip(pools, (w, pos)):
+                pool[table[b, t // page], h, t % page] = x[b][h]
+    want, want_kv = [x.copy() for x in pools], [x.clone() for x in kv]
+    for b, n in enumerate(lens):
+        for h in range(hkv):
+            holes, movers = R.evict(w[b][h], pos[b][h], n, fixed, gone, budget, recent)
+            for pool, old in zip(want, pools):
+                pool[table[b, holes // page], h, holes % page] = old[table[b, movers // page], h, movers % page]
+            src, dst = ([torch.from_numpy(x.astype(np.int64)).cuda() for x in (table[b, y // page], y % page)]
+                        for y in (movers, holes))
+            for pool, old in zip(want_kv, kv):
+                pool[dst[0], h, dst[1]] = old[src[0], h, src[1]]
+    cfg = B.LocksConfig(batch=batch, n_q_heads=hkv, n_kv_heads=hkv, head_dim=128, page_size=page, rank=8,
+                        max_pages=pages, num_blocks=blocks)
+    dev = [torch.from_numpy(x).cuda() for x in pools]
+    seq_lens, evicted, status = Batch.ints(lens), Batch.ints([gone] * batch), Batch.ints([0])
+    ws = torch.zeros(B.evict_workspace_bytes(cfg, budget), dtype=torch.uint8, device="cuda")
+    B.locks_evict(cfg, budget, recent, *kv, Batch.ints(table), seq_lens, *dev, evicted, ws, fixed=Batch.ints([fixed] * batch),
+                  status=status)
+    after = [min(n, fixed + budget) for n in lens]
+    assert seq_lens.tolist() == after and status.item() == 0
+    assert evicted.tolist() == [gone + n - m for n, m in zip(lens, after)]
+    for got, x in zip(dev, want):
+        assert (got.cpu().numpy().view(np.int32) == x.view(np.int32)).all()
+    for got, x in zip(kv, want_kv):
+        assert torch.equal(got.view(torch.int16), x.view(torch.int16))
+
+
+@pytest.mark.parametrize("lens,hkv,page,budget,recent,fixed", RECENT)
+@pytest.mark.parametrize("distinct", [0, 5])
+def test_evict_recent_tokens_of_long_heads(lens, hkv, page, budget, recent, fixed, distinct):
+    """The newest positions lie anywhere and stay, the lightest of all among them."""
+    rng = np.random.default_rng(budget + recent)
+    gone, w, pos = 777, [], []
+    for n in lens:
+        w.append(rng.random((hkv, n), np.float32))
+        if distinct:
+            w[-1] = np.floor(w[-1] * distinct)
+        pos.append(np.empty((hkv, n), np.int32))
+        for h in range(hkv):
+            held = rng.choice(n + gone - recent - fixed, n - fixed - recent, replace=False) + fixed
+            held = np.concatenate([held, np.arange(n + gone - recent, n + gone)])
+            pos[-1][h, :fixed], pos[-1][h, fixed:] = np.arange(fixed), rng.permutation(held)
+            newest = pos[-1][h] >= n + gone - recent
+            assert newest.sum() == recent > 0
+            light = newest & (rng.random(n) < 0.5)
+            assert light.any()
+            w[-1][h, light] = -1.0                              # below every other: only their positions keep them
+    run_evict(lens, hkv, page, budget, recent, fixed, w, pos, gone)
+
+
+@pytest.mark.parametrize("lens,budget", [([40000], 3000), ([300], 40), ([700000], 5000)])
+def test_evict_more_recent_tokens_than_the_budget(lens, budget):
+    """Positions that occur twice: of equal ones the lower slots stay."""
+    rng = np.random.default_rng(budget)
+    w = [rng.random((1, n), np.float32) for n in lens]
+    pos = [rng.integers(n - budget, n, (1, n)).astype(np.int32) for n in lens]
+    pos[0][0, ::3] = 0
+    assert (pos[0] >= lens[0] - budget).sum() > budget
+    run_evict(lens, 1, 16, budget, budget, 2, w, pos, 0)
