@@ -571,7 +571,7 @@ def locks_prefix_decode(cfg: LocksConfig, q, k_cache, v_cache, block_table, seq_
     wsb = workspace_bytes if workspace_bytes is not None else workspace.nbytes
     row = (cfg.head_dim,)
     rc = load_library().locks_prefix_decode(
-        cfg.ref, _sized(q, "bfloat16", shape, "q"), rows,
+        cfg.ref, _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
         _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", row),
         _pages(v_cache, cfg, "bfloat16", "v_cache", row),
         _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),
@@ -594,7 +594,7 @@ def locks_weigh(cfg: LocksConfig, q, lse, k_cache, block_table, seq_lens, weight
     if q.dim() == 4:
         shape = (cfg.batch, rows, cfg.n_q_heads, cfg.head_dim)
     rc = load_library().locks_weigh(
-        cfg.ref, _sized(q, "bfloat16", shape, "q"), rows,
+        cfg.ref, _sized(_here(q, "q"), "bfloat16", shape, "q"), rows,
         _sized(lse, "float32", shape[:-1], "lse"),
         _pages(_here(k_cache, "k_cache"), cfg, "bfloat16", "k_cache", (cfg.head_dim,)),
         _sized(block_table, "int32", (cfg.batch, cfg.max_pages), "block_table"),

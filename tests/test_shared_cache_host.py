@@ -137,3 +137,37 @@ def test_eviction_launches_clusters_that_the_device_takes(rule):
     assert rule(10, 1 << 16, whole) == 16 and rule(10, 1 << 16, small) == 8
     assert rule(8, 1 << 17, [152 // c if c < 13 else 6 for c in range(1, 17)]) == 12
     assert rule(200, 1 << 17, whole) == 1 and rule(3, 2047, whole) == 1
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The queries and the pools of a call lie on the current device."""
+    import torch
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    c = B.LocksConfig(batch=2, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=64, rank=8, max_pages=4, num_blocks=8)
+
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, device, dtype, *shape):
+            self.device, self.dtype, self.shape = device, dtype, torch.Size(shape)
+            self.nbytes = 1 << 30
+
+        def __getattr__(self, name):
+            return {"dim": lambda: len(self.shape), "get_device": lambda: self.device, "is_contiguous": lambda: True,
+                    "data_ptr": lambda: 0x10000}[name]
+
+    def call(fn, q=0, k=0):
+        qs, pool = Tensor(q, torch.bfloat16, 2, 8, 128), Tensor(k, torch.bfloat16, 8, 2, 64, 128)
+        ints, table = Tensor(0, torch.int32, 2), Tensor(0, torch.int32, 2, 4)
+        rec, ws = Tensor(0, torch.float32, 8, 2, 64), Tensor(0, torch.uint8, 1 << 30)
+        if fn is B.locks_prefix_decode:
+            fn(c, qs, pool, pool, table, ints, None, None, qs, ws)
+        elif fn is B.locks_weigh:
+            fn(c, qs, Tensor(0, torch.float32, 2, 8), pool, table, ints, None, rec)
+        else:
+            fn(c, 64, 0, pool, pool, table, ints, rec, Tensor(0, torch.int32, 8, 2, 64), ints, ws)
+
+    for fn, where in ((B.locks_prefix_decode, "q"), (B.locks_prefix_decode, "k"), (B.locks_weigh, "q"),
+                      (B.locks_weigh, "k"), (B.locks_evict, "k")):
+        with pytest.raises(ValueError, match="current device"):
+            call(fn, **{where: 1})
