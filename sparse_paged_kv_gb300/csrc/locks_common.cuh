@@ -171,7 +171,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------
-// packed fp32 FMA (two lanes of fp32 per instruction on sm_100+)
+// packed fp32 arithmetic (two lanes of fp32 per instruction on sm_100+)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   unsigned long long ra, rb, rc, rd;
@@ -179,6 +179,14 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   rb = *reinterpret_cast<unsigned long long*>(&b);
   rc = *reinterpret_cast<unsigned long long*>(&c);
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
+  return *reinterpret_cast<float2*>(&rd);
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  ra = *reinterpret_cast<unsigned long long*>(&a);
+  rb = *reinterpret_cast<unsigned long long*>(&b);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
   return *reinterpret_cast<float2*>(&rd);
 }
 

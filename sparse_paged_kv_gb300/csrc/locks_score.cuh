@@ -154,13 +154,6 @@ __device__ __forceinline__ void load_qfrag(QFrag& f, const __nv_bfloat16* qh, in
                         __uint_as_float(raw[s][h] & 0xffff0000u) * down);
 }
 
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long ra, rb, rd;
-  ra = *reinterpret_cast<unsigned long long*>(&a);
-  rb = *reinterpret_cast<unsigned long long*>(&b);
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
-  return *reinterpret_cast<float2*>(&rd);
-}
 __device__ __forceinline__ float2 shfl_xor2(float2 v, int o) {
   return make_float2(__shfl_xor_sync(kFull, v.x, o), __shfl_xor_sync(kFull, v.y, o));
 }

@@ -177,15 +177,6 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// packed float addition
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long rd;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(rd)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&rd);
-}
-
 // ---- waits ------------------------------------------------------------------------
 // Wait for phase `parity` of `bar`.  False, and *dead set, if the limit ran out or another
 // thread of the block gave up: every role then leaves its loop.
