@@ -382,7 +382,9 @@ class BatchCache:
 
     Keys are cached as they are given, rotated: the token that a step appends stands at
     next_positions().  Until observe() has weighed a prompt, its tokens have weight 0 and stand
-    where the block table first put them.  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
+    where the block table first put them.  append() writes at a sequence's length, and what one that
+    ends inside its prefix appends there is its whole group's: the empty rows of a padded batch belong
+    outside the groups.  append() and step() have the limits of locks_append_kv (pages of 64 or 16,
     1, 2, 4 or 8 query heads a KV head)."""
 
     def __init__(self, cfg: B.LocksConfig, block_table, group_starts=None, prefix_pages=None,
@@ -415,8 +417,9 @@ class BatchCache:
         if self.budget < 0 or not 0 <= self.recent <= self.budget:
             raise ValueError("budget_tokens >= 0 and recent_tokens of 0 to budget_tokens expected")
         # a step evicts once it has appended; without room for that token a sequence would fill up and
-        # stay full, its further tokens refused
-        room = cfg.max_pages * cfg.page_size - int(held.max(initial=0))
+        # stay full, its further tokens refused (one whose every token is fixed is never cut)
+        room = cfg.max_pages * cfg.page_size - held
+        room = int(room[room > 0].min(initial=cfg.max_pages * cfg.page_size))
         if self.budget and self.budget >= room:
             raise ValueError(f"budget_tokens: fewer than the {room} tokens of a sequence's pages behind its fixed "
                              f"ones expected, got {self.budget}")
@@ -487,7 +490,8 @@ class BatchCache:
 
     def weigh(self, q, lse, n_new: int, fresh: bool = False, stream=None):
         """Add the weight that q's rows (with their log-sum-exps) give every token behind the fixed
-        ones; the last n_new tokens, or with `fresh` all of them, had none."""
+        ones; the last n_new tokens, or with `fresh` all of them, had none and are numbered by their
+        slots (so `fresh` is for sequences that have lost no token)."""
         if not self.budget:
             raise ValueError("a BatchCache made without budget_tokens weighs nothing")
         self._weigh(q, lse, self.seq_lens, None if fresh else self.weights, n_new, stream)

@@ -74,8 +74,9 @@ def test_a_budget_leaves_room_for_a_token():
     for kw in (dict(budget_tokens=128), dict(budget_tokens=200), dict(budget_tokens=64, fixed=[128, 192])):
         with pytest.raises(ValueError, match="budget_tokens"):
             cache(**kw)                               # 256 slots a sequence, 128 of them its prefix
-    for kw in (dict(budget_tokens=127), dict(budget_tokens=63, fixed=[128, 192]), dict(fixed=[128, 256])):
-        cache(**kw)
+    for kw in (dict(budget_tokens=127), dict(budget_tokens=63, fixed=[128, 192]), dict(fixed=[128, 256]),
+               dict(budget_tokens=127, fixed=[128, 256]), dict(budget_tokens=127, fixed=[1 << 30, 128])):
+        cache(**kw)                                   # (a sequence that is fixed whole is never cut)
 
 
 def test_a_bool_for_each_sequence_is_expected():
