@@ -19,7 +19,8 @@
 // mover its number.  The lists of pool rows go through the workspace, and all warps of the
 // cluster move rows, 16 bytes a lane: lanes 0-15 the key, 16-31 the value.
 // Bound: long prompts by the chain of phases and then the moves' traffic (four 32K prompts cut to 4096
-// tokens: 25 us, and 16 for 117 MB read and written at 7.3 TB/s), a decode step by latency (8 us).
+// tokens, on the device: 44 us, of which 16 for 117 MB read and written at 7.3 TB/s; one of 128K to 8192:
+// 46), a decode step by latency (7 us).
 #include <atomic>
 #include <climits>
 
@@ -40,7 +41,7 @@ constexpr int kMostCluster = kEvictMostBlocks;
 constexpr int kMaxKeys = 40 * 1024;                   // kept in shared memory by a block
 constexpr int kAhead = 2, kMoveAhead = 4;             // loads ahead: four slots of a thread, rows of a warp
 // Up to so many slots to evict are found one after another, as least keys (a decode step evicts as many
-// as it added: 4097 slots in 8 us, by digits 28 us).
+// as it added: 4097 slots in 7 to 8 us on the device, by digits 28).
 constexpr int kFew = 8;
 constexpr uint32_t kKeyRecent = 0xFFFFFFFFu, kKeyNaN = 0xFFFFFFFEu;
 

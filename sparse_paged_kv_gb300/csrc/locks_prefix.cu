@@ -27,8 +27,8 @@
 // a new maximum only where a row's maximum grew by more than 2^8, so rarely.
 // A second kernel joins the pieces of each row.
 //
-// 64 sequences behind a 32K prompt (32 heads on 8, 202 MB): 62 us, 3.2 TB/s with everything, memory
-// busy at 4 TB/s while stages run; 256 samples of a 16K prompt (64 heads on 8, 138 GFLOP): 160 us, 866
+// 64 sequences behind a 32K prompt (32 heads on 8, 202 MB): 63 us, 3.2 TB/s with everything, memory
+// busy at 4 TB/s while stages run; 256 samples of a 16K prompt (64 heads on 8, 138 GFLOP): 158 us, 875
 // TFLOP/s.  A stage's chain (S, softmax, P V) bounds both, the tensor cores half busy; few rows are
 // bound by memory but for the 4 us before the first key and as many behind the last.
 //

@@ -15,7 +15,7 @@
 // groups of four take stages in turn, thread = token, each with an accumulator
 // of its own in tensor memory.  Weights and block ids of a stage are loaded
 // before the wait for its product.  A step of 32 sequences of 4224 tokens (248 MB) takes 44 us, 5.65
-// TB/s; the last 32 tokens of four 32K prompts (128 rows, 241 MB) 45.6 us, 5.3 TB/s.
+// TB/s; the last 32 tokens of four 32K prompts (128 rows, 241 MB) 45.8 us, 5.25 TB/s.
 #include "locks_batch.h"
 #include "locks_batch.cuh"
 #include "locks_kv.cuh"
